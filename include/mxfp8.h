@@ -62,8 +62,9 @@ typedef enum mxfp8_status {
   MXFP8_ERR_CUDA = 4,             /* a CUDA runtime/driver call failed */
   MXFP8_ERR_BAD_OFFSETS = 5,      /* (device) expert offsets not 0-based, non-decreasing,
                                      32-aligned and ending at total_rows */
-  MXFP8_ERR_TIMEOUT = 6           /* (device) a pipeline wait in a kernel ran out; the
+  MXFP8_ERR_TIMEOUT = 6,          /* (device) a pipeline wait in a kernel ran out; the
                                      kernel abandoned its work */
+  MXFP8_ERR_BAD_TARGET = 7        /* (device) a target token at or past the vocabulary */
 } mxfp8_status;
 
 typedef enum mxfp8_axis {
@@ -219,6 +220,45 @@ int mxfp8_quantize_blockwise(const void* src_dev, int64_t rows, int64_t cols, vo
                              float* scale_inv_dev, int scale_type, void* stream);
 
 /*
+ * FP8 block-wise quantization with 1 x 128 blocks along one axis of a BF16 matrix: the
+ * activations and gradients of the block-wise recipe, as mxfp8_blockwise_gemm reads them.
+ * The scale and code rule is that of mxfp8_quantize_blockwise, with amax over the 128 (at
+ * the edge: fewer) values of a block.
+ *   src_dev        BF16 [rows][cols], 16-byte aligned
+ *   axis ROW       blocks along the columns; cols % 16 == 0. out_dev E4M3 [rows][cols],
+ *                  scale_inv_dev float [ceil(cols/128)][rows].
+ *   axis COL       blocks along the rows, emitted transposed; cols % 8 == 0, any number of
+ *                  rows. out_dev E4M3 [cols][pitch], pitch = rows rounded up to a multiple
+ *                  of 16, the codes past `rows` zero; scale_inv_dev float
+ *                  [ceil(rows/128)][cols].
+ * Scales lie block-major, so that a GEMM tile's scales of one block are contiguous.
+ * rows == 0 or cols == 0 is a no-op. Deterministic.
+ * Errors as for mxfp8_quantize_blockwise.
+ */
+int mxfp8_quantize_blockwise_1d(const void* src_dev, int64_t rows, int64_t cols, int axis,
+                                void* out_dev, float* scale_inv_dev, int scale_type,
+                                void* stream);
+
+/*
+ * mxfp8_quantize_blockwise_1d ROW and COL from one read of the input (cols % 16 == 0):
+ * what a learner needs of X and dY. Bytes equal those of the two separate calls.
+ */
+int mxfp8_quantize_blockwise_1d_dual(const void* src_dev, int64_t rows, int64_t cols,
+                                     void* row_out_dev, float* row_scale_inv_dev,
+                                     void* col_out_dev, float* col_scale_inv_dev,
+                                     int scale_type, void* stream);
+
+/*
+ * mxfp8_quantize_blockwise and the transpose of its result from one read (rows % 16 == 0,
+ * cols % 16 == 0): the weight as the forward and the data-gradient GEMM read it.
+ *   out_dev / scale_inv_dev      as mxfp8_quantize_blockwise writes them
+ *   out_t_dev / scale_inv_t_dev  E4M3 [cols][rows], float [ceil(cols/128)][ceil(rows/128)]
+ */
+int mxfp8_quantize_blockwise_dual(const void* src_dev, int64_t rows, int64_t cols,
+                                  void* out_dev, float* scale_inv_dev, void* out_t_dev,
+                                  float* scale_inv_t_dev, int scale_type, void* stream);
+
+/*
  * `batch` independent matrices [batch][rows][cols] quantized as by mxfp8_quantize, each
  * with its own scale block of mxfp8_scale_bytes(rows, cols, axis, layout) bytes; the
  * scale blocks are concatenated in batch order. Used for per-expert MoE weights.
@@ -323,6 +363,32 @@ int mxfp8_gemm_ws(const void* A_dev, const void* sA_dev, const void* B_dev, cons
 size_t mxfp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int op, int out_dtype);
 
 /*
+ * GEMM of block-wise FP8 operands (tcgen05 kind::f8f6f4, E4M3 x E4M3): C[M][N] =
+ * sum_k deq(A)[m][k] * deq(B)[n][k], both operands K-major. The product of each 128-deep
+ * block is accumulated by the tensor cores in FP32 and folded, times its two scales, into
+ * an FP32 sum in registers, so scales need not be powers of two.
+ *   A_dev / sA_dev  E4M3 [M][K] and float [ceil(K/128)][M], 1 x 128 blocks
+ *                   (mxfp8_quantize_blockwise_1d)
+ *   B_dev / sB_dev  FPROP, DGRAD: E4M3 [N][K] and float [ceil(N/128)][ceil(K/128)],
+ *                   128 x 128 blocks (mxfp8_quantize_blockwise, or the transposed copy of
+ *                   mxfp8_quantize_blockwise_dual for DGRAD);
+ *                   WGRAD: E4M3 [N][K] and float [ceil(K/128)][N], 1 x 128 blocks (K = the
+ *                   tokens, padded as the COL copies are)
+ *   C_dev           [M][N], BF16 or FP32, fully overwritten
+ * Requires K % 16 == 0 and N % 8 == 0; any M (WGRAD too). Accuracy: |C - C_exact| <=
+ * 2^-9 * sum_k |a_k b_k| per element before the output rounding. A NaN scale or code gives
+ * NaN in the elements it reaches. Deterministic.
+ * Empty sizes: M == 0 or N == 0 writes nothing, K == 0 zero-fills C (the operands may then
+ * be NULL).
+ * Errors: MXFP8_ERR_INVALID_ARG (negative or too large sizes, unknown enums, null
+ * pointers), MXFP8_ERR_ALIGNMENT (K % 16, N % 8, codes or C not 16-byte aligned, scales
+ * not 4-byte aligned); a pipeline wait that runs out latches MXFP8_ERR_TIMEOUT.
+ */
+int mxfp8_blockwise_gemm(const void* A_dev, const float* sA_dev, const void* B_dev,
+                         const float* sB_dev, void* C_dev, int64_t M, int64_t N, int64_t K,
+                         int op, int out_dtype, void* stream);
+
+/*
  * Grouped (MoE expert) block-scaled GEMMs over token segments off[e] .. off[e+1]
  * (expert_offsets_dev as for mxfp8_quantize_grouped).
  *   op FPROP / DGRAD:  A [total_rows][K] with grouped ROW scales (one block per expert,
@@ -400,6 +466,62 @@ int mxfp8_selfcheck_noalloc(const void* w_codes_dev, const void* w_scales_dev,
                             int64_t K, const void* x_bf16_dev, int64_t tokens,
                             float* rel_err_dev, void* stream);
 
+#define MXFP8_MAX_TOP 32
+
+/*
+ * Log probabilities of given tokens: for each row of logits x, with temperature T,
+ * m = max x and log_sum = log sum_v exp((x_v - m) / T),
+ *   logprob = (x_target - m) / T - log_sum,
+ *   entropy = -sum_v p_v log p_v,  p = softmax(x / T),
+ * and the `top` likeliest tokens. The pages measure the drift between sampler and learner by
+ * these log probabilities (section "A different grid, and drift").
+ *   logits_dev       BF16 or FP32 (logits_dtype: MXFP8_OUT_BF16 / MXFP8_OUT_FP32)
+ *                    [rows][ld], aligned to its element; the first `vocab` values of each
+ *                    row are read, ld >= vocab
+ *   targets_dev      int64 [rows]. A negative target is not scored: its logprob is 0. One
+ *                    at or past vocab gives NaN and latches MXFP8_ERR_BAD_TARGET.
+ *   logprob_dev      float [rows]
+ *   entropy_dev      float [rows]
+ *   stats_dev        float [rows][2]: m and log_sum, which the gradient call reads
+ *   top              0 .. MXFP8_MAX_TOP
+ *   top_logprob_dev  float [rows][top], falling; NULL if top == 0
+ *   top_id_dev       int64 [rows][top]; equal logits: the lowest token first. Where fewer
+ *                    than `top` logits are above -inf: -1, with log probability -inf.
+ * Masks: a logit of -inf has probability 0. A row whose logits are all -inf has log
+ * probability -inf (0 if not scored), entropy 0, stats (-inf, 0) and no top tokens. A row
+ * holding a NaN or +inf gives NaN (top_id -1).
+ * Sums are FP32. Deterministic. rows == 0 is a no-op.
+ * Errors: MXFP8_ERR_INVALID_ARG (negative sizes, vocab == 0 or above 2^31 - 1, ld < vocab,
+ * a temperature that is not positive or whose reciprocal is not a finite, normal float, top
+ * out of range, unknown dtype, null pointers), MXFP8_ERR_ALIGNMENT.
+ */
+int mxfp8_token_logprobs(const void* logits_dev, int logits_dtype, int64_t rows,
+                         int64_t vocab, int64_t ld, const int64_t* targets_dev,
+                         double temperature, float* logprob_dev, float* entropy_dev,
+                         float* stats_dev, int top, float* top_logprob_dev,
+                         int64_t* top_id_dev, void* stream);
+
+/*
+ * Gradient of the three results of mxfp8_token_logprobs with respect to the logits:
+ *   dx_v = (1/T) [ g 1(v = target) + sum_j gt_j 1(v = id_j)
+ *                  - p_v (g + sum_j gt_j + h (log p_v + entropy)) ]
+ *   targets_dev, stats_dev, entropy_dev, top_id_dev   as that call read or wrote them
+ *   grad_logprob_dev  g, float [rows] (not read where the target is negative: 0)
+ *   grad_entropy_dev  h, float [rows], or NULL for 0
+ *   grad_top_dev      gt, float [rows][top]; NULL, as top_id_dev, if top == 0. An id of -1
+ *                     is skipped, and its gt is not read.
+ *   grad_logits_dev   the logits' dtype, [rows][grad_ld], its first `vocab` columns
+ *                     written; may be the logits' own buffer (then grad_ld == ld)
+ * A row whose logits are all -inf gets zeros. Errors as above.
+ */
+int mxfp8_token_logprobs_backward(const void* logits_dev, int logits_dtype, int64_t rows,
+                                  int64_t vocab, int64_t ld, const int64_t* targets_dev,
+                                  double temperature, const float* stats_dev,
+                                  const float* entropy_dev, const float* grad_logprob_dev,
+                                  const float* grad_entropy_dev, int top,
+                                  const int64_t* top_id_dev, const float* grad_top_dev,
+                                  void* grad_logits_dev, int64_t grad_ld, void* stream);
+
 /*
  * Sets how long a GEMM kernel's pipeline waits (a stage's copies, the tensor cores, the
  * accumulator hand-over) may take before the kernel gives up, for every GEMM launched
@@ -417,8 +539,8 @@ int mxfp8_set_wait_limit_ns(uint64_t ns);
 /*
  * Synchronizes `stream`, then returns and clears the current device's status word:
  * MXFP8_OK, or the first device-side error latched since the last call
- * (MXFP8_ERR_BAD_OFFSETS, MXFP8_ERR_TIMEOUT), or MXFP8_ERR_CUDA if the synchronization
- * itself failed. The word is read and cleared in one atomic exchange, enqueued on
+ * (MXFP8_ERR_BAD_OFFSETS, MXFP8_ERR_TIMEOUT, MXFP8_ERR_BAD_TARGET), or MXFP8_ERR_CUDA if
+ * the synchronization itself failed. The word is read and cleared in one atomic exchange, enqueued on
  * `stream` after its earlier work. An error that a kernel on another stream latches
  * concurrently is reported by this call or by the next one; it is never cleared unread.
  */

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -22,12 +23,13 @@ RULE_FLOOR, RULE_CEIL = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
 
 OK, ERR_INVALID_ARG, ERR_ALIGNMENT, ERR_UNSUPPORTED_ARCH, ERR_CUDA, ERR_BAD_OFFSETS, \
-    ERR_TIMEOUT = range(7)
+    ERR_TIMEOUT, ERR_BAD_TARGET = range(8)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxfp8.so")
 
 # every symbol include/mxfp8.h declares: (name, restype, argtypes)
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_D = ctypes.c_double
 SIGNATURES = {
     "mxfp8_version": (_I, []),
     "mxfp8_status_string": (ctypes.c_char_p, [_I]),
@@ -39,6 +41,9 @@ SIGNATURES = {
     "mxfp8_quantize_dual_multi": (_I, [_P, _I, _I, _P]),
     "mxfp8_blockwise_scale_count": (_SZ, [_I64, _I64]),
     "mxfp8_quantize_blockwise": (_I, [_P, _I64, _I64, _P, _P, _I, _P]),
+    "mxfp8_quantize_blockwise_1d": (_I, [_P, _I64, _I64, _I, _P, _P, _I, _P]),
+    "mxfp8_quantize_blockwise_1d_dual": (_I, [_P, _I64, _I64, _P, _P, _P, _P, _I, _P]),
+    "mxfp8_quantize_blockwise_dual": (_I, [_P, _I64, _I64, _P, _P, _P, _P, _I, _P]),
     "mxfp8_quantize_batched": (_I, [_P, _I64, _I64, _I64, _I, _P, _P, _I, _P]),
     "mxfp8_quantize_grouped_dual": (_I, [_P, _I64, _I64, _P, _I, _P, _P, _P, _P, _P]),
     "mxfp8_quantize_grouped": (_I, [_P, _I64, _I64, _I, _P, _I, _P, _P, _P]),
@@ -46,6 +51,10 @@ SIGNATURES = {
     "mxfp8_gemm_ws": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P, _SZ, _P]),
     "mxfp8_gemm_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _I]),
     "mxfp8_grouped_gemm": (_I, [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I, _I, _P]),
+    "mxfp8_blockwise_gemm": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P]),
+    "mxfp8_token_logprobs": (_I, [_P, _I, _I64, _I64, _I64, _P, _D, _P, _P, _P, _I, _P, _P, _P]),
+    "mxfp8_token_logprobs_backward": (_I, [_P, _I, _I64, _I64, _I64, _P, _D, _P, _P, _P, _P, _I,
+                                           _P, _P, _P, _I64, _P]),
     "mxfp8_selfcheck_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "mxfp8_selfcheck": (_I, [_P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _SZ, _P, _P]),
     "mxfp8_selfcheck_noalloc": (_I, [_P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _P]),
@@ -115,6 +124,14 @@ def _buffer(t: torch.Tensor, dtype, numel: int, name: str):
     if t.numel() < numel:
         raise ValueError(f"{name} holds {t.numel()} elements; {numel} are needed")
     return t
+
+
+def _new(shape, dtype, device, stream):
+    """A result tensor whose memory belongs to the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 # ------------------------------------------------------------------------- quantizer
@@ -214,6 +231,87 @@ def quantize_blockwise(src: torch.Tensor, scale_type: int = BW_FP32, out=None, s
                                           scale_type, _stream(stream)),
            "mxfp8_quantize_blockwise")
     return out, scale_inv
+
+
+def _blockwise_1d_buffers(rows, cols, axis, dev, out, scale_inv, names, stream):
+    """Codes and scales of one 1 x 128 copy: given ones checked, absent ones allocated."""
+    if axis == ROW:
+        oshape, sshape = (rows, cols), ((cols + 127) // 128, rows)
+    else:
+        oshape, sshape = (cols, (rows + 15) // 16 * 16), ((rows + 127) // 128, cols)
+    if out is None:
+        out = _new(oshape, torch.uint8, dev, stream)
+    else:
+        _buffer(out, torch.uint8, oshape[0] * oshape[1], names[0])
+    if scale_inv is None:
+        scale_inv = _new(sshape, torch.float32, dev, stream)
+    else:
+        _buffer(scale_inv, torch.float32, sshape[0] * sshape[1], names[1])
+    return out, scale_inv
+
+
+def quantize_blockwise_1d(src: torch.Tensor, axis: int = ROW, scale_type: int = BW_FP32,
+                          out=None, scale_inv=None, stream=None):
+    """FP8 block-wise quantization with 1 x 128 blocks along one axis (activations and
+    gradients of blockwise_gemm). Returns (E4M3 codes as uint8, float32 scale_inv): ROW:
+    [rows, cols] and [ceil(cols/128), rows]; COL (transposed): [cols, rows rounded up to 16]
+    with zero codes past `rows`, and [ceil(rows/128), cols]."""
+    _require(src, torch.bfloat16, "src")
+    rows, cols = src.shape
+    if axis not in (ROW, COL):
+        raise ValueError(f"axis must be ROW or COL, got {axis}")
+    out, scale_inv = _blockwise_1d_buffers(rows, cols, axis, src.device, out, scale_inv,
+                                           ("out", "scale_inv"), stream)
+    _check(lib().mxfp8_quantize_blockwise_1d(_ptr(src), rows, cols, axis, _ptr(out),
+                                             _ptr(scale_inv), scale_type, _stream(stream)),
+           "mxfp8_quantize_blockwise_1d")
+    return out, scale_inv
+
+
+def quantize_blockwise_1d_dual(src: torch.Tensor, scale_type: int = BW_FP32, row_out=None,
+                               row_scale_inv=None, col_out=None, col_scale_inv=None,
+                               stream=None):
+    """quantize_blockwise_1d ROW and COL from one read. Returns (row_codes, row_scale_inv,
+    col_codes, col_scale_inv)."""
+    _require(src, torch.bfloat16, "src")
+    rows, cols = src.shape
+    row_out, row_scale_inv = _blockwise_1d_buffers(rows, cols, ROW, src.device, row_out,
+                                                   row_scale_inv, ("row_out", "row_scale_inv"),
+                                                   stream)
+    col_out, col_scale_inv = _blockwise_1d_buffers(rows, cols, COL, src.device, col_out,
+                                                   col_scale_inv, ("col_out", "col_scale_inv"),
+                                                   stream)
+    _check(lib().mxfp8_quantize_blockwise_1d_dual(_ptr(src), rows, cols, _ptr(row_out),
+                                                  _ptr(row_scale_inv), _ptr(col_out),
+                                                  _ptr(col_scale_inv), scale_type,
+                                                  _stream(stream)),
+           "mxfp8_quantize_blockwise_1d_dual")
+    return row_out, row_scale_inv, col_out, col_scale_inv
+
+
+def quantize_blockwise_dual(src: torch.Tensor, scale_type: int = BW_FP32, out=None,
+                            scale_inv=None, out_t=None, scale_inv_t=None, stream=None):
+    """quantize_blockwise and the transpose of its result from one read (rows and cols
+    multiples of 16): a weight for the forward and the data-gradient product. Returns (codes
+    [rows, cols], scale_inv, codes_t [cols, rows], scale_inv_t)."""
+    _require(src, torch.bfloat16, "src")
+    rows, cols = src.shape
+    rb, cb, dev = (rows + 127) // 128, (cols + 127) // 128, src.device
+    out = _new((rows, cols), torch.uint8, dev, stream) if out is None else out
+    out_t = _new((cols, rows), torch.uint8, dev, stream) if out_t is None else out_t
+    if scale_inv is None:
+        scale_inv = _new((rb, cb), torch.float32, dev, stream)
+    if scale_inv_t is None:
+        scale_inv_t = _new((cb, rb), torch.float32, dev, stream)
+    _buffer(out, torch.uint8, rows * cols, "out")
+    _buffer(out_t, torch.uint8, rows * cols, "out_t")
+    _buffer(scale_inv, torch.float32, rb * cb, "scale_inv")
+    _buffer(scale_inv_t, torch.float32, rb * cb, "scale_inv_t")
+    _check(lib().mxfp8_quantize_blockwise_dual(_ptr(src), rows, cols, _ptr(out),
+                                               _ptr(scale_inv), _ptr(out_t), _ptr(scale_inv_t),
+                                               scale_type, _stream(stream)),
+           "mxfp8_quantize_blockwise_dual")
+    return out, scale_inv, out_t, scale_inv_t
 
 
 class DualJob(ctypes.Structure):
@@ -392,6 +490,140 @@ def grouped_gemm(a, sa, b, sb, offsets: torch.Tensor, op: int = FPROP,
     _check(lib().mxfp8_grouped_gemm(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(out),
                                     _ptr(offsets), e, total, n_, k_, op, out_dtype,
                                     _stream(stream)), "mxfp8_grouped_gemm")
+    return out
+
+
+def blockwise_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
+                   op: int = FPROP, out_dtype: int = OUT_BF16, out=None,
+                   stream=None) -> torch.Tensor:
+    """C[M, N] = deq(A)[M, K] . deq(B)[N, K]^T of block-wise FP8 operands (both K-major). A
+    and sa as quantize_blockwise_1d writes them; B and sb as quantize_blockwise does (128 x
+    128 blocks), or for WGRAD as quantize_blockwise_1d does. K % 16 == 0, N % 8 == 0."""
+    _require(a, torch.uint8, "A")
+    _require(b, torch.uint8, "B")
+    m, k = a.shape
+    n, k2 = b.shape
+    if k != k2:
+        raise ValueError(f"K mismatch: {k} vs {k2}")
+    dt = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
+    if out is None:
+        out = _new((m, n), dt, a.device, stream)
+    else:
+        _buffer(out, dt, m * n, "out")
+    kb = (k + 127) // 128
+    if m and n and k:  # the scales are read only when there is a reduction to run
+        _buffer(sa, torch.float32, kb * m, "sA")
+        _buffer(sb, torch.float32, kb * (n if op == WGRAD else (n + 127) // 128), "sB")
+    _check(lib().mxfp8_blockwise_gemm(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(out), m, n, k,
+                                      op, out_dtype, _stream(stream)), "mxfp8_blockwise_gemm")
+    return out
+
+
+# --------------------------------------------------------------- token log probabilities
+
+MAX_TOP = 32
+
+
+class TokenLogprobs(NamedTuple):
+    """Result of token_logprobs, one entry (or row) per row of logits."""
+    logprob: torch.Tensor                # float32 [rows]
+    entropy: torch.Tensor                # float32 [rows]
+    stats: torch.Tensor                  # float32 [rows, 2]: max logit, log of the sum
+    top_logprob: Optional[torch.Tensor]  # float32 [rows, top], or None for top = 0
+    top_id: Optional[torch.Tensor]       # int64 [rows, top], or None
+
+
+def _logits(t: torch.Tensor, name: str):
+    """Logits as the library takes them: 2-D, BF16 or FP32, each row contiguous, on the
+    current device. Returns (dtype code, rows, vocab, row pitch)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}; the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    rows, vocab = t.shape
+    pitch, step = t.stride()
+    if rows <= 1:
+        pitch = vocab
+    if vocab > 1 and step != 1 or pitch < vocab:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap, got strides "
+                         f"{t.stride()}")
+    return OUT_BF16 if t.dtype == torch.bfloat16 else OUT_FP32, rows, vocab, pitch
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, temperature: float = 1.0,
+                   top: int = 0, stream=None) -> TokenLogprobs:
+    """Log probability of each row's target token under softmax(logits / temperature), the
+    entropy, and the `top` (at most MAX_TOP) likeliest tokens, equal logits lowest token
+    first. logits: BF16 or FP32 [rows, vocab], rows of any pitch; targets: int64 [rows],
+    negative where a row is not scored (logprob 0). Masked logits are -inf; see
+    include/mxfp8.h for rows with nothing left, and for NaN."""
+    dt, rows, vocab, pitch = _logits(logits, "logits")
+    _buffer(targets, torch.int64, rows, "targets")
+    if not 0 <= top <= MAX_TOP:
+        raise ValueError(f"top must be 0 to {MAX_TOP}, got {top}")
+    dev = logits.device
+    logprob = _new((rows,), torch.float32, dev, stream)
+    entropy = _new((rows,), torch.float32, dev, stream)
+    stats = _new((rows, 2), torch.float32, dev, stream)
+    top_logprob = top_id = None
+    if top:
+        top_logprob = _new((rows, top), torch.float32, dev, stream)
+        top_id = _new((rows, top), torch.int64, dev, stream)
+    _check(lib().mxfp8_token_logprobs(_ptr(logits), dt, rows, vocab, pitch, _ptr(targets),
+                                      temperature, _ptr(logprob), _ptr(entropy), _ptr(stats),
+                                      top, _ptr(top_logprob) if top else None,
+                                      _ptr(top_id) if top else None, _stream(stream)),
+           "mxfp8_token_logprobs")
+    return TokenLogprobs(logprob, entropy, stats, top_logprob, top_id)
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor,
+                            entropy: torch.Tensor, grad_logprob: torch.Tensor,
+                            grad_entropy=None, top_id=None, grad_top=None,
+                            temperature: float = 1.0, out=None, stream=None) -> torch.Tensor:
+    """Gradient with respect to the logits of a loss whose gradients with respect to
+    token_logprobs' logprob, entropy and top_logprob are given (float32; the last two
+    optional). `stats`, `entropy` and `top_id` are that call's, `temperature` its
+    temperature. The result has the logits' type, shape and row pitch; `out` may be any such
+    tensor of contiguous rows, the logits themselves included."""
+    dt, rows, vocab, pitch = _logits(logits, "logits")
+    _buffer(targets, torch.int64, rows, "targets")
+    _buffer(stats, torch.float32, 2 * rows, "stats")
+    _buffer(entropy, torch.float32, rows, "entropy")
+    _buffer(grad_logprob, torch.float32, rows, "grad_logprob")
+    if grad_entropy is not None:
+        _buffer(grad_entropy, torch.float32, rows, "grad_entropy")
+    top = 0
+    if (grad_top is None) != (top_id is None):
+        raise ValueError("top_id and grad_top go together")
+    if grad_top is not None:
+        if grad_top.dim() != 2 or not 1 <= grad_top.shape[1] <= MAX_TOP:
+            raise ValueError(f"grad_top must be [rows, 1 to {MAX_TOP}], got "
+                             f"{tuple(grad_top.shape)}")
+        top = grad_top.shape[1]
+        if tuple(top_id.shape) != tuple(grad_top.shape):
+            raise ValueError(f"top_id is {tuple(top_id.shape)}; grad_top is "
+                             f"{tuple(grad_top.shape)}")
+        _buffer(grad_top, torch.float32, rows * top, "grad_top")
+        _buffer(top_id, torch.int64, rows * top, "top_id")
+    if out is None:
+        out = _new((rows, pitch), logits.dtype, logits.device, stream)[:, :vocab]
+        out_pitch = pitch
+    else:
+        odt, orows, ovocab, out_pitch = _logits(out, "out")
+        if (odt, orows, ovocab) != (dt, rows, vocab):
+            raise ValueError(f"out must be {logits.dtype} {tuple(logits.shape)}, got {out.dtype} "
+                             f"{tuple(out.shape)}")
+    _check(lib().mxfp8_token_logprobs_backward(
+        _ptr(logits), dt, rows, vocab, pitch, _ptr(targets), temperature, _ptr(stats),
+        _ptr(entropy), _ptr(grad_logprob), None if grad_entropy is None else _ptr(grad_entropy),
+        top, _ptr(top_id) if top else None, _ptr(grad_top) if top else None, _ptr(out),
+        out_pitch, _stream(stream)), "mxfp8_token_logprobs_backward")
     return out
 
 

@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp8.so")
-SOURCES = ("api.cu", "quantize.cu", "gemm.cu", "selfcheck.cu")
+SOURCES = ("api.cu", "quantize.cu", "gemm.cu", "blockwise_gemm.cu",
+           "logprob.cu", "selfcheck.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

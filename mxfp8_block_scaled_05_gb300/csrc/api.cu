@@ -77,6 +77,9 @@ int device_state(DeviceState** out) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // a * b * c into *out, false if the product leaves int64 (sizes of impossible tensors).
@@ -136,6 +139,7 @@ const char* mxfp8_status_string(int status) {
     case MXFP8_ERR_UNSUPPORTED_ARCH: return "unsupported device (needs compute capability 10.3, sm_103a)";
     case MXFP8_ERR_CUDA: return "CUDA call failed";
     case MXFP8_ERR_BAD_OFFSETS: return "expert offsets invalid (must be 0-based, non-decreasing, 32-aligned, end at total_rows)";
+    case MXFP8_ERR_BAD_TARGET: return "a target token is at or past the vocabulary";
     case MXFP8_ERR_TIMEOUT: return "a kernel pipeline wait timed out; its work was abandoned";
     default: return "unknown status";
   }
@@ -311,6 +315,55 @@ int mxfp8_quantize_blockwise(const void* src_dev, int64_t rows, int64_t cols, vo
              : MXFP8_ERR_CUDA;
 }
 
+static int blockwise_1d(const void* src, int64_t rows, int64_t cols, void* row_out,
+                        float* row_inv, void* col_out, float* col_inv, bool row, bool col,
+                        bool two_d, int scale_type, void* stream) {
+  if (scale_type != MXFP8_BW_SCALE_FP32 && scale_type != MXFP8_BW_SCALE_POW2)
+    return MXFP8_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 0) return MXFP8_ERR_INVALID_ARG;
+  if (cols % (row ? 16 : 8) || (two_d && rows % 16)) return MXFP8_ERR_ALIGNMENT;
+  if (rows == 0 || cols == 0) return MXFP8_OK;
+  if (!src || (row && (!row_out || !row_inv)) || (col && (!col_out || !col_inv)))
+    return MXFP8_ERR_INVALID_ARG;
+  if (!aligned16(src) || (row && !aligned16(row_out)) || (col && !aligned16(col_out)) ||
+      (row && !aligned4(row_inv)) || (col && !aligned4(col_inv)))
+    return MXFP8_ERR_ALIGNMENT;
+  if (cdiv(rows, 128) > kMaxTokenTiles || cols > 0x7FFFFF00) return MXFP8_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  const int st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  const BlockwiseArgs a{src, rows, cols, row ? row_out : nullptr, row_inv,
+                        col ? col_out : nullptr, col_inv, two_d,
+                        scale_type == MXFP8_BW_SCALE_POW2};
+  return launch_blockwise_tiles(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MXFP8_OK
+             : MXFP8_ERR_CUDA;
+}
+
+int mxfp8_quantize_blockwise_1d(const void* src_dev, int64_t rows, int64_t cols, int axis,
+                                void* out_dev, float* scale_inv_dev, int scale_type,
+                                void* stream) {
+  if (axis != MXFP8_AXIS_ROW && axis != MXFP8_AXIS_COL) return MXFP8_ERR_INVALID_ARG;
+  const bool row = axis == MXFP8_AXIS_ROW;
+  return blockwise_1d(src_dev, rows, cols, out_dev, scale_inv_dev, out_dev, scale_inv_dev, row,
+                      !row, false, scale_type, stream);
+}
+
+int mxfp8_quantize_blockwise_1d_dual(const void* src_dev, int64_t rows, int64_t cols,
+                                     void* row_out_dev, float* row_scale_inv_dev,
+                                     void* col_out_dev, float* col_scale_inv_dev,
+                                     int scale_type, void* stream) {
+  return blockwise_1d(src_dev, rows, cols, row_out_dev, row_scale_inv_dev, col_out_dev,
+                      col_scale_inv_dev, true, true, false, scale_type, stream);
+}
+
+int mxfp8_quantize_blockwise_dual(const void* src_dev, int64_t rows, int64_t cols,
+                                  void* out_dev, float* scale_inv_dev, void* out_t_dev,
+                                  float* scale_inv_t_dev, int scale_type, void* stream) {
+  return blockwise_1d(src_dev, rows, cols, out_dev, scale_inv_dev, out_t_dev, scale_inv_t_dev,
+                      true, true, true, scale_type, stream);
+}
+
 int mxfp8_quantize_batched(const void* src_dev, int64_t batch, int64_t rows, int64_t cols,
                            int axis, void* out_dev, void* scales_dev, int scale_layout,
                            void* stream) {
@@ -405,6 +458,28 @@ int mxfp8_gemm_ws(const void* A_dev, const void* sA_dev, const void* B_dev, cons
   return launch_gemm(a, static_cast<cudaStream_t>(stream));
 }
 
+int mxfp8_blockwise_gemm(const void* A_dev, const float* sA_dev, const void* B_dev,
+                         const float* sB_dev, void* C_dev, int64_t M, int64_t N, int64_t K,
+                         int op, int out_dtype, void* stream) {
+  if (M < 0 || N < 0 || K < 0) return MXFP8_ERR_INVALID_ARG;
+  if (M > 0x7FFFFF00 || N > 0x7FFFFF00 || K > 0x7FFFFF00) return MXFP8_ERR_INVALID_ARG;
+  if (K % 16 || N % 8) return MXFP8_ERR_ALIGNMENT;
+  if (op < MXFP8_OP_FPROP || op > MXFP8_OP_WGRAD) return MXFP8_ERR_INVALID_ARG;
+  if (out_dtype != MXFP8_OUT_BF16 && out_dtype != MXFP8_OUT_FP32) return MXFP8_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return MXFP8_OK;
+  if (K == 0) return zero_fill_output(C_dev, M * N, out_dtype, stream);
+  if (!A_dev || !sA_dev || !B_dev || !sB_dev || !C_dev) return MXFP8_ERR_INVALID_ARG;
+  if (!aligned16(A_dev) || !aligned16(B_dev) || !aligned16(C_dev) || !aligned4(sA_dev) ||
+      !aligned4(sB_dev))
+    return MXFP8_ERR_ALIGNMENT;
+  DeviceState* d = nullptr;
+  const int st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  const BlockwiseGemmArgs a{A_dev, sA_dev, B_dev, sB_dev, C_dev, M, N, K,
+                            op == MXFP8_OP_WGRAD, out_dtype == MXFP8_OUT_FP32, d->status};
+  return launch_blockwise_gemm(a, static_cast<cudaStream_t>(stream));
+}
+
 int mxfp8_grouped_gemm(const void* A_dev, const void* sA_dev, const void* B_dev,
                        const void* sB_dev, void* C_dev, const int32_t* expert_offsets_dev,
                        int num_experts, int64_t total_rows, int64_t N, int64_t K, int op,
@@ -493,6 +568,83 @@ int mxfp8_selfcheck_noalloc(const void* w_codes_dev, const void* w_scales_dev,
   SelfcheckArgs a{w_codes_dev, w_scales_dev, ref_codes_dev, ref_scales_dev, N, K, x_bf16_dev,
                   tokens, ws, rel_err_dev, d->status};
   return launch_selfcheck(a, static_cast<cudaStream_t>(stream));
+}
+
+// Checks that both log probability calls share; *inv_t gets 1 / temperature.
+static int logprob_checks(int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                          double temperature, int top, float* inv_t) {
+  if (dtype != MXFP8_OUT_BF16 && dtype != MXFP8_OUT_FP32) return MXFP8_ERR_INVALID_ARG;
+  if (rows < 0 || vocab <= 0 || vocab > 0x7FFFFFFF || ld < vocab) return MXFP8_ERR_INVALID_ARG;
+  if (top < 0 || top > MXFP8_MAX_TOP) return MXFP8_ERR_INVALID_ARG;
+  int64_t bytes = 0;
+  if (!mul3(rows, ld, 4, &bytes)) return MXFP8_ERR_INVALID_ARG;
+  if (!(temperature > 0)) return MXFP8_ERR_INVALID_ARG;  // NaN too
+  const double inv = 1.0 / temperature;
+  if (!(inv >= 1.2e-38 && inv <= 2.0e38)) return MXFP8_ERR_INVALID_ARG;  // log2(e) / T fits too
+  *inv_t = static_cast<float>(inv);
+  return MXFP8_OK;
+}
+
+int mxfp8_token_logprobs(const void* logits_dev, int logits_dtype, int64_t rows,
+                         int64_t vocab, int64_t ld, const int64_t* targets_dev,
+                         double temperature, float* logprob_dev, float* entropy_dev,
+                         float* stats_dev, int top, float* top_logprob_dev,
+                         int64_t* top_id_dev, void* stream) {
+  float inv_t = 0.f;
+  int st = logprob_checks(logits_dtype, rows, vocab, ld, temperature, top, &inv_t);
+  if (st != MXFP8_OK) return st;
+  if (rows == 0) return MXFP8_OK;
+  if (!logits_dev || !targets_dev || !logprob_dev || !entropy_dev || !stats_dev ||
+      (top && (!top_logprob_dev || !top_id_dev)))
+    return MXFP8_ERR_INVALID_ARG;
+  const bool fp32 = logits_dtype == MXFP8_OUT_FP32;
+  if ((reinterpret_cast<uintptr_t>(logits_dev) & (fp32 ? 3u : 1u)) || !aligned8(targets_dev) ||
+      !aligned4(logprob_dev) || !aligned4(entropy_dev) || !aligned4(stats_dev) ||
+      (top && (!aligned4(top_logprob_dev) || !aligned8(top_id_dev))))
+    return MXFP8_ERR_ALIGNMENT;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  const LogprobArgs a{logits_dev, rows, vocab, ld, fp32, targets_dev, inv_t, logprob_dev,
+                      entropy_dev, stats_dev, top, top_logprob_dev, top_id_dev, d->status};
+  const cudaError_t e = launch_logprob(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXFP8_OK
+                          : e == cudaErrorInvalidValue ? MXFP8_ERR_INVALID_ARG : MXFP8_ERR_CUDA;
+}
+
+int mxfp8_token_logprobs_backward(const void* logits_dev, int logits_dtype, int64_t rows,
+                                  int64_t vocab, int64_t ld, const int64_t* targets_dev,
+                                  double temperature, const float* stats_dev,
+                                  const float* entropy_dev, const float* grad_logprob_dev,
+                                  const float* grad_entropy_dev, int top,
+                                  const int64_t* top_id_dev, const float* grad_top_dev,
+                                  void* grad_logits_dev, int64_t grad_ld, void* stream) {
+  float inv_t = 0.f;
+  int st = logprob_checks(logits_dtype, rows, vocab, ld, temperature, top, &inv_t);
+  if (st != MXFP8_OK) return st;
+  int64_t bytes = 0;
+  if (grad_ld < vocab || !mul3(rows, grad_ld, 4, &bytes)) return MXFP8_ERR_INVALID_ARG;
+  if (rows == 0) return MXFP8_OK;
+  if (!logits_dev || !targets_dev || !stats_dev || !entropy_dev || !grad_logprob_dev ||
+      !grad_logits_dev || (top && (!top_id_dev || !grad_top_dev)))
+    return MXFP8_ERR_INVALID_ARG;
+  if (grad_logits_dev == logits_dev && grad_ld != ld) return MXFP8_ERR_INVALID_ARG;
+  const bool fp32 = logits_dtype == MXFP8_OUT_FP32;
+  if (((reinterpret_cast<uintptr_t>(logits_dev) | reinterpret_cast<uintptr_t>(grad_logits_dev)) &
+       (fp32 ? 3u : 1u)) ||
+      !aligned8(targets_dev) || !aligned4(stats_dev) || !aligned4(entropy_dev) ||
+      !aligned4(grad_logprob_dev) || !aligned4(grad_entropy_dev) ||
+      (top && (!aligned8(top_id_dev) || !aligned4(grad_top_dev))))
+    return MXFP8_ERR_ALIGNMENT;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  const LogprobGradArgs a{logits_dev, rows, vocab, ld, fp32, targets_dev, inv_t, stats_dev,
+                          entropy_dev, grad_logprob_dev, grad_entropy_dev, top, top_id_dev,
+                          grad_top_dev, grad_logits_dev, grad_ld, d->status};
+  const cudaError_t e = launch_logprob_grad(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXFP8_OK
+                          : e == cudaErrorInvalidValue ? MXFP8_ERR_INVALID_ARG : MXFP8_ERR_CUDA;
 }
 
 int mxfp8_set_wait_limit_ns(uint64_t ns) {

@@ -1867,6 +1867,14 @@ int duo_grouped_width(int mode, int64_t N, bool fp32) {
 
 }  // namespace
 
+bool make_operand_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                      uint32_t box_outer) {
+  return make_map(map, base, 2, inner, outer, 1, BK, box_outer);
+}
+
+uint64_t pipeline_wait_ns() { return wait_limit_ns(); }
+uint64_t pipeline_drain_ns() { return drain_limit_ns(wait_limit_ns()); }
+
 void set_wait_limit_ns(uint64_t ns) { g_wait_override_ns.store(ns, std::memory_order_relaxed); }
 
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {

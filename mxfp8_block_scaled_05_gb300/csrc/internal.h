@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace mxfp8 {
@@ -54,6 +55,21 @@ cudaError_t launch_quantize_jobs(const QuantizeJobs& j, cudaStream_t stream);
 cudaError_t launch_blockwise(const void* src, int64_t rows, int64_t cols, void* out,
                              float* scale_inv, bool pow2, cudaStream_t stream);
 
+// Operands of the block-wise GEMM from one read of a BF16 matrix: row-wise and / or
+// transposed copies with 1 x 128 blocks, or (two_d) both copies with 128 x 128 blocks. A
+// null row_out / col_out leaves that copy out.
+struct BlockwiseArgs {
+  const void* src;
+  int64_t rows, cols;
+  void* row_out;
+  float* row_inv;
+  void* col_out;
+  float* col_inv;
+  bool two_d, pow2;
+};
+
+cudaError_t launch_blockwise_tiles(const BlockwiseArgs& a, cudaStream_t stream);
+
 struct GemmArgs {
   const void* A;
   const void* sA;
@@ -80,6 +96,30 @@ int launch_gemm(const GemmArgs& a, cudaStream_t stream);
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
 int launch_grouped_gemm(const GemmArgs& a, cudaStream_t stream);
 
+// The block-wise GEMM: C [M][N] = deq(A) [M][K] . deq(B) [N][K]^T.
+struct BlockwiseGemmArgs {
+  const void* A;
+  const float* sA;   // [ceil(K/128)][M]
+  const void* B;
+  const float* sB;   // [ceil(N/128)][ceil(K/128)], or (wgrad) [ceil(K/128)][N]
+  void* C;
+  int64_t M, N, K;
+  bool wgrad, out_fp32;
+  int* status;
+};
+
+// Returns MXFP8_OK or an mxfp8_status code.
+int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream);
+
+// Tensor map of a row-major byte matrix [outer][inner] in 128-byte x box_outer boxes with
+// the 128-byte swizzle.
+bool make_operand_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                      uint32_t box_outer);
+
+// Limits of pipeline waits, and of waits for work in flight on the way out of a kernel.
+uint64_t pipeline_wait_ns();
+uint64_t pipeline_drain_ns();
+
 struct SelfcheckArgs {
   const void* w_codes;   // E4M3 [N][K] as the GEMM reads it
   const void* w_scales;  // swizzled scales as the GEMM reads them
@@ -99,6 +139,43 @@ int64_t selfcheck_workspace_bytes(int64_t T, int64_t N, int64_t K);
 constexpr int64_t kSelfcheckNoallocMaxBytes = int64_t(8) << 20;
 int selfcheck_noalloc_workspace(void** out);
 int launch_selfcheck(const SelfcheckArgs& a, cudaStream_t stream);
+
+// Log probabilities of given tokens (logits BF16, or FP32 with fp32 set).
+struct LogprobArgs {
+  const void* logits;     // [rows][ld], the first `vocab` of each row are read
+  int64_t rows, vocab, ld;
+  bool fp32;
+  const int64_t* targets;
+  float inv_t;            // 1 / temperature
+  float* logprob;         // [rows]
+  float* entropy;         // [rows]
+  float* stats;           // [rows][2]: maximum logit, log of the sum
+  int top;                // alternatives per row, 0 .. 32
+  float* top_logprob;     // [rows][top]
+  int64_t* top_id;        // [rows][top]
+  int* status;
+};
+
+struct LogprobGradArgs {
+  const void* logits;
+  int64_t rows, vocab, ld;
+  bool fp32;
+  const int64_t* targets;
+  float inv_t;
+  const float* stats;
+  const float* entropy;
+  const float* g_logprob;
+  const float* g_entropy;  // or nullptr
+  int top;
+  const int64_t* top_id;
+  const float* g_top;
+  void* out;               // [rows][out_ld], the logits' type; may be the logits
+  int64_t out_ld;
+  int* status;
+};
+
+cudaError_t launch_logprob(const LogprobArgs& a, cudaStream_t stream);
+cudaError_t launch_logprob_grad(const LogprobGradArgs& a, cudaStream_t stream);
 
 int num_sms();  // of the current device (cached)
 

@@ -549,6 +549,32 @@ quantize_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t col
   }
 }
 
+// Factor s of a block-wise block from its largest |BF16| bits, and 1 / s. The factor is
+// 448 / amax in IEEE single precision (clamped to the largest float on overflow) or the
+// power of two 2^-ceil(log2(amax / 448)); 1 for a zero block; 0 marks a block holding a NaN
+// or an infinity, whose inverse is NaN.
+__device__ __forceinline__ void blockwise_scale(uint32_t a, bool pow2, float& f, float& inv) {
+  if (a >= 0x7F80u) {                 // NaN or Inf in the block
+    f = 0.f;
+    inv = __uint_as_float(0x7FC00000u);
+  } else if (a == 0) {                // all zero
+    f = 1.f;
+    inv = 1.f;
+  } else if (pow2) {
+    // e = ceil(log2(amax / 448)) >= -127; the BF16 exponent gives floor(log2 amax)
+    int e = static_cast<int>(a >> 7) - 127 - 8 + ((a & 0x7Fu) > 0x60u ? 1 : 0);
+    if ((a >> 7) == 0) e = -127;      // BF16 subnormal
+    e = e < -127 ? -127 : e;
+    f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    inv = e >= -126 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23)
+                    : __uint_as_float(0x00400000u);  // 2^-127
+  } else {
+    f = __fdiv_rn(448.f, __uint_as_float(a << 16));
+    if (isinf(f)) f = 3.40282347e38f;  // the largest finite float
+    inv = __fdiv_rn(1.f, f);
+  }
+}
+
 // FP8 block-wise weight quantization: one FP32 (or power-of-two) scale per 128 x 128
 // block ("End-to-End MXFP8 RL on Blackwell", section "A different grid, and drift"). One
 // CTA per block: the block maximum comes from packed 16-bit maxima, warp shuffles and a
@@ -589,25 +615,7 @@ blockwise_quantize_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_
     uint32_t a = 0;
     for (int w = 0; w < kThreads / 32; ++w) a = max(a, warp_max[w]);
     float f, inv;
-    if (a >= 0x7F80u) {                 // NaN or Inf in the block
-      f = 0.f;
-      inv = __uint_as_float(0x7FC00000u);
-    } else if (a == 0) {                // all zero
-      f = 1.f;
-      inv = 1.f;
-    } else if (pow2) {
-      // e = ceil(log2(amax / 448)) >= -127; the BF16 exponent gives floor(log2 amax)
-      int e = static_cast<int>(a >> 7) - 127 - 8 + ((a & 0x7Fu) > 0x60u ? 1 : 0);
-      if ((a >> 7) == 0) e = -127;      // BF16 subnormal
-      e = e < -127 ? -127 : e;
-      f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      inv = e >= -126 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23)
-                      : __uint_as_float(0x00400000u);  // 2^-127
-    } else {
-      f = __fdiv_rn(448.f, __uint_as_float(a << 16));
-      if (isinf(f)) f = 3.40282347e38f;  // the largest finite float
-      inv = __fdiv_rn(1.f, f);
-    }
+    blockwise_scale(a, pow2 != 0, f, inv);
     s_factor = f;
     scale_inv[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = inv;
   }
@@ -627,6 +635,174 @@ blockwise_quantize_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_
       o.y = nan4(x[j].z, x[j].w);
     }
     *reinterpret_cast<uint2*>(out + (row0 + r) * cols + col0 + 8 * v) = o;
+  }
+}
+
+// FP8 block-wise operands of the block-wise GEMM: 1 x 128 blocks along either axis of a
+// BF16 matrix (activations and gradients), or 128 x 128 blocks with a transposed copy
+// (weights). Scales and codes follow the rule of the 128 x 128 quantizer above.
+//   kRow  row-wise copy: codes [rows][cols], blocks along the columns, scale inverses
+//         [ceil(cols/128)][rows];
+//   kCol  transposed copy: codes [cols][pitch], pitch = rows rounded up to 16 (the extra
+//         codes are zero), blocks along the rows, scale inverses [ceil(rows/128)][cols];
+//   k2D   one scale per 128 x 128 block for both copies, [row tiles][column tiles] and its
+//         transpose.
+// Bound by memory: 2 bytes read and 1 or 2 written per element. One CTA owns a 128 x 128
+// tile, read once into registers with every load in flight; a thread holds an 8 x 8 patch
+// (8 consecutive rows of 8 columns), so that the transposed copy needs no shuffle: the
+// E4M3 conversion takes two values at once, and here takes them from two rows, which leaves
+// the 8 codes of a column in 8 consecutive bytes. They pass through shared memory (16 KB,
+// 8-byte units XOR-swizzled by the patch column) to leave as 16-byte stores. The scales of
+// the 8 rows a half-warp shares are computed by 8 of its lanes, one division each, instead
+// of 8 divisions in every lane.
+template <bool kRow, bool kCol, bool k2D>
+__global__ void __launch_bounds__(kThreads)
+blockwise_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t cols,
+                      uint8_t* __restrict__ row_out, float* __restrict__ row_inv,
+                      uint8_t* __restrict__ col_out, float* __restrict__ col_inv, int pow2) {
+  __shared__ __align__(16) uint8_t stage[kCol ? kTile * kTile : 16];
+  __shared__ __align__(16) uint32_t warp_max[kThreads / 32][kTile / 2];  // two columns a word
+  __shared__ __align__(16) float factor[kTile];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int t = threadIdx.x, v = t & 15, g = t >> 4, lane = t & 31;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * kTile;
+  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kTile;
+  const int rows_valid = static_cast<int>((rows - row0) < kTile ? (rows - row0) : kTile);
+  const int cols_valid = static_cast<int>((cols - col0) < kTile ? (cols - col0) : kTile);
+  const bool col_ok = 8 * v < cols_valid;  // cols % 8 == 0
+  uint32_t x[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = 8 * g + j;
+    const uint4 w = (col_ok && r < rows_valid) ? ld_nc_v4(src + (row0 + r) * cols + col0 + 8 * v)
+                                               : make_uint4(0, 0, 0, 0);
+    x[j][0] = w.x;
+    x[j][1] = w.y;
+    x[j][2] = w.z;
+    x[j][3] = w.w;
+  }
+
+  float fb = 0.f;  // k2D: the tile's factor
+  if constexpr (k2D) {
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) m2 = max_u16x2(m2, x[j][w] & kAbs2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m2 = max_u16x2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, o));
+    if (lane == 0) warp_max[t >> 5][0] = m2;
+    __syncthreads();
+    m2 = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) m2 = max_u16x2(m2, warp_max[w][0]);
+    float inv;
+    blockwise_scale(max(m2 & 0xFFFFu, m2 >> 16), pow2 != 0, fb, inv);
+    if (t == 0) {
+      row_inv[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = inv;
+      col_inv[static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y] = inv;
+    }
+  }
+
+  if constexpr (kCol && !k2D) {  // column maxima over the tile's rows, then their factors
+    uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) m[w] = max_u16x2(m[w], x[j][w] & kAbs2);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m[w] = max_u16x2(m[w], __shfl_xor_sync(0xFFFFFFFFu, m[w], 16));
+    if (lane < 16)
+      *reinterpret_cast<uint4*>(&warp_max[t >> 5][4 * v]) = make_uint4(m[0], m[1], m[2], m[3]);
+    __syncthreads();
+    if (t < kTile) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w)
+        a = max(a, static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(warp_max[w])[t]));
+      float f, inv;
+      blockwise_scale(a, pow2 != 0, f, inv);
+      factor[t] = f;
+      if (t < cols_valid) col_inv[static_cast<int64_t>(blockIdx.y) * cols + col0 + t] = inv;
+    }
+    __syncthreads();
+  }
+
+  if constexpr (kRow) {
+    float mine = fb;  // lane v < 8 of a half-warp: the factor of row 8 g + v
+    if constexpr (!k2D) {
+      uint32_t m[4];  // rows j and j + 4 in the two halves of a word
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a = 0, b = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          a = max_u16x2(a, x[j][w] & kAbs2);
+          b = max_u16x2(b, x[j + 4][w] & kAbs2);
+        }
+        m[j] = max(a & 0xFFFFu, a >> 16) | (max(b & 0xFFFFu, b >> 16) << 16);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = max_u16x2(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], o));
+      const uint32_t lo = (v & 1) ? m[1] : m[0], hi = (v & 1) ? m[3] : m[2];
+      const uint32_t w = (v & 2) ? hi : lo;
+      float inv;
+      blockwise_scale((v & 4) ? w >> 16 : w & 0xFFFFu, pow2 != 0, mine, inv);
+      if (v < 8 && 8 * g + v < rows_valid)
+        row_inv[static_cast<int64_t>(blockIdx.x) * rows + row0 + 8 * g + v] = inv;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = k2D ? fb : __shfl_sync(0xFFFFFFFFu, mine, (lane & 16) + j);
+      const int r = 8 * g + j;
+      if (!col_ok || r >= rows_valid) continue;
+      uint2 o;
+      if (f != 0.f) {
+        o.x = e4m3x4(x[j][0], x[j][1], f);
+        o.y = e4m3x4(x[j][2], x[j][3], f);
+      } else {
+        o.x = nan4(x[j][0], x[j][1]);
+        o.y = nan4(x[j][2], x[j][3]);
+      }
+      *reinterpret_cast<uint2*>(row_out + (row0 + r) * cols + col0 + 8 * v) = o;
+    }
+  }
+
+  if constexpr (kCol) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // column 8 v + i of the tile, its rows 8 g .. 8 g + 7
+      const float f = k2D ? fb : factor[8 * v + i];
+      uint32_t bits[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        bits[j] = (i & 1) ? x[j][i >> 1] & 0xFFFF0000u : x[j][i >> 1] << 16;
+      uint2 o;
+      if (f != 0.f) {
+        o.x = e4m3x2_f32bits(bits[0], bits[1], f) | (e4m3x2_f32bits(bits[2], bits[3], f) << 16);
+        o.y = e4m3x2_f32bits(bits[4], bits[5], f) | (e4m3x2_f32bits(bits[6], bits[7], f) << 16);
+      } else {  // 0x7F with each sign (zero in the padding rows, as in the finite case)
+        o.x = o.y = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t b = 8 * g + j < rows_valid ? 0x7Fu | ((bits[j] >> 24) & 0x80u) : 0u;
+          if (j < 4) o.x |= b << (8 * j); else o.y |= b << (8 * (j - 4));
+        }
+      }
+      *reinterpret_cast<uint2*>(stage + (8 * v + i) * kTile + 8 * (g ^ v)) = o;
+    }
+    __syncthreads();
+    const int64_t pitch = (rows + 15) / 16 * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // 16 rows of one column per thread and step
+      const int c = (t >> 3) + 32 * i, p = t & 7, cv = c >> 3;
+      if (c >= cols_valid || row0 + 16 * p >= pitch) continue;
+      uint4 o = *reinterpret_cast<const uint4*>(stage + c * kTile + 16 * (p ^ (cv >> 1)));
+      if (cv & 1) o = make_uint4(o.z, o.w, o.x, o.y);
+      *reinterpret_cast<uint4*>(col_out + (col0 + c) * pitch + row0 + 16 * p) = o;
+    }
   }
 }
 
@@ -723,6 +899,20 @@ cudaError_t launch_blockwise(const void* src, int64_t rows, int64_t cols, void* 
   return launch_pdl(blockwise_quantize_kernel, grid, 0, stream,
                     static_cast<const uint16_t*>(src), rows, cols, static_cast<uint8_t*>(out),
                     scale_inv, pow2 ? 1 : 0);
+}
+
+cudaError_t launch_blockwise_tiles(const BlockwiseArgs& a, cudaStream_t stream) {
+  const int64_t gx = (a.cols + kTile - 1) / kTile, gy = (a.rows + kTile - 1) / kTile;
+  if (gx == 0 || gy == 0) return cudaSuccess;
+  if (gy > 65535 || gx > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  auto k = a.two_d ? blockwise_tile_kernel<true, true, true>
+           : !a.col_out ? blockwise_tile_kernel<true, false, false>
+           : !a.row_out ? blockwise_tile_kernel<false, true, false>
+                        : blockwise_tile_kernel<true, true, false>;
+  return launch_pdl(k, grid, 0, stream, static_cast<const uint16_t*>(a.src), a.rows, a.cols,
+                    static_cast<uint8_t*>(a.row_out), a.row_inv,
+                    static_cast<uint8_t*>(a.col_out), a.col_inv, a.pow2 ? 1 : 0);
 }
 
 cudaError_t launch_quantize(const QuantizeArgs& a, cudaStream_t stream) {
