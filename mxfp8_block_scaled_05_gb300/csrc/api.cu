@@ -461,6 +461,22 @@ int mxfp8_gemm_ws(const void* A_dev, const void* sA_dev, const void* B_dev, cons
 int mxfp8_blockwise_gemm(const void* A_dev, const float* sA_dev, const void* B_dev,
                          const float* sB_dev, void* C_dev, int64_t M, int64_t N, int64_t K,
                          int op, int out_dtype, void* stream) {
+  return mxfp8_blockwise_gemm_ws(A_dev, sA_dev, B_dev, sB_dev, C_dev, M, N, K, op, out_dtype,
+                                 nullptr, 0, stream);
+}
+
+size_t mxfp8_blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
+  if (M <= 0 || N <= 0 || K <= 0 || M > 0x7FFFFF00 || N > 0x7FFFFF00 || K > 0x7FFFFF00)
+    return 0;
+  if (out_dtype != MXFP8_OUT_BF16 && out_dtype != MXFP8_OUT_FP32) return 0;
+  return static_cast<size_t>(
+      blockwise_gemm_workspace_bytes(M, N, K, out_dtype == MXFP8_OUT_FP32));
+}
+
+int mxfp8_blockwise_gemm_ws(const void* A_dev, const float* sA_dev, const void* B_dev,
+                            const float* sB_dev, void* C_dev, int64_t M, int64_t N, int64_t K,
+                            int op, int out_dtype, void* workspace_dev, size_t workspace_bytes,
+                            void* stream) {
   if (M < 0 || N < 0 || K < 0) return MXFP8_ERR_INVALID_ARG;
   if (M > 0x7FFFFF00 || N > 0x7FFFFF00 || K > 0x7FFFFF00) return MXFP8_ERR_INVALID_ARG;
   if (K % 16 || N % 8) return MXFP8_ERR_ALIGNMENT;
@@ -472,11 +488,13 @@ int mxfp8_blockwise_gemm(const void* A_dev, const float* sA_dev, const void* B_d
   if (!aligned16(A_dev) || !aligned16(B_dev) || !aligned16(C_dev) || !aligned4(sA_dev) ||
       !aligned4(sB_dev))
     return MXFP8_ERR_ALIGNMENT;
+  if (workspace_dev && !aligned16(workspace_dev)) return MXFP8_ERR_ALIGNMENT;
   DeviceState* d = nullptr;
   const int st = device_state(&d);
   if (st != MXFP8_OK) return st;
   const BlockwiseGemmArgs a{A_dev, sA_dev, B_dev, sB_dev, C_dev, M, N, K,
-                            op == MXFP8_OP_WGRAD, out_dtype == MXFP8_OUT_FP32, d->status};
+                            op == MXFP8_OP_WGRAD, out_dtype == MXFP8_OUT_FP32, d->status,
+                            workspace_dev, workspace_dev ? workspace_bytes : 0};
   return launch_blockwise_gemm(a, static_cast<cudaStream_t>(stream));
 }
 

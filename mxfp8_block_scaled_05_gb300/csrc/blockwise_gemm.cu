@@ -15,8 +15,8 @@
 // fold 256 (one FMA per element, 128 lanes; 512 with a scale for every column), TMEM reads
 // 256. All overlap.
 //
-// Roles of a CTA's 320 threads: warp 0 TMA producer, warp 1 MMA issuer (and TMEM
-// allocation), warps 2-9 fold and store, two per TMEM lane quarter, each half the columns.
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (and TMEM allocation), the last eight warps
+// fold and store, two per TMEM lane quarter, each half the columns.
 //
 // Modes, by which operand lies along the 128 TMEM lanes ("rows") and the columns:
 //   kFprop    rows = A (a scale per row and block), columns = B (128 x 128 blocks)
@@ -45,28 +45,40 @@ namespace {
 
 constexpr int BM = 128;        // tile rows per CTA = TMEM lanes
 constexpr int BK = 128;        // K per block and pipeline stage
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kFoldFirst = 4;  // warps 0-3: producer, MMA issuer, scales, none
+constexpr int kScaleRing = 4;  // blocks whose scales are in shared memory or on their way
 
 enum Mode : int { kFprop = 0, kWgrad = 1, kSwapped = 2 };
 
 template <int BN, bool kPair>
 struct Cfg {
-  static constexpr int kBRows = kPair ? BN / 2 : BN;   // column-operand rows staged per CTA
+  static constexpr int kBRows = kPair ? BN / 2 : BN;  // column-operand rows staged per CTA
   static constexpr int kABytes = BM * BK;
   static constexpr int kBBytes = kBRows * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  // narrow tiles leave room for two or three CTAs on an SM
+  // narrow tiles leave room for two CTAs on an SM
   static constexpr int kStages = BN >= 128 ? 6 : 4;
-  static constexpr int kNC = BN / 2;                   // columns per epilogue warp
+  // four folding warps (a TMEM lane quarter each) for each group of columns
+  static constexpr int kColGroups = BN == 192 ? 3 : 2;
+  static constexpr int kNC = BN / kColGroups;         // columns per folding warp
+  static constexpr int kFoldWarps = 4 * kColGroups;
+  static constexpr int kThreads = 32 * (kFoldFirst + kFoldWarps);
+  // Pairs hold their sums in more registers than an even share: the folding warpgroups take
+  // some over from the first one (12 x 168 = 8 x 224 + 4 x 56; 16 x 128 = 12 x 152 + 4 x 56).
+  static constexpr int kFoldRegs = BN == 192 ? 152 : 224, kOtherRegs = 56;
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kOffA + kStages * kABytes;
-  static constexpr int kOffScale = kOffB + kStages * kBBytes;  // column scales, per warp
-  static constexpr int kOffBar = kOffScale + kEpiWarps * kNC * 4;
-  static constexpr int kNumBars = 2 * kStages + 5;     // full, empty, acc_full, acc_empty, done
+  // store staging: one 32-row x 64-byte box per folding warp, 1024-byte aligned
+  static constexpr int kBoxBytes = 32 * 64;
+  static constexpr int kOffBox = kOffB + kStages * kBBytes;
+  static constexpr int kOffScale = kOffBox + kFoldWarps * kBoxBytes;
+  static constexpr int kScaleFloats = BM + (BN < 32 ? 32 : BN);  // a block's row, column scales
+  static constexpr int kOffBar = kOffScale + kScaleRing * kScaleFloats * 4;
+  // full, empty [kStages]; sc_full, sc_free [kScaleRing]; acc_full, acc_empty [2]; done
+  static constexpr int kNumBars = 2 * kStages + 2 * kScaleRing + 5;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + slack for 1024-byte alignment
-  static constexpr int kTmemCols = 2 * BN;             // two accumulators
+  static constexpr int kTmemCols = BN == 192 ? 512 : 2 * BN;  // two accumulators
   static constexpr int kMinCtas = BN <= 64 ? 2 : 1;
   static_assert(kTmemCols >= 32 && kTmemCols <= 512, "TMEM columns");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory overflow");
@@ -82,12 +94,14 @@ struct Params {
   int64_t nr, nc;       // valid rows and columns
   int nkb;              // blocks of 128 along K
   int out_fp32;
-  int vec32;            // output rows take 32-byte stores
   int split;            // CTAs that share a tile's reduction (a cluster)
   uint32_t tiles, row_tiles, col_tiles;  // pairs: row tiles are of 256 rows
   uint32_t band;        // row tiles per raster band
   int* status;
   uint64_t wait_ns, drain_ns;
+  // the kernel returns at once unless one of these words is set (nullptr: it runs)
+  const uint32_t* only_if;
+  int num_only_if;
 };
 
 // Tile `id` of a banded raster: bands of `band` row tiles sweep across the columns, rows
@@ -104,6 +118,11 @@ __device__ __forceinline__ void tile_at(const Params& p, uint32_t id, int64_t& r
 
 // TMEM loads of G columns of the warp's lanes, and the wait for them. The wait carries the
 // registers, so that no use of them moves ahead of it.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
@@ -119,64 +138,110 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7])
-               :: "memory");
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31,"
+      " %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47,"
+      " %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]),
+        "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]),
+        "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
+        "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]),
+        "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :: "memory");
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+  tmem_ld_32x32b_x32(taddr, r);
 }
-
-__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
-  return pack2(__uint_as_float(lo), __uint_as_float(hi));
-}
-
-// Scales of extreme magnitude. |P_b| <= 448^2 * 128 < 2^25, so P_b times a factor within
-// 2^-100 .. 2^100 stays inside FP32's normal range; beyond it the factor sr is split into
-// two of half its exponent, and the column's scale is applied between them.
-__device__ __forceinline__ bool extreme(float s) { return s < 0x1p-100f || s > 0x1p100f; }
-
-__device__ __forceinline__ void halves_of(float s, float& s1, float& s2) {
-  const int e = static_cast<int>((__float_as_uint(s) >> 23) & 0xFFu) - 127;
-  s1 = __uint_as_float(static_cast<uint32_t>(e / 2 + 127) << 23);
-  s2 = s * __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);
-}
-
-// acc[i] += s1 sc_i s2 P_i for the warp's kNC columns of one block: P from TMEM, read one
-// group ahead of its use.
-//   kColVec  the column scales sc_i come from shared memory; else all are `sc`
-//   kSplit   the row scale is s1 s2, applied on both sides of the column's; else it is s1
-//            (kColVec), or s1 is the product of both scales and nothing else applies
-template <int kNC, bool kColVec, bool kSplit>
-__device__ __forceinline__ void fold(uint64_t (&acc)[kNC / 2], uint32_t taddr, float s1, float s2,
-                                     float sc, const float* col_scale) {
-  constexpr int G = kNC < 16 ? kNC : 16;
-  constexpr int kGroups = kNC / G;
-  uint32_t r[2][G];
-  tmem_ld(taddr, r[0]);
-  const uint64_t f1 = pack2(s1, s1), f2 = pack2(s2, s2), fc = pack2(sc, sc);
+template <int G>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[G]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    tmem_wait(r[g & 1]);
-    if (g + 1 < kGroups) tmem_ld(taddr + G * (g + 1), r[(g + 1) & 1]);
-#pragma unroll
-    for (int i = 0; i < G / 2; ++i) {
-      const uint64_t v = pair_of(r[g & 1][2 * i], r[g & 1][2 * i + 1]);
-      uint64_t& a = acc[g * (G / 2) + i];
-      uint64_t c2 = fc;
-      if constexpr (kColVec) {
-        const float2 cs = *reinterpret_cast<const float2*>(col_scale + g * G + 2 * i);
-        c2 = pack2(cs.x, cs.y);
+  for (int i = 0; i < G; ++i) asm volatile("" : "+r"(r[i]) :: "memory");
+}
+
+// 4 bytes global -> shared, and an arrival on `bar` once this thread's copies so far are in.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// A whole warp waits for a phase, every lane for itself (one lane and a shuffle or vote took
+// longer); true for all lanes or for none, and the warp is converged again. The clock is
+// read, and the abort flag looked at, only once 64 polls have failed: the fold's hand-overs
+// are on the critical path.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                           uint64_t limit_ns) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+      ok = mbar_try_wait(bar, parity);
+      if (ok) break;
+      if ((i & 63) == 0) {
+        if (*abort) break;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        else if (t - t0 > limit_ns) break;
       }
-      if constexpr (kSplit) a = fma2(mul2(mul2(v, f1), c2), f2, a);
-      else if constexpr (kColVec) a = fma2(mul2(v, f1), c2, a);
-      else a = fma2(v, f1, a);
+    }
+  }
+  ok = __all_sync(0xFFFFFFFFu, ok);
+  __syncwarp();  // a vote does not reconverge the warp, as the .aligned instructions need it
+  return ok;
+}
+
+// An arrival by one lane of the warp, as a predicated instruction instead of a branch.
+__device__ __forceinline__ void arrive_if(bool one, uint32_t cluster_addr) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}"
+      ::"r"(cluster_addr), "r"(one ? 1 : 0)
+      : "memory");
+}
+
+// Moves registers between the warpgroups of a CTA; executed by every warp of a warpgroup.
+template <int kRegs>
+__device__ __forceinline__ void set_max_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void set_max_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// acc[i] += s v[i] for G columns of one block, or += s c[i] v[i] with a scale for each column
+// (kColVec), which all lanes read from the same place in shared memory.
+template <int G, bool kColVec>
+__device__ __forceinline__ void fold(float* acc, const uint32_t (&v)[G], float s,
+                                     const float* c) {
+#pragma unroll
+  for (int i = 0; i < G; i += 4) {
+    if constexpr (kColVec) {
+      const float4 c4 = *reinterpret_cast<const float4*>(c + i);
+      acc[i] = fmaf(__uint_as_float(v[i]), s * c4.x, acc[i]);
+      acc[i + 1] = fmaf(__uint_as_float(v[i + 1]), s * c4.y, acc[i + 1]);
+      acc[i + 2] = fmaf(__uint_as_float(v[i + 2]), s * c4.z, acc[i + 2]);
+      acc[i + 3] = fmaf(__uint_as_float(v[i + 3]), s * c4.w, acc[i + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i + k] = fmaf(__uint_as_float(v[i + k]), s, acc[i + k]);
     }
   }
 }
@@ -188,41 +253,62 @@ __device__ __forceinline__ void store_one(const Params& p, int64_t at, float v) 
     static_cast<uint16_t*>(p.C)[at] = static_cast<uint16_t>(cvt_bf16x2(0.f, v));
 }
 
-// One thread's row of kNC columns, from column c0, in 32- or 16-byte stores (the number of
-// columns is a multiple of 8).
+// The warp's 32 rows x kNC columns of the tile, from column c0: each 64-byte column group is
+// written into the warp's staging box (16-byte chunks XOR-swizzled as the tensor map's 64-byte
+// swizzle expects) and sent with one TMA store, clipped at the matrix edge. A store of one
+// row per lane would touch 32 cache lines an instruction: with those, a tile's stores took
+// 2.5 us, a sixth of the tile at K = 4096.
 template <int kNC>
-__device__ __forceinline__ void store_row(const Params& p, const uint64_t (&acc)[kNC / 2],
-                                          int64_t row, int64_t c0) {
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, const Params& p,
+                                           const float (&acc)[kNC], uint8_t* box, int64_t row0,
+                                           int64_t c0, int lane) {
+  auto send = [&](const uint4 (&w)[4], int col) {
+    if (lane == 0) bulk_wait_read_all();  // the box is free again
+    __syncwarp();
 #pragma unroll
-  for (int g = 0; g < kNC / 8; ++g) {
-    const int64_t c = c0 + 8 * g;
-    if (c >= p.nc) return;
-    float f[8];
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(box + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) = w[j];
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, box, static_cast<int32_t>(c0 + col), static_cast<int32_t>(row0));
+      bulk_commit_group();
+    }
+  };
+  if (row0 >= p.nr) return;
+  if (p.out_fp32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack2(acc[4 * g + i], f[2 * i], f[2 * i + 1]);
-    if (p.out_fp32) {
-      float* o = static_cast<float*>(p.C) + row * p.ldo + c;
-      if (p.vec32) {
-        st_global_cg_v8(o, __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                        __float_as_uint(f[3]), __float_as_uint(f[4]), __float_as_uint(f[5]),
-                        __float_as_uint(f[6]), __float_as_uint(f[7]));
-      } else {
-        reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    for (int u = 0; u < kNC; u += 16) {
+      if (c0 + u >= p.nc) continue;
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = make_uint4(__float_as_uint(acc[u + 4 * j]), __float_as_uint(acc[u + 4 * j + 1]),
+                          __float_as_uint(acc[u + 4 * j + 2]),
+                          __float_as_uint(acc[u + 4 * j + 3]));
+      send(w, u);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kNC; u += 32) {
+      if (c0 + u >= p.nc) continue;
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float* a = &acc[u + 8 * j];
+        w[j] = make_uint4(cvt_bf16x2(a[1], a[0]), cvt_bf16x2(a[3], a[2]),
+                          cvt_bf16x2(a[5], a[4]), cvt_bf16x2(a[7], a[6]));
       }
-    } else {
-      uint16_t* o = static_cast<uint16_t*>(p.C) + row * p.ldo + c;
-      const uint4 w = make_uint4(cvt_bf16x2(f[1], f[0]), cvt_bf16x2(f[3], f[2]),
-                                 cvt_bf16x2(f[5], f[4]), cvt_bf16x2(f[7], f[6]));
-      *reinterpret_cast<uint4*>(o) = w;
+      send(w, u);
     }
   }
 }
 
 template <int BN, int kMode, bool kPair>
-__global__ void __launch_bounds__(kThreads, Cfg<BN, kPair>::kMinCtas)
+__global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, Cfg<BN, kPair>::kMinCtas)
 blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
-                      const __grid_constant__ CUtensorMap map_c, const Params p) {
+                      const __grid_constant__ CUtensorMap map_c,
+                      const __grid_constant__ CUtensorMap map_o, const Params p) {
   using C = Cfg<BN, kPair>;
   constexpr int kStages = C::kStages, kNC = C::kNC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -230,8 +316,10 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // pair: the leader's
   uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;   // [2]
-  uint64_t* acc_empty = acc_full + 2;     // [2]; pair: the leader's
+  uint64_t* sc_full = empty + kStages;
+  uint64_t* sc_free = sc_full + kScaleRing;
+  uint64_t* acc_full = sc_free + kScaleRing;  // [2]
+  uint64_t* acc_empty = acc_full + 2;         // [2]; pair: the leader's
   uint64_t* mma_done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -239,6 +327,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
   // single CTA writes both), [2] stage uses consumed by the MMA issuer (one accumulator
   // commit each), [3] this CTA's producer tail completed
   volatile uint32_t* rec = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 8);
+
+  float* scales = reinterpret_cast<float*>(smem + C::kOffScale);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = kPair ? cluster_ctarank() : 0;
@@ -251,14 +341,19 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
   const int kb1 = kPair ? p.nkb
                         : static_cast<int>(static_cast<int64_t>(p.nkb) * (part + 1) / p.split);
 
+  if (p.only_if && !any_word_set(p.only_if, p.num_only_if)) return;  // the whole cluster does
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kPair ? 2 * kEpiWarps : kEpiWarps);
+    for (int i = 0; i < kScaleRing; ++i) {
+      mbar_init(&sc_full[i], 32);
+      mbar_init(&sc_free[i], C::kFoldWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], (kPair ? 2 : 1) * C::kFoldWarps);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -266,6 +361,7 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     fence_barrier_init();
     tma_prefetch_desc(&map_r);
     tma_prefetch_desc(&map_c);
+    tma_prefetch_desc(&map_o);
   }
   if (warp == 1) {
     if constexpr (kPair) tmem_alloc_2sm(tmem_slot, C::kTmemCols);
@@ -279,7 +375,9 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
   grid_dependency_wait();
   grid_launch_dependents();
 
+  // each role sets its own register limit, inside its branch
   if (warp == 0) {
+    if constexpr (kPair) set_max_regs_dec<C::kOtherRegs>();
     // ------------------------------------------------------------- TMA producer
     const bool issuer = elect_one();
     const uint32_t full0 = kPair ? cluster_map(&full[0], 0) : smem_u32(&full[0]);
@@ -289,17 +387,17 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       int64_t rt, ct;
       tile_at(p, id, rt, ct);
       const int32_t r0 = static_cast<int32_t>(kPair ? (2 * rt + crank) * BM : rt * BM);
-      const int32_t c0 = static_cast<int32_t>(ct * BN + crank * C::kBRows);
+      const int32_t c0 = static_cast<int32_t>(ct * BN);
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-        if (!warp_wait(&empty[s], ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
+        if (!wait_phase(&empty[s], ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
         if (issuer) {
           uint8_t* as = smem + C::kOffA + s * C::kABytes;
           uint8_t* bs = smem + C::kOffB + s * C::kBBytes;
           if constexpr (kPair) {
             if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
             tma_load_2d_2sm(as, &map_r, kb * BK, r0, full0 + 8 * s);
-            tma_load_2d_2sm(bs, &map_c, kb * BK, c0, full0 + 8 * s);
+            tma_load_2d_2sm(bs, &map_c, kb * BK, c0 + crank * (BN / 2), full0 + 8 * s);
           } else {
             mbar_arrive_expect_tx(&full[s], C::kStageBytes);
             tma_load_2d(as, &map_r, kb * BK, r0, &full[s]);
@@ -324,10 +422,63 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     // the MMA issuer's release of the last stage uses must have arrived before the CTA exits
     bool tail_ok = ok;
     for (uint32_t i = it > kStages ? it - kStages : 0; tail_ok && i < it; ++i)
-      tail_ok = warp_wait(&empty[i % kStages], (i / kStages) & 1, abort_flag, p.wait_ns);
+      tail_ok = wait_phase(&empty[i % kStages], (i / kStages) & 1, abort_flag, p.wait_ns);
     if (issuer) rec[3] = tail_ok ? 1u : 0u;
     __syncwarp();
-  } else if (warp == 1 && leader) {
+  } else if (kMode != kFprop && warp == 2) {
+    if constexpr (kPair) set_max_regs_dec<C::kOtherRegs>();
+    // ------------------------------------------------------------- scales
+    // Up to kScaleRing blocks ahead of the fold, because a load from L2 takes longer than a
+    // block: the row scales (kSwapped: the row tile's one) and column scales (kFprop: one
+    // for each 128 columns) of a block, copied asynchronously. What lies past the matrix is
+    // left as it is: the products there are zero and their sums are not stored.
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t id = first_id; ok && id < p.tiles; id += id_step) {
+      int64_t rt, ct;
+      tile_at(p, id, rt, ct);
+      const int64_t r0 = (kPair ? 2 * rt + crank : rt) * BM, c0 = ct * BN;
+      const int rows = static_cast<int>(p.nr - r0 < BM ? p.nr - r0 : BM);
+      const int cols = static_cast<int>(p.nc - c0 < BN ? p.nc - c0 : BN);
+      const float* sr = kMode == kSwapped ? p.sr + rt * p.nkb + kb0
+                                          : p.sr + kb0 * p.ldr + r0 + lane;
+      const float* sc = kMode == kFprop ? p.sc + (c0 / 128 + lane) * p.nkb + kb0
+                                        : p.sc + kb0 * p.ldc + c0 + lane;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t n = it % kScaleRing, ph = (it / kScaleRing) & 1;
+        if (!wait_phase(&sc_free[n], ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
+        float* slot = scales + n * C::kScaleFloats;
+        if constexpr (kMode == kSwapped) {
+          if (lane == 0) cp_async4(slot, sr);
+          ++sr;
+        } else {
+#pragma unroll
+          for (int i = 0; i < BM; i += 32)
+            if (i + lane < rows) cp_async4(slot + i + lane, sr + i);
+          sr += p.ldr;
+        }
+        if constexpr (kMode == kFprop) {
+          if (128 * lane < cols) cp_async4(slot + BM + lane, sc);
+          ++sc;
+        } else {
+#pragma unroll
+          for (int i = 0; i < BN; i += 32)
+            if (i + lane < cols) cp_async4(slot + BM + i + lane, sc + i);
+          sc += p.ldc;
+        }
+        cp_async_arrive(&sc_full[n]);
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      latch_error(p.status, MXFP8_ERR_TIMEOUT);
+    }
+    cp_async_wait_all();
+    __syncwarp();
+  } else if (warp < kFoldFirst && !(warp == 1 && leader)) {
+    if constexpr (kPair) set_max_regs_dec<C::kOtherRegs>();
+  } else if (warp == 1) {
+    if constexpr (kPair) set_max_regs_dec<C::kOtherRegs>();
     // ------------------------------------------------------------- MMA issuer
     const bool issuer = elect_one();
     uint32_t it = 0;
@@ -339,11 +490,9 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1;
         const uint32_t b = it & 1, aph = (it >> 1) & 1;
-        if (!warp_wait(&acc_empty[b], aph ^ 1, abort_flag, p.wait_ns) ||
-            !warp_wait(&full[s], ph, abort_flag, p.wait_ns)) {
-          ok = false;
-          break;
-        }
+        ok = wait_phase(&full[s], ph, abort_flag, p.wait_ns) &&
+             wait_phase(&acc_empty[b], aph ^ 1, abort_flag, p.wait_ns);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t ad = a_desc0 + s * (C::kABytes / 16);
         const uint64_t bd = b_desc0 + s * (C::kBBytes / 16);
@@ -355,11 +504,11 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
             else mma_f8(d, ad + 2 * k, bd + 2 * k, kId, k > 0);
           }
           if constexpr (kPair) {
-            mma_commit_2sm_mc(&empty[s], 3);
             mma_commit_2sm_mc(&acc_full[b], 3);
+            mma_commit_2sm_mc(&empty[s], 3);
           } else {
-            mma_commit(&empty[s]);
             mma_commit(&acc_full[b]);
+            mma_commit(&empty[s]);
           }
         }
         __syncwarp();
@@ -381,75 +530,93 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       mbar_wait_timed(mma_done, 0, p.drain_ns);
     }
     __syncwarp();
-  } else if (warp >= 2) {
+  } else {
+    if constexpr (kPair) set_max_regs_inc<C::kFoldRegs>();
     // ------------------------------------------------------------- fold and store
-    const int q = warp & 3;            // TMEM lane quarter this warp may access
-    const int half = (warp - 2) >> 2;  // which half of the columns
-    float* cs = reinterpret_cast<float*>(smem + C::kOffScale) + (warp - 2) * kNC;
+    const int q = warp & 3;                   // TMEM lane quarter this warp may access
+    const int half = (warp - kFoldFirst) >> 2;  // which group of the columns
+    uint8_t* box = smem + C::kOffBox + (warp - kFoldFirst) * C::kBoxBytes;
     const uint32_t acc_empty0 = kPair ? cluster_map(&acc_empty[0], 0) : smem_u32(&acc_empty[0]);
     constexpr bool kColVec = kMode != kFprop;
-    constexpr int kPre = (kNC + 31) / 32;  // column scales prefetched per lane
+    constexpr int G = BN == 192 ? 32 : kNC < 64 ? kNC : 64;  // columns a TMEM read
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * kNC;
+    // kFprop: the scales of two blocks, and those of the next two under way
+    uint32_t ahead_id = first_id;
+    int ahead_kb = kb0;
+    const float *srp = nullptr, *scp = nullptr;
+    float nr[2], nc[2];
+    auto fetch = [&]() {
+      if (ahead_id >= p.tiles) return;
+      if (ahead_kb == kb0) {
+        int64_t rt, ct;
+        tile_at(p, ahead_id, rt, ct);
+        const int64_t row = (kPair ? 2 * rt + crank : rt) * BM + 32 * q + lane;
+        const int64_t col = ct * BN + half * kNC;
+        srp = p.sr + kb0 * p.ldr + (row < p.nr ? row : p.nr - 1);
+        scp = p.sc + (col < p.nc ? col : p.nc - 1) / 128 * p.nkb + kb0;
+      }
+      nr[0] = __ldg(srp);
+      nc[0] = __ldg(scp);
+      if (ahead_kb + 1 < kb1) {
+        nr[1] = __ldg(srp + p.ldr);
+        nc[1] = __ldg(scp + 1);
+      }
+      srp += 2 * p.ldr;
+      scp += 2;
+      ahead_kb += 2;
+      if (ahead_kb >= kb1) {
+        ahead_kb = kb0;
+        ahead_id += id_step;
+      }
+    };
+    if constexpr (!kColVec) fetch();
     uint32_t it = 0;
     bool ok = true;
     for (uint32_t id = first_id; ok && id < p.tiles; id += id_step) {
       int64_t rt, ct;
       tile_at(p, id, rt, ct);
-      const int64_t row0 = (kPair ? 2 * rt + crank : rt) * BM;
-      const int64_t row = row0 + 32 * q + lane;
+      const int64_t row0 = (kPair ? 2 * rt + crank : rt) * BM + 32 * q;
       const int64_t col = ct * BN + half * kNC;  // this warp's first column
-      uint64_t acc[kNC / 2];
+      const bool row_ok = row0 + lane < p.nr;
+      float acc[kNC];
 #pragma unroll
-      for (int i = 0; i < kNC / 2; ++i) acc[i] = 0;
-      // scales one block ahead: of this thread's row (or the row tile's block), and of the
-      // warp's columns (or their block)
-      const bool row_ok = row < p.nr;
-      const float* srp = kMode == kSwapped ? p.sr + rt * p.nkb : p.sr + (row_ok ? row : 0);
-      const int64_t srs = kMode == kSwapped ? 1 : p.ldr;
-      const float* scp = kColVec ? p.sc
-                                 : p.sc + ((col < p.nc ? col : p.nc - 1) / 128) * p.nkb;
-      float sr = 0.f, sc[kPre] = {};
-      auto prefetch = [&](int kb) {
-        sr = row_ok || kMode == kSwapped ? __ldg(srp + kb * srs) : 1.f;
-        if constexpr (kColVec) {
-#pragma unroll
-          for (int i = 0; i < kPre; ++i) {
-            const int64_t c = col + 32 * i + lane;
-            sc[i] = c < p.nc && 32 * i + lane < kNC ? __ldg(scp + kb * p.ldc + c) : 0.f;
-          }
-        } else {
-          sc[0] = __ldg(scp + kb);
-        }
-      };
-      if (kb0 < kb1) prefetch(kb0);
+      for (int i = 0; i < kNC; ++i) acc[i] = 0.f;
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t b = it & 1, ph = (it >> 1) & 1;
-        const float s = sr, s2 = sc[0];
+        const uint32_t n = it % kScaleRing, b = it & 1;
+        float s;
+        const float* cs = nullptr;
         if constexpr (kColVec) {
-#pragma unroll
-          for (int i = 0; i < kPre; ++i)
-            if (32 * i + lane < kNC) cs[32 * i + lane] = sc[i];
-          __syncwarp();
-        }
-        if (kb + 1 < kb1) prefetch(kb + 1);
-        int got = 0;  // one lane waits, the warp follows its verdict
-        if (lane == 0) got = mbar_wait_bounded(&acc_full[b], ph, abort_flag, p.wait_ns);
-        got = __shfl_sync(0xFFFFFFFFu, got, 0);
-        if (!got) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + b * BN + half * kNC;
-        const float both = kColVec ? s : s * s2;
-        if (__any_sync(0xFFFFFFFFu, extreme(both))) {
-          float h1, h2;
-          halves_of(s, h1, h2);
-          fold<kNC, kColVec, true>(acc, taddr, h1, h2, s2, cs);
+          ok = wait_phase(&sc_full[n], (it / kScaleRing) & 1, abort_flag, p.wait_ns);
+          const float* slot = scales + n * C::kScaleFloats;
+          s = kMode == kSwapped ? slot[0] : row_ok ? slot[32 * q + lane] : 1.f;
+          cs = slot + BM + half * kNC;
         } else {
-          fold<kNC, kColVec, false>(acc, taddr, both, 0.f, 0.f, cs);
+          if (((kb - kb0) & 1) == 0) {
+            s0 = nr[0] * nc[0];
+            s1 = nr[1] * nc[1];
+            fetch();
+          }
+          s = ((kb - kb0) & 1) ? s1 : s0;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (kPair) mbar_arrive_cluster_relaxed(acc_empty0 + 8 * b);
-          else mbar_arrive_relaxed(&acc_empty[b]);
+        ok = ok && wait_phase(&acc_full[b], (it >> 1) & 1, abort_flag, p.wait_ns);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int g = 0; g < kNC; g += G) {
+          uint32_t r[G];
+          tmem_ld(tbase + b * BN + g, r);
+          tmem_wait(r);
+          if (g + G == kNC) {  // the block has left TMEM
+            tc_fence_before();
+            arrive_if(lane == 0, acc_empty0 + 8 * b);
+          }
+          fold<G, kColVec>(acc + g, r, s, cs + g);
+        }
+        if constexpr (kColVec) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_relaxed(&sc_free[n]);
         }
       }
       if (!ok) break;
@@ -457,26 +624,21 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
         // partial sums into the (now idle) stages, [column][row]
         float* part_sum = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int i = 0; i < kNC / 2; ++i) {
-          float a, b2;
-          unpack2(acc[i], a, b2);
-          part_sum[(half * kNC + 2 * i) * BM + 32 * q + lane] = a;
-          part_sum[(half * kNC + 2 * i + 1) * BM + 32 * q + lane] = b2;
-        }
+        for (int i = 0; i < kNC; ++i)
+          part_sum[(half * kNC + i) * BM + 32 * q + lane] = acc[i];
       } else if constexpr (kMode == kSwapped) {
         if (row_ok) {
 #pragma unroll
-          for (int i = 0; i < kNC / 2; ++i) {
-            float a, b2;
-            unpack2(acc[i], a, b2);
-            if (col + 2 * i < p.nc) store_one(p, (col + 2 * i) * p.ldo + row, a);
-            if (col + 2 * i + 1 < p.nc) store_one(p, (col + 2 * i + 1) * p.ldo + row, b2);
-          }
+          for (int i = 0; i < kNC; ++i)
+            if (col + i < p.nc) store_one(p, (col + i) * p.ldo + row0 + lane, acc[i]);
         }
       } else {
-        if (row_ok) store_row<kNC>(p, acc, row, col);
+        store_tile<kNC>(&map_o, p, acc, box, row0, col, lane);
       }
     }
+    // its stores must have finished reading shared memory before the CTA exits
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
     if (!ok && lane == 0) {
       *abort_flag = 1;
       latch_error(p.status, MXFP8_ERR_TIMEOUT);
@@ -519,7 +681,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     const int c_lo = BN * static_cast<int>(part) / p.split;
     const int c_hi = BN * static_cast<int>(part + 1) / p.split;
     const uint32_t base = smem_u32(smem);
-    for (int i = c_lo * BM + static_cast<int>(threadIdx.x); i < c_hi * BM; i += kThreads) {
+    for (int i = c_lo * BM + static_cast<int>(threadIdx.x); i < c_hi * BM;
+         i += C::kThreads) {
       const int64_t row = rt * BM + i % BM, col = ct * BN + i / BM;
       if (row >= p.nr || col >= p.nc) continue;
       float sum = 0.f;
@@ -542,11 +705,74 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
   }
 }
 
+// ------------------------------------------------------- power-of-two scales (MXFP8 form)
+//
+// A power-of-two scale on a block of 128 is the same E8M0 scale on each of its four blocks of
+// 32, so operands quantized with power-of-two scales can run on the block-scaled MMA
+// (mxfp8_gemm), where the tensor cores apply the scales and nothing is folded. Whether all
+// scales are powers of two is known on the device only: this kernel writes the scales in the
+// MMA's 128 x 4 tile layout and, for each CTA, a word that says whether it met another one.
+// The block-scaled kernel then returns at once if any word is set, the folding one if none
+// is. Measured at 4096 x 24576 x 4096: 328 us folded; the two extra launches cost 4 us.
+constexpr int kConvertCtas = 608;  // four on each SM
+constexpr int kConvertThreads = 256;
+
+struct ConvertArgs {
+  const float* s[2];       // A's and B's scales
+  uint32_t* tiles[2];      // their tiles, 512 bytes each
+  int64_t rows[2];
+  int row_tiles[2];
+  bool two_d[2];           // [row tiles][nkb] instead of [nkb][rows]
+  int nkb;
+  uint32_t* other;         // [kConvertCtas]
+};
+
+__global__ void __launch_bounds__(kConvertThreads) convert_scales_kernel(const ConvertArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  bool other = false;
+  const int t = threadIdx.x & 127;  // row within a tile; two tiles at a time
+  constexpr int kUnroll = 4;
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const uint32_t row_tiles = static_cast<uint32_t>(a.row_tiles[o]);
+    const uint32_t tiles = row_tiles * static_cast<uint32_t>(a.nkb);
+    const uint32_t step = 2 * gridDim.x;
+    for (uint32_t i0 = 2 * blockIdx.x + (threadIdx.x >> 7); i0 < tiles; i0 += kUnroll * step) {
+      uint32_t bits[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t i = i0 + u * step, kb = i / row_tiles, rt = i - kb * row_tiles;
+        const int64_t row = static_cast<int64_t>(rt) * BM + t;
+        bits[u] = i < tiles && row < a.rows[o]
+                      ? __float_as_uint(a.two_d[o] ? a.s[o][static_cast<int64_t>(rt) * a.nkb + kb]
+                                                   : a.s[o][kb * a.rows[o] + row])
+                      : 0x3F800000u;
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t i = i0 + u * step, kb = i / row_tiles, rt = i - kb * row_tiles;
+        if (i >= tiles) continue;
+        const uint32_t e = bits[u] >> 23;  // the sign too: a negative scale is another one
+        uint32_t byte = e & 0xFFu;
+        if ((bits[u] & 0x7FFFFFFFu) > 0x7F800000u) byte = 0xFFu;                 // NaN
+        else if (bits[u] != 0x00400000u /* 2^-127 */ &&
+                 ((bits[u] & 0x7FFFFFu) != 0 || e == 0 || e > 254)) other = true;
+        // scale (r, k) of a tile at byte (r % 32) * 16 + (r / 32) * 4 + k
+        a.tiles[o][(static_cast<int64_t>(rt) * a.nkb + kb) * 128 + (t & 31) * 4 + (t >> 5)] =
+            byte * 0x01010101u;
+      }
+    }
+  }
+  const int any = __syncthreads_or(other);
+  if (threadIdx.x == 0) a.other[blockIdx.x] = any ? 1u : 0u;
+}
+
 // ------------------------------------------------------------------------- host side
 
 template <int BN, int kMode, bool kPair>
-int launch(const CUtensorMap& mr, const CUtensorMap& mc, const Params& p, int64_t grid,
-           int cluster, cudaStream_t stream) {
+int launch(const CUtensorMap& mr, const CUtensorMap& mc, const CUtensorMap& mo, const Params& p,
+           int64_t grid, int cluster, cudaStream_t stream) {
   auto k = blockwise_gemm_kernel<BN, kMode, kPair>;
   constexpr int kSmem = Cfg<BN, kPair>::kSmemBytes;
   static std::atomic<bool> attr_set[64] = {};  // per device; setting it twice is harmless
@@ -560,7 +786,7 @@ int launch(const CUtensorMap& mr, const CUtensorMap& mc, const Params& p, int64_
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(Cfg<BN, kPair>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -573,34 +799,39 @@ int launch(const CUtensorMap& mr, const CUtensorMap& mc, const Params& p, int64_
     attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
   }
-  return cudaLaunchKernelEx(&cfg, k, mr, mc, p) == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k, mr, mc, mo, p) == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
 }
 
-// 256 x 256 tiles on CTA pairs. `a` is the row operand.
-template <int kMode>
+// 256 x BN tiles on CTA pairs. `a` is the row operand.
+template <int BN, int kMode>
 int launch_pairs(const BlockwiseGemmArgs& a, Params p, cudaStream_t stream) {
-  using C = Cfg<256, true>;
-  CUtensorMap mr, mc;
-  if (!make_operand_map(&mr, a.A, a.K, a.M, BM) || !make_operand_map(&mc, a.B, a.K, a.N, C::kBRows))
+  using C = Cfg<BN, true>;
+  CUtensorMap mr, mc, mo;
+  if (!make_operand_map(&mr, a.A, a.K, a.M, BM) ||
+      !make_operand_map(&mc, a.B, a.K, a.N, C::kBRows) ||
+      !make_store_map(&mo, a.C, a.M, a.N, a.out_fp32))
     return MXFP8_ERR_CUDA;
   p.row_tiles = static_cast<uint32_t>((a.M + 255) / 256);
-  p.col_tiles = static_cast<uint32_t>((a.N + 255) / 256);
+  p.col_tiles = static_cast<uint32_t>((a.N + BN - 1) / BN);
   const int64_t tiles = static_cast<int64_t>(p.row_tiles) * p.col_tiles;
   if (tiles > 0x7FFFFFFF / 2) return MXFP8_ERR_INVALID_ARG;
   p.tiles = static_cast<uint32_t>(tiles);
   p.band = p.row_tiles < 8 ? p.row_tiles : 8;
   p.split = 1;
   const int64_t pairs = num_sms() / 2;
-  return launch<256, kMode, true>(mr, mc, p, 2 * (tiles < pairs ? tiles : pairs), 2, stream);
+  return launch<BN, kMode, true>(mr, mc, mo, p, 2 * (tiles < pairs ? tiles : pairs), 2, stream);
 }
 
 // 128 x BN tiles on single CTAs, the reduction split over clusters of `split`.
 template <int BN, int kMode>
 int launch_single(const void* R, int64_t nr, const void* Cop, int64_t nc, int64_t K, Params p,
                   int split, cudaStream_t stream) {
-  CUtensorMap mr, mc;
+  CUtensorMap mr, mc, mo;
   if (!make_operand_map(&mr, R, K, nr, BM) || !make_operand_map(&mc, Cop, K, nc, BN))
     return MXFP8_ERR_CUDA;
+  // swapped tiles are stored transposed, without a map
+  if (kMode == kSwapped) mo = mr;
+  else if (!make_store_map(&mo, p.C, nr, nc, p.out_fp32 != 0)) return MXFP8_ERR_CUDA;
   p.row_tiles = static_cast<uint32_t>((nr + BM - 1) / BM);
   p.col_tiles = static_cast<uint32_t>((nc + BN - 1) / BN);
   const int64_t tiles = static_cast<int64_t>(p.row_tiles) * p.col_tiles;
@@ -611,7 +842,7 @@ int launch_single(const void* R, int64_t nr, const void* Cop, int64_t nc, int64_
   int64_t grid = tiles * split;
   const int64_t fit = static_cast<int64_t>(num_sms()) * Cfg<BN, false>::kMinCtas;
   if (split == 1 && grid > fit) grid = fit;  // persistent
-  return launch<BN, kMode, false>(mr, mc, p, grid, split, stream);
+  return launch<BN, kMode, false>(mr, mc, mo, p, grid, split, stream);
 }
 
 // Parts of the reduction: enough to give every SM a CTA, at least 4 blocks each.
@@ -621,7 +852,19 @@ int split_for(int64_t tiles, int64_t nkb) {
   return s;
 }
 
+// From this many operations on, the gain of the block-scaled MMA for power-of-two scales
+// (a fifth to a quarter of the time) is worth what the conversion and the check cost others.
+constexpr double kMxMinFlops = 1e11;
+
 }  // namespace
+
+int64_t blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool out_fp32) {
+  // FP32 results keep the FP32 sum over the blocks: the tensor cores' own accumulation over
+  // all of K measured 2e-6 off (K = 4096), which a BF16 result's rounding (2e-3) covers
+  if (out_fp32 || M <= 128 || N <= 128 || 2.0 * M * N * K < kMxMinFlops) return 0;
+  const int64_t nkb = (K + BK - 1) / BK;
+  return ((M + 127) / 128 + (N + 127) / 128) * nkb * 512 + kConvertCtas * 4;
+}
 
 int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
   Params p{};
@@ -629,7 +872,6 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
   p.ldo = a.N;
   p.nkb = static_cast<int>((a.K + BK - 1) / BK);
   p.out_fp32 = a.out_fp32 ? 1 : 0;
-  p.vec32 = (reinterpret_cast<uintptr_t>(a.C) & 31u) == 0 && (a.N * 4) % 32 == 0;
   p.status = a.status;
   p.wait_ns = pipeline_wait_ns();
   p.drain_ns = pipeline_drain_ns();
@@ -652,9 +894,43 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
   p.ldc = a.N;
   p.nr = a.M;
   p.nc = a.N;
+  const int64_t need = a.workspace ? blockwise_gemm_workspace_bytes(a.M, a.N, a.K, a.out_fp32) : 0;
+  if (need > 0 && a.workspace_bytes >= static_cast<size_t>(need)) {
+    const int64_t rta = (a.M + 127) / 128, rtb = (a.N + 127) / 128;
+    if ((rta + rtb) * p.nkb > 0x7FFFFFFF) return MXFP8_ERR_INVALID_ARG;  // 32-bit tile index
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    ConvertArgs c{};
+    c.s[0] = a.sA;
+    c.s[1] = a.sB;
+    c.tiles[0] = reinterpret_cast<uint32_t*>(ws);
+    c.tiles[1] = c.tiles[0] + rta * p.nkb * 128;
+    c.rows[0] = a.M;
+    c.rows[1] = a.N;
+    c.row_tiles[0] = static_cast<int>(rta);
+    c.row_tiles[1] = static_cast<int>(rtb);
+    c.two_d[1] = !a.wgrad;
+    c.nkb = p.nkb;
+    c.other = c.tiles[1] + rtb * p.nkb * 128;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kConvertCtas, 1, 1);
+    cfg.blockDim = dim3(kConvertThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_attr(&attr[0]);
+    if (cudaLaunchKernelEx(&cfg, convert_scales_kernel, c) != cudaSuccess) return MXFP8_ERR_CUDA;
+    GemmArgs g{a.A, c.tiles[0], a.B, c.tiles[1], a.C, a.M, a.N, a.K, MXFP8_OP_FPROP,
+               MXFP8_OUT_BF16, nullptr, 0, 0, a.status};
+    g.unless = c.other;
+    g.num_unless = kConvertCtas;
+    const int st = launch_gemm(g, stream);
+    if (st != MXFP8_OK) return st;
+    p.only_if = c.other;
+    p.num_only_if = kConvertCtas;
+  }
   const int64_t pair_tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256);
   if (pair_tiles >= num_sms() / 4)
-    return a.wgrad ? launch_pairs<kWgrad>(a, p, stream) : launch_pairs<kFprop>(a, p, stream);
+    return a.wgrad ? launch_pairs<192, kWgrad>(a, p, stream) : launch_pairs<256, kFprop>(a, p, stream);
   const int split = split_for(((a.M + 127) / 128) * ((a.N + 127) / 128), p.nkb);
   return a.wgrad ? launch_single<128, kWgrad>(a.A, a.M, a.B, a.N, a.K, p, split, stream)
                  : launch_single<128, kFprop>(a.A, a.M, a.B, a.N, a.K, p, split, stream);

@@ -89,6 +89,15 @@ __device__ __forceinline__ bool flag_wait_bounded(const uint32_t* flag, uint32_t
   }
 }
 
+// Whether any of `n` words is set, for every thread of the CTA (called by all of them, before
+// any other global access: it waits for the previous kernel, which wrote the words).
+__device__ __forceinline__ bool any_word_set(const uint32_t* words, int n) {
+  grid_dependency_wait();
+  uint32_t w = 0;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) w |= __ldcg(words + i);
+  return __syncthreads_or(w != 0) != 0;
+}
+
 // ------------------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {

@@ -114,6 +114,9 @@ struct Params {
   uint4* ws = nullptr;           // split-K: FP32 partials of pieces 0 .. kSplitK - 2
   uint32_t* ws_flags = nullptr;  // split-K: one arrival counter per (tile, CTA rank, epilogue
                                  // warp); zero between launches
+  // dense: the kernel returns at once if any of these words is set
+  const uint32_t* unless = nullptr;
+  int num_unless = 0;
 };
 
 // Everything a role needs to know about one output tile.
@@ -291,6 +294,9 @@ mxfp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  if constexpr (kMode == kDense) {
+    if (p.unless && any_word_set(p.unless, p.num_unless)) return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -886,6 +892,9 @@ mxfp8_gemm_2sm_kernel(const __grid_constant__ CUtensorMap map_a,
   const int64_t id_step = gridDim.x >> 1;
   DuoSeg* seg = D::kGrouped ? reinterpret_cast<DuoSeg*>(smem + D::kOffSeg) : nullptr;
 
+  if constexpr (kMode == kDense) {  // both CTAs of the pair read the same words
+    if (p.unless && any_word_set(p.unless, p.num_unless)) return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -1872,6 +1881,10 @@ bool make_operand_map(CUtensorMap* map, const void* base, uint64_t inner, uint64
   return make_map(map, base, 2, inner, outer, 1, BK, box_outer);
 }
 
+bool make_store_map(CUtensorMap* map, void* base, int64_t rows, int64_t N, bool fp32) {
+  return make_out_map(map, base, rows, N, 1, fp32, 2);
+}
+
 uint64_t pipeline_wait_ns() { return wait_limit_ns(); }
 uint64_t pipeline_drain_ns() { return drain_limit_ns(wait_limit_ns()); }
 
@@ -1899,6 +1912,8 @@ int launch_gemm(const GemmArgs& a, cudaStream_t stream) {
   p.status = a.status;
   p.wait_ns = wait_limit_ns();
   p.drain_ns = drain_limit_ns(p.wait_ns);
+  p.unless = a.unless;
+  p.num_unless = a.num_unless;
   const bool wide = a.N > 128;
   const int bn = wide ? 256 : 128;
   p.num_m_tiles = static_cast<int>((a.M + BM - 1) / BM);

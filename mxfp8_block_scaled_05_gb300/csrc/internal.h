@@ -87,6 +87,9 @@ struct GemmArgs {
   // dense call: caller-owned workspace for a split-K last wave (nullptr: none)
   void* workspace = nullptr;
   size_t workspace_bytes = 0;
+  // dense call: run only if none of these device words is set (nullptr: always)
+  const uint32_t* unless = nullptr;
+  int num_unless = 0;
 };
 
 // Returns MXFP8_OK or an mxfp8_status code.
@@ -106,15 +109,23 @@ struct BlockwiseGemmArgs {
   int64_t M, N, K;
   bool wgrad, out_fp32;
   int* status;
+  void* workspace;   // blockwise_gemm_workspace_bytes(...) bytes, or nullptr
+  size_t workspace_bytes;
 };
 
 // Returns MXFP8_OK or an mxfp8_status code.
 int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream);
+// Workspace with which power-of-two scales run on the block-scaled MMA (0: never).
+int64_t blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool out_fp32);
 
 // Tensor map of a row-major byte matrix [outer][inner] in 128-byte x box_outer boxes with
 // the 128-byte swizzle.
 bool make_operand_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                       uint32_t box_outer);
+
+// Tensor map of a row-major output [rows][N] for stores of 32-row x 64-byte boxes with the
+// 64-byte swizzle.
+bool make_store_map(CUtensorMap* map, void* base, int64_t rows, int64_t N, bool fp32);
 
 // Limits of pipeline waits, and of waits for work in flight on the way out of a kernel.
 uint64_t pipeline_wait_ns();
