@@ -29,8 +29,7 @@
 namespace mxfp8 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 256;  // of the gradient kernel, and the most of the forward one
 constexpr int kMaxSplit = 8;   // CTAs of a cluster that share one row (the portable limit)
 constexpr int kMaxTop = 32;    // alternatives: one per lane of a warp's list
 constexpr float kLowest = -256.f;  // 2^t is 0 from here on
@@ -126,8 +125,9 @@ struct Softmax {
     m = sub = to;
   }
 
+  // adds kN values; returns their maximum
   template <int kN>
-  __device__ __forceinline__ void add(const float (&x)[kN], float c) {
+  __device__ __forceinline__ float add(const float (&x)[kN], float c) {
     float top = x[0];
 #pragma unroll
     for (int i = 1; i < kN; ++i) top = fmaxf(top, x[i]);
@@ -149,6 +149,7 @@ struct Softmax {
     s = a + b;
     unpack2(e2, a, b);
     e = a + b;
+    return top;
   }
 
   __device__ __forceinline__ void join(float om, float os, float oe, float c) {
@@ -200,30 +201,36 @@ struct WarpTop {
   }
 };
 
+constexpr int kMaxCandidates = 512;
+
+template <int kThreads>
 struct Shared {
-  float part[kWarps][3];
-  float cta[3];                     // this CTA's m, S, E (read by the cluster's first CTA)
+  static constexpr int kWarps = kThreads / 32;
+  float part[kWarps][3];            // the warps' m, S, E
+  float parts[kMaxSplit][3];        // first CTA of a cluster: the CTAs' m, S, E
   float row[2];                     // the row's maximum and log S
-  alignas(16) float thread_max[kThreads];  // read four at a time
-  int chosen[kThreads];             // threads whose values may hold alternatives
-  int num_chosen;
-  uint32_t bar;                     // order of the smallest chosen thread maximum
-  uint64_t keys[kMaxSplit * kMaxTop];
-  uint64_t top[kMaxTop];            // this CTA's k best keys
+  uint32_t warp_bar[kWarps];        // order of each warp's j-th largest thread maximum
+  int chosen[kThreads];             // threads whose largest value reaches the bar
+  int reread[kThreads];             // and of those, the ones whose second vector does too
+  int num_chosen, num_reread, num_candidates;
+  uint64_t keys[kMaxCandidates];    // candidates; then lists to be merged
+  uint64_t lists[kMaxSplit * kMaxTop];  // first CTA of a cluster: the CTAs' best keys
+  uint64_t top[kMaxTop];            // the best keys, in order
 };
 
-// Keys [0, n) in sh.keys: the k largest, in order, into `out` (kNoKey where fewer exist).
+// The k largest of keys [0, n), in order, into `out` (kNoKey where fewer exist). Keys are
+// distinct but for kNoKey. Called by the whole CTA; `out` is ready after the next barrier.
+template <int kThreads>
 __device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int k, uint64_t* out,
                                           int tid) {
-  if (tid < k) out[tid] = kNoKey;
+  for (int t = tid; t < k; t += kThreads) out[t] = kNoKey;
   __syncthreads();
-  if (tid < n) {
-    const uint64_t mine = keys[tid];
+  for (int t = tid; t < n; t += kThreads) {
+    const uint64_t mine = keys[t];
     int above = 0;
     for (int i = 0; i < n; ++i) above += keys[i] > mine;
     if (mine > kNoKey && above < k) out[above] = mine;
   }
-  __syncthreads();
 }
 
 struct Params {
@@ -240,21 +247,151 @@ struct Params {
   int* status;
 };
 
+// What the stream keeps for the alternatives, of a thread's vectors: the largest value and
+// which vector holds it, and the largest value of the other vectors.
+struct Best {
+  float top = -kInf, second = -kInf;
+  uint32_t at = 0;  // relative to the CTA's first vector
+
+  __device__ __forceinline__ void add(float x, uint32_t v) {
+    second = fmaxf(second, fminf(x, top));
+    at = x > top ? v : at;
+    top = fmaxf(top, x);
+  }
+};
+
+// The CTA's k best keys into sh.top, from what its threads kept of their vectors (v0 + tid + i
+// kThreads) and from its single values.
+//
+// A bar that at least k of the threads' largest values reach bounds the k-th best value from
+// below, so the values that reach it are all there is to look at. The bar is the smallest,
+// over the warps with values in every lane, of the warp's j-th largest maximum, with j such
+// that those are k values in all: for k = 8 about 20 values of a row reach it. Most are alone
+// in their thread, which reads the vector that holds it once more. Only a thread whose second
+// vector reaches the bar too has all its vectors read again. (Reading all vectors of every
+// thread that reaches the bar took 46% longer at 4096 x 131072: 32-byte pieces 4 KB apart.)
+// What reaches the bar is listed, and ranked by counting; where it is more than the list holds
+// (many equal values), sorted lists kept by the warps take over.
+template <int kThreads, typename T>
+__device__ __forceinline__ void find_top(Shared<kThreads>& sh, const T* row, const RowShape& shape,
+                                         int64_t v0, int64_t v1, bool first, bool last,
+                                         const Best& kept, int k) {
+  constexpr int kN = Vec<T>::kN, kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint4* body = reinterpret_cast<const uint4*>(row + shape.head);
+  const int64_t tail0 = shape.head + shape.nv * kN;
+  constexpr uint32_t kNone = static_cast<uint32_t>(kNoKey >> 32);  // order of -inf
+  const uint32_t own = order_of(kept.top);
+  const int64_t full = (v1 - v0) / 32;  // warps with a vector in every lane
+  const int warps = static_cast<int>(full < kWarps ? full : kWarps);
+  uint32_t bar_order = kNone + 1;
+  if (warps > 0 && 32 * warps >= k) {
+    const int j = (k + warps - 1) / warps;
+    uint32_t v = own, best = 0;
+    for (int i = 0; i < j; ++i) {
+      best = __reduce_max_sync(0xFFFFFFFFu, v);
+      const int at = __ffs(__ballot_sync(0xFFFFFFFFu, v == best)) - 1;
+      if (lane == at) v = 0;
+    }
+    if (lane == 0) sh.warp_bar[warp] = best;
+  }
+  if (tid == 0) sh.num_chosen = sh.num_reread = sh.num_candidates = 0;
+  __syncthreads();
+  if (warps > 0 && 32 * warps >= k) {
+    uint32_t least = 0xFFFFFFFFu;
+    for (int w = 0; w < warps; ++w) least = min(least, sh.warp_bar[w]);
+    bar_order = max(least, kNone + 1);
+  }
+  const float bar = value_of(static_cast<uint64_t>(bar_order) << 32);
+  auto list = [&](float x, int64_t place) {
+    if (!(x >= bar)) return;
+    const int at = atomicAdd(&sh.num_candidates, 1);
+    if (at < kMaxCandidates) sh.keys[at] = key_of(x, static_cast<uint32_t>(place));
+  };
+  auto list_vector = [&](const uint4& w, int64_t v) {
+    float x[kN];
+    Vec<T>::unpack(w, x);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) list(x[i], shape.head + v * kN + i);
+  };
+  if (own >= bar_order) {
+    sh.chosen[atomicAdd(&sh.num_chosen, 1)] = tid;
+    if (order_of(kept.second) >= bar_order) sh.reread[atomicAdd(&sh.num_reread, 1)] = tid;
+    else list_vector(__ldg(body + v0 + kept.at), v0 + kept.at);
+  }
+  const bool has_head = first && tid < shape.head, has_tail = last && tid < shape.tail;
+  if (has_head) list(Vec<T>::load(row + tid), tid);
+  if (has_tail) list(Vec<T>::load(row + tail0 + tid), tail0 + tid);
+  __syncthreads();
+  const int steps = static_cast<int>((v1 - v0 + kThreads - 1) / kThreads);
+  const int runs = (steps + 31) / 32;  // of 32 vectors, one a lane, for each thread
+  const int all = sh.num_reread * runs;
+  for (int g = warp; g < all; g += kWarps) {
+    const int c = g / runs;
+    const int64_t v = v0 + sh.reread[c] + static_cast<int64_t>((g - c * runs) * 32 + lane) * kThreads;
+    if (v < v1) list_vector(__ldg(body + v), v);
+  }
+  __syncthreads();
+  int listed = sh.num_candidates;
+  if (listed > kMaxCandidates) {
+    __syncthreads();
+    const int n = sh.num_chosen;
+    WarpTop best;
+    best.least = bar_order > kNone + 1 ? (static_cast<uint64_t>(bar_order) << 32) - 1 : kNoKey;
+    for (int q = warp; q < n; q += kWarps) {
+      const int owner = sh.chosen[q];
+      for (int r = 0; r < runs; ++r) {
+        const int64_t v = v0 + owner + static_cast<int64_t>(r * 32 + lane) * kThreads;
+        const bool live = v < v1;
+        float x[kN];
+        Vec<T>::unpack(live ? __ldg(body + v) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll 1
+        for (int i = 0; i < kN; ++i) {
+          float xi = x[0];
+#pragma unroll
+          for (int e = 1; e < kN; ++e) xi = e == i ? x[e] : xi;
+          best.offer(live ? key_of(xi, static_cast<uint32_t>(shape.head + v * kN + i)) : kNoKey,
+                     k, lane);
+        }
+      }
+    }
+    if (warp == 0) {  // the single values, fewer than 8 on either side
+      uint64_t key = kNoKey;
+      if (has_head) key = key_of(Vec<T>::load(row + lane), static_cast<uint32_t>(lane));
+      best.offer(key, k, lane);
+      key = kNoKey;
+      if (has_tail) key = key_of(Vec<T>::load(row + tail0 + lane), static_cast<uint32_t>(tail0 + lane));
+      best.offer(key, k, lane);
+    }
+    sh.keys[warp * kMaxTop + lane] = lane < k ? best.mine : kNoKey;
+    listed = kWarps * kMaxTop;
+    __syncthreads();
+  }
+  rank_keys<kThreads>(sh.keys, listed, k, sh.top, tid);
+  __syncthreads();
+}
+
+// Halves of a cluster barrier: every thread of every CTA of the cluster does both.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // One cluster of `split` CTAs per row; each CTA streams a contiguous part of it once.
 //
-// Bound by memory (2 or 4 bytes a logit). The alternatives do not slow the stream down: it
-// only keeps each thread's maximum, which the softmax needs anyway. A value among the k
-// largest sits in a thread whose maximum is among the k largest thread maxima, so only
-// those threads' values, k / 256 of the row, are read again (from L2) and sorted into
-// per-warp lists. Rows are split over a cluster only when there are too few of them to
-// fill the GPU; the parts are joined through distributed shared memory, without a
-// workspace.
-template <typename T>
+// Bound by memory (2 or 4 bytes a logit): 16-byte loads, eight of them in flight a thread.
+// Rows are split over a cluster only when there are too few of them to fill the GPU; each
+// CTA then hands its sums and best keys to the first through distributed shared memory,
+// without a workspace.
+template <typename T, bool kTop, int kThreads>
 __global__ void __launch_bounds__(kThreads)
 logprob_kernel(const Params p, int split) {
-  constexpr int kN = Vec<T>::kN;
+  constexpr int kN = Vec<T>::kN, kWarps = kThreads / 32;
   constexpr int kUnroll = 4;
-  __shared__ Shared sh;
+  __shared__ Shared<kThreads> sh;
+  if (split > 1) cluster_arrive();  // this CTA has started: its shared memory may be written
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -264,12 +401,20 @@ logprob_kernel(const Params p, int split) {
   const RowShape shape = row_shape(row, p.vocab);
   const int64_t v0 = shape.nv * rank / split, v1 = shape.nv * (rank + 1) / split;
   const uint4* body = reinterpret_cast<const uint4*>(row + shape.head);
-  const bool has_head = rank == 0 && tid < shape.head;
-  const bool has_tail = rank == split - 1 && tid < shape.tail;
+  const bool first = rank == 0, last = rank == split - 1;
+  const bool has_head = first && tid < shape.head, has_tail = last && tid < shape.tail;
   const int64_t tail0 = shape.head + shape.nv * kN;
   const float c = p.inv_t * kLog2e;
+  // thread 0 of the first CTA will need the target's logit
+  int64_t target = 0;
+  float target_logit = 0.f;
+  if (first && tid == 0) {
+    target = p.targets[row_id];
+    if (target >= 0 && target < p.vocab) target_logit = Vec<T>::load(row + target);
+  }
 
   Softmax sm;
+  Best kept;
   int64_t v = v0 + tid;
   for (; v + (kUnroll - 1) * kThreads < v1; v += kUnroll * kThreads) {
     uint4 w[kUnroll];
@@ -279,13 +424,15 @@ logprob_kernel(const Params p, int split) {
     for (int u = 0; u < kUnroll; ++u) {
       float x[kN];
       Vec<T>::unpack(w[u], x);
-      sm.add(x, c);
+      const float top = sm.add(x, c);
+      if constexpr (kTop) kept.add(top, static_cast<uint32_t>(v - v0) + u * kThreads);
     }
   }
   for (; v < v1; v += kThreads) {
     float x[kN];
     Vec<T>::unpack(ld_nc_v4(body + v), x);
-    sm.add(x, c);
+    const float top = sm.add(x, c);
+    if constexpr (kTop) kept.add(top, static_cast<uint32_t>(v - v0));
   }
   if (has_head || has_tail) {
     const float x[2] = {has_head ? Vec<T>::load(row + tid) : -kInf,
@@ -293,135 +440,85 @@ logprob_kernel(const Params p, int split) {
     sm.add(x, c);
   }
   const float own_max = sm.m;
-
   // join the CTA's threads
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float om = __shfl_xor_sync(0xFFFFFFFFu, sm.m, o);
-    const float os = __shfl_xor_sync(0xFFFFFFFFu, sm.s, o);
-    const float oe = __shfl_xor_sync(0xFFFFFFFFu, sm.e, o);
-    sm.join(om, os, oe, c);
-  }
+  auto join_lanes = [&](int lanes) {
+    for (int o = lanes / 2; o > 0; o >>= 1) {
+      const float om = __shfl_xor_sync(0xFFFFFFFFu, sm.m, o);
+      const float os = __shfl_xor_sync(0xFFFFFFFFu, sm.s, o);
+      const float oe = __shfl_xor_sync(0xFFFFFFFFu, sm.e, o);
+      sm.join(om, os, oe, c);
+    }
+  };
+  join_lanes(32);
   if (lane == 0) {
     sh.part[warp][0] = sm.m;
     sh.part[warp][1] = sm.s;
     sh.part[warp][2] = sm.e;
   }
-  sh.thread_max[tid] = own_max;
-  if (tid == 0) {
-    sh.num_chosen = 0;
-    sh.bar = 0xFFFFFFFFu;
-  }
   __syncthreads();
-  if (tid == 0) {
-    Softmax all;
-    for (int w = 0; w < kWarps; ++w) all.join(sh.part[w][0], sh.part[w][1], sh.part[w][2], c);
-    sh.cta[0] = all.m;
-    sh.cta[1] = all.s;
-    sh.cta[2] = all.e;
+  if (warp == 0) {
+    sm.m = sh.part[lane % kWarps][0];
+    sm.s = sh.part[lane % kWarps][1];
+    sm.e = sh.part[lane % kWarps][2];
+    sm.sub = sm.m == -kInf ? 0.f : sm.m;
+    join_lanes(kWarps);
   }
-
-  if (p.top > 0) {
-    // threads with fewer than k larger thread maxima
-    int above = 0;
-    for (int i = 0; i < kThreads; i += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(&sh.thread_max[i]);
-      above += (o.x > own_max) + (o.y > own_max) + (o.z > own_max) + (o.w > own_max);
-    }
-    if (above < p.top && own_max > -kInf) {
-      sh.chosen[atomicAdd(&sh.num_chosen, 1)] = tid;
-      atomicMin(&sh.bar, order_of(own_max));
-    }
-    __syncthreads();
-    WarpTop best;
-    const int n = sh.num_chosen;
-    // k chosen maxima bound the k-th best key from below; fewer do not
-    best.least = n >= p.top ? (static_cast<uint64_t>(sh.bar) << 32) - 1 : kNoKey;
-    const int64_t steps = (v1 - v0 + kThreads - 1) / kThreads;
-    for (int q = warp; q < n; q += kWarps) {
-      const int owner = sh.chosen[q];
-      for (int64_t j0 = 0; j0 < steps; j0 += 32) {
-        const int64_t at = v0 + owner + (j0 + lane) * kThreads;
-        const bool live = at < v1;
-        float x[kN];
-        Vec<T>::unpack(live ? __ldg(body + at) : make_uint4(0, 0, 0, 0), x);
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-          best.offer(live ? key_of(x[i], static_cast<uint32_t>(shape.head + at * kN + i)) : kNoKey,
-                     p.top, lane);
-      }
-      // the owner's single values
-      uint64_t key = kNoKey;
-      if (lane == 0 && rank == 0 && owner < shape.head)
-        key = key_of(Vec<T>::load(row + owner), static_cast<uint32_t>(owner));
-      if (lane == 1 && rank == split - 1 && owner < shape.tail)
-        key = key_of(Vec<T>::load(row + tail0 + owner), static_cast<uint32_t>(tail0 + owner));
-      best.offer(key, p.top, lane);
-    }
-    sh.keys[warp * kMaxTop + lane] = lane < p.top ? best.mine : kNoKey;
-    __syncthreads();
-    rank_keys(sh.keys, kWarps * kMaxTop, p.top, sh.top, tid);
-  } else {
-    __syncthreads();
-  }
+  if constexpr (kTop) find_top(sh, row, shape, v0, v1, first, last, kept, p.top);
 
   // join the cluster's CTAs in its first
   if (split > 1) {
-    cluster_sync();
-    if (rank == 0) {
-      if (p.top > 0) {
-        const int r = tid / kMaxTop, i = tid % kMaxTop;
-        uint64_t key = kNoKey;
-        if (r < split && i < p.top) {
-          const uint32_t from = cluster_map(&sh.top[i], static_cast<uint32_t>(r));
-          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(from) : "memory");
-        }
-        sh.keys[tid] = key;
-      }
-      if (tid == 0) {
-        Softmax all;
-        for (int r = 0; r < split; ++r) {
-          float o[3];
-          for (int i = 0; i < 3; ++i) {
-            const uint32_t from = cluster_map(&sh.cta[i], static_cast<uint32_t>(r));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o[i]) : "r"(from) : "memory");
-          }
-          all.join(o[0], o[1], o[2], c);
-        }
-        sh.part[0][0] = all.m;
-        sh.part[0][1] = all.s;
-        sh.part[0][2] = all.e;
+    cluster_wait();
+    const uint32_t dst = 0;
+    if (tid == 0) {
+      const float o[3] = {sm.m, sm.s, sm.e};
+      for (int i = 0; i < 3; ++i)
+        st_cluster_u32(cluster_map(&sh.parts[rank][i], dst), __float_as_uint(o[i]));
+    }
+    if constexpr (kTop) {
+      if (tid < p.top) {
+        const uint64_t key = sh.top[tid];
+        const uint32_t to = cluster_map(&sh.lists[rank * p.top + tid], dst);
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(key) : "memory");
       }
     }
-    cluster_sync();  // no CTA leaves while its shared memory is being read
+    cluster_arrive();
+    cluster_wait();
     if (rank != 0) return;
-    if (tid == 0)
-      for (int i = 0; i < 3; ++i) sh.cta[i] = sh.part[0][i];
-    __syncthreads();
-    if (p.top > 0) rank_keys(sh.keys, kThreads, p.top, sh.top, tid);
+    if (warp == 0) {
+      const int r = lane % kMaxSplit;
+      sm.m = r < split ? sh.parts[r][0] : -kInf;
+      sm.s = r < split ? sh.parts[r][1] : 0.f;
+      sm.e = r < split ? sh.parts[r][2] : 0.f;
+      sm.sub = sm.m == -kInf ? 0.f : sm.m;
+      join_lanes(kMaxSplit);
+    }
+    if constexpr (kTop) {
+      rank_keys<kThreads>(sh.lists, split * p.top, p.top, sh.top, tid);
+      __syncthreads();
+    }
   }
 
   if (tid == 0) {
-    const float m = sh.cta[0], s = sh.cta[1], e = sh.cta[2];
+    const float m = sm.m, s = sm.s, e = sm.e;
     const bool empty = m == -kInf && s == 0.f;  // every logit -inf (a NaN makes s NaN)
     const float log_s = empty ? 0.f : logf(s);
-    const int64_t target = p.targets[row_id];
     float lp = 0.f;
     if (target >= p.vocab) {
       latch_error(p.status, MXFP8_ERR_BAD_TARGET);
       lp = __uint_as_float(0x7FC00000u);
     } else if (target >= 0) {
-      lp = empty ? -kInf : (Vec<T>::load(row + target) - m) * p.inv_t - log_s;
+      lp = empty ? -kInf : (target_logit - m) * p.inv_t - log_s;
     }
     if (isnan(s)) lp = s;
+    const float row_max = isnan(s) ? s : m;
     p.logprob[row_id] = lp;
     p.entropy[row_id] = empty ? 0.f : log_s - kLn2 * e / s;
-    p.stats[2 * row_id] = isnan(s) ? s : m;
+    p.stats[2 * row_id] = row_max;
     p.stats[2 * row_id + 1] = log_s;
-    sh.row[0] = isnan(s) ? s : m;
+    sh.row[0] = row_max;
     sh.row[1] = log_s;
   }
-  if (p.top > 0) {
+  if constexpr (kTop) {
     __syncthreads();
     if (tid < p.top) {
       const uint64_t key = sh.top[tid];
@@ -570,11 +667,11 @@ logprob_grad_kernel(const GradParams p) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*k)(KArgs...), unsigned grid, int cluster, cudaStream_t stream,
-                   Args... args) {
+cudaError_t launch(void (*k)(KArgs...), unsigned grid, int threads, int cluster,
+                   cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
@@ -589,6 +686,23 @@ cudaError_t launch(void (*k)(KArgs...), unsigned grid, int cluster, cudaStream_t
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
+// Threads of a CTA: few enough that each has 16 vectors or more of its part to stream, because
+// the joins and the ranking after the stream are hidden only by other CTAs on the SM (4096 x
+// 8000 BF16, top 8: 45 us with 256 threads, 30 with 128, 25 with 64; 2000 x 16000: 29, 23, 27;
+// 4096 x 131072, top 32: 206, 231, 356); more where the rows alone would leave SMs short of
+// threads.
+template <typename T, bool kTop>
+cudaError_t launch_forward(const Params& p, int split, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>(p.rows * split);
+  const int64_t vectors = p.vocab / Vec<T>::kN / split;
+  int threads = vectors >= 4096 ? 256 : vectors >= 1536 ? 128 : 64;
+  while (threads < 256 && p.rows * split * threads < int64_t{1024} * num_sms()) threads *= 2;
+  auto k = threads == 256   ? logprob_kernel<T, kTop, 256>
+           : threads == 128 ? logprob_kernel<T, kTop, 128>
+                            : logprob_kernel<T, kTop, 64>;
+  return launch(k, grid, threads, split, stream, p, split);
+}
+
 }  // namespace
 
 cudaError_t launch_logprob(const LogprobArgs& a, cudaStream_t stream) {
@@ -601,8 +715,10 @@ cudaError_t launch_logprob(const LogprobArgs& a, cudaStream_t stream) {
     split *= 2;
   const int64_t grid = a.rows * split;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  return launch(a.fp32 ? logprob_kernel<float> : logprob_kernel<__nv_bfloat16>,
-                static_cast<unsigned>(grid), split, stream, p, split);
+  return a.fp32 ? (a.top ? launch_forward<float, true>(p, split, stream)
+                         : launch_forward<float, false>(p, split, stream))
+                : (a.top ? launch_forward<__nv_bfloat16, true>(p, split, stream)
+                         : launch_forward<__nv_bfloat16, false>(p, split, stream));
 }
 
 cudaError_t launch_logprob_grad(const LogprobGradArgs& a, cudaStream_t stream) {
@@ -627,7 +743,7 @@ cudaError_t launch_logprob_grad(const LogprobGradArgs& a, cudaStream_t stream) {
   auto k = a.fp32 ? (vector ? logprob_grad_kernel<float, true> : logprob_grad_kernel<float, false>)
                   : (vector ? logprob_grad_kernel<__nv_bfloat16, true>
                             : logprob_grad_kernel<__nv_bfloat16, false>);
-  return launch(k, static_cast<unsigned>(grid), 1, stream, p);
+  return launch(k, static_cast<unsigned>(grid), kThreads, 1, stream, p);
 }
 
 }  // namespace mxfp8

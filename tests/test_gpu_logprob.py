@@ -329,3 +329,20 @@ def test_refusals(m):
         assert e.value.status == m.ERR_INVALID_ARG
     with pytest.raises(m.MXFP8Error):
         m.token_logprobs(x[:, :0], t)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(2501, 517, torch.bfloat16), (2600, 130, torch.float32),
+                                              (1300, 12500, torch.bfloat16),
+                                              (1250, 6400, torch.float32)])
+@pytest.mark.parametrize("top", [0, 7, 32])
+def test_many_rows_of_smaller_vocabularies(m, rows, vocab, dtype, top):
+    """Enough rows for CTAs of 64 and of 128 threads; some rows tied, masked or empty."""
+    x, t = make(rows + top, rows, vocab, dtype, vocab + 3, 1)
+    x[5] = 2.0
+    x[6, 3:] = -INF
+    x[7] = -INF
+    x[8] = torch.arange(vocab, device=DEV).to(dtype)
+    x[9, ::2] = torch.finfo(dtype).min
+    x[10, 11] = float("nan")
+    t[8:11] = 4
+    check_forward(m, x, t, 0.9, top)
