@@ -45,45 +45,54 @@ namespace {
 
 constexpr int BM = 128;        // tile rows per CTA = TMEM lanes
 constexpr int BK = 128;        // K per block and pipeline stage
-constexpr int kFoldFirst = 4;  // warps 0-3: producer, MMA issuer, scales, none
-constexpr int kScaleRing = 4;  // blocks whose scales are in shared memory or on their way
+constexpr int kScaleRing = 4;  // blocks whose scales a warp has in shared memory or on their way
 
 enum Mode : int { kFprop = 0, kWgrad = 1, kSwapped = 2 };
 
-template <int BN, bool kPair>
+template <int BN, int kMode, bool kPair>
 struct Cfg {
   static constexpr int kBRows = kPair ? BN / 2 : BN;  // column-operand rows staged per CTA
   static constexpr int kABytes = BM * BK;
   static constexpr int kBBytes = kBRows * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   // narrow tiles leave room for two CTAs on an SM
-  static constexpr int kStages = BN >= 128 ? 6 : 4;
+  static constexpr int kStages = BN < 128 ? 4 : kMode == kWgrad ? 5 : 6;
   // four folding warps (a TMEM lane quarter each) for each group of columns
   static constexpr int kColGroups = BN == 192 ? 3 : 2;
   static constexpr int kNC = BN / kColGroups;         // columns per folding warp
   static constexpr int kFoldWarps = 4 * kColGroups;
+  // warps 0 and 1 copy and issue; a pair has two idle ones after them, because registers move
+  // between whole warpgroups
+  static constexpr int kFoldFirst = kPair ? 4 : 2;
   static constexpr int kThreads = 32 * (kFoldFirst + kFoldWarps);
-  // Pairs hold their sums in more registers than an even share: the folding warpgroups take
-  // some over from the first one (12 x 168 = 8 x 224 + 4 x 56; 16 x 128 = 12 x 152 + 4 x 56).
-  static constexpr int kFoldRegs = BN == 192 ? 152 : 224, kOtherRegs = 56;
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kOffA + kStages * kABytes;
-  // store staging: one 32-row x 64-byte box per folding warp, 1024-byte aligned
+  // store staging: two 32-row x 64-byte boxes per folding warp, 1024-byte aligned
   static constexpr int kBoxBytes = 32 * 64;
   static constexpr int kOffBox = kOffB + kStages * kBBytes;
-  static constexpr int kOffScale = kOffBox + kFoldWarps * kBoxBytes;
-  static constexpr int kScaleFloats = BM + (BN < 32 ? 32 : BN);  // a block's row, column scales
-  static constexpr int kOffBar = kOffScale + kScaleRing * kScaleFloats * 4;
-  // full, empty [kStages]; sc_full, sc_free [kScaleRing]; acc_full, acc_empty [2]; done
-  static constexpr int kNumBars = 2 * kStages + 2 * kScaleRing + 5;
+  static constexpr int kOffScale = kOffBox + (kMode == kSwapped ? 0 : 2 * kFoldWarps * kBoxBytes);
+  static constexpr int kScaleFloats = 32 + kNC;  // a warp's row and column scales of a block
+  static constexpr int kOffBar =
+      kOffScale + (kMode == kFprop ? 0 : kFoldWarps * kScaleRing * kScaleFloats * 4);
+  static constexpr int kNumBars = 2 * kStages + 5;  // full, empty, acc_full, acc_empty, done
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + slack for 1024-byte alignment
   static constexpr int kTmemCols = BN == 192 ? 512 : 2 * BN;  // two accumulators
   static constexpr int kMinCtas = BN <= 64 ? 2 : 1;
   static_assert(kTmemCols >= 32 && kTmemCols <= 512, "TMEM columns");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory overflow");
-  static_assert(BN * BM * 4 <= kStages * kStageBytes, "split-K partial overflow");
+  // split-K partial sums: [row][column], or (kSwapped) [column][row]; the padding keeps the
+  // rows of a 16-byte access on different banks
+  static constexpr int kPartPitch = (kMode == kSwapped ? BM : BN) + 4;
+  static_assert((kMode == kSwapped ? BN : BM) * kPartPitch * 4 <= kStages * kStageBytes,
+                "split-K partial overflow");
 };
+
+// Pairs need more registers for their sums than an even share: the folding warpgroups take
+// some over from the first one (12 warps x 168 = 8 x 224 + 4 x 56; 16 x 128 = 12 x 152 + 4 x 56).
+template <int BN>
+constexpr int kFoldRegs = BN == 192 ? 152 : 224;
+constexpr int kOtherRegs = 56;
 
 struct Params {
   const float* sr;      // scales of the row operand: [nkb][ldr], or [row blocks][nkb] (kSwapped)
@@ -118,11 +127,6 @@ __device__ __forceinline__ void tile_at(const Params& p, uint32_t id, int64_t& r
 
 // TMEM loads of G columns of the warp's lanes, and the wait for them. The wait carries the
 // registers, so that no use of them moves ahead of it.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
@@ -168,17 +172,17 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[G]) {
   for (int i = 0; i < G; ++i) asm volatile("" : "+r"(r[i]) :: "memory");
 }
 
-// 4 bytes global -> shared, and an arrival on `bar` once this thread's copies so far are in.
+// 4 bytes global -> shared, in this thread's current group of copies.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {  // all but the last kPending groups are in
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
 // A whole warp waits for a phase, every lane for itself (one lane and a shuffle or vote took
@@ -246,6 +250,36 @@ __device__ __forceinline__ void fold(float* acc, const uint32_t (&v)[G], float s
   }
 }
 
+// The weight gradient's fold: a scale for every row and every column. A scale that each lane
+// needs for every column costs one shared-memory cycle a warp and column, 1024 for a 256-wide
+// block (measured 837 cycles a block in the fold alone). So TMEM is read in the 16x256b shape, which gives
+// a lane few columns of several rows: of columns 8 j + 2 (lane % 4) and the next, rows lane / 4
+// (r[4 j], r[4 j + 1]) and lane / 4 + 8 (r[4 j + 2], r[4 j + 3]), of 16 rows and 64 columns a
+// read; column scales are read two at a time and serve four rows.
+__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void fold_quads(float (&acc)[8][4], const uint32_t (&r)[32], float s0,
+                                           float s1, const float2 (&c)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    acc[j][0] = fmaf(__uint_as_float(r[4 * j]), s0 * c[j].x, acc[j][0]);
+    acc[j][1] = fmaf(__uint_as_float(r[4 * j + 1]), s0 * c[j].y, acc[j][1]);
+    acc[j][2] = fmaf(__uint_as_float(r[4 * j + 2]), s1 * c[j].x, acc[j][2]);
+    acc[j][3] = fmaf(__uint_as_float(r[4 * j + 3]), s1 * c[j].y, acc[j][3]);
+  }
+}
+
 __device__ __forceinline__ void store_one(const Params& p, int64_t at, float v) {
   if (p.out_fp32)
     static_cast<float*>(p.C)[at] = v;
@@ -253,73 +287,166 @@ __device__ __forceinline__ void store_one(const Params& p, int64_t at, float v) 
     static_cast<uint16_t*>(p.C)[at] = static_cast<uint16_t>(cvt_bf16x2(0.f, v));
 }
 
-// The warp's 32 rows x kNC columns of the tile, from column c0: each 64-byte column group is
-// written into the warp's staging box (16-byte chunks XOR-swizzled as the tensor map's 64-byte
-// swizzle expects) and sent with one TMA store, clipped at the matrix edge. A store of one
-// row per lane would touch 32 cache lines an instruction: with those, a tile's stores took
-// 2.5 us, a sixth of the tile at K = 4096.
-template <int kNC>
-__device__ __forceinline__ void store_tile(const CUtensorMap* map, const Params& p,
-                                           const float (&acc)[kNC], uint8_t* box, int64_t row0,
-                                           int64_t c0, int lane) {
-  auto send = [&](const uint4 (&w)[4], int col) {
-    if (lane == 0) bulk_wait_read_all();  // the box is free again
+// A warp's 32 rows x kNC columns of the tile leave through two staging boxes in turn: each
+// 64-byte column group is written into a box (16-byte chunks XOR-swizzled as the tensor map's
+// 64-byte swizzle expects) and sent with one TMA store, clipped at the matrix edge. Stores of
+// one row per lane touch 32 cache lines an instruction: with those, a tile's stores took 2.5
+// us, a sixth of the tile at K = 4096.
+struct BoxStore {
+  const CUtensorMap* map;
+  uint8_t* boxes;
+  int turn;
+
+  // the box to write into, free again
+  __device__ __forceinline__ uint8_t* open(int lane) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
     __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint4*>(box + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) = w[j];
+    return boxes + (turn & 1) * (32 * 64);
+  }
+  // its first column and row
+  __device__ __forceinline__ void send(int64_t col, int64_t row, int lane) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(map, box, static_cast<int32_t>(c0 + col), static_cast<int32_t>(row0));
+      tma_store_2d(map, boxes + (turn & 1) * (32 * 64), static_cast<int32_t>(col),
+                   static_cast<int32_t>(row));
       bulk_commit_group();
     }
-  };
+    ++turn;
+  }
+};
+
+// Sums held one row per lane (acc[i]: column i).
+template <int kNC>
+__device__ __forceinline__ void store_rows(BoxStore& out, const Params& p, const float (&acc)[kNC],
+                                           int64_t row0, int64_t c0, int lane) {
   if (row0 >= p.nr) return;
-  if (p.out_fp32) {
 #pragma unroll
-    for (int u = 0; u < kNC; u += 16) {
-      if (c0 + u >= p.nc) continue;
-      uint4 w[4];
+  for (int u = 0; u < kNC; u += 16) {
+    if (!p.out_fp32 && (u & 16)) continue;  // BF16: 32 columns a box
+    if (c0 + u >= p.nc) continue;
+    uint4 w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = make_uint4(__float_as_uint(acc[u + 4 * j]), __float_as_uint(acc[u + 4 * j + 1]),
-                          __float_as_uint(acc[u + 4 * j + 2]),
-                          __float_as_uint(acc[u + 4 * j + 3]));
-      send(w, u);
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < kNC; u += 32) {
-      if (c0 + u >= p.nc) continue;
-      uint4 w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float* a = &acc[u + 8 * j];
+    for (int j = 0; j < 4; ++j) {
+      if (p.out_fp32) {
+        const float* a = &acc[u + 4 * j];
+        w[j] = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
+                          __float_as_uint(a[3]));
+      } else {
+        const float* a = &acc[(u & ~31) + 8 * j];
         w[j] = make_uint4(cvt_bf16x2(a[1], a[0]), cvt_bf16x2(a[3], a[2]),
                           cvt_bf16x2(a[5], a[4]), cvt_bf16x2(a[7], a[6]));
       }
-      send(w, u);
+    }
+    uint8_t* box = out.open(lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(box + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) = w[j];
+    out.send(c0 + u, row0, lane);
+  }
+}
+
+// Sums held in quads (see fold_quads).
+__device__ __forceinline__ void store_quads(BoxStore& out, const Params& p,
+                                            const float (&acc)[2][8][4], int64_t row0, int64_t c0,
+                                            int lane) {
+  if (row0 >= p.nr) return;
+  const int t4 = lane & 3;
+#pragma unroll
+  for (int u = 0; u < 64; u += 16) {
+    if (!p.out_fp32 && (u & 16)) continue;  // BF16: 32 columns a box
+    if (c0 + u >= p.nc) continue;
+    uint8_t* box = out.open(lane);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {  // rows lane / 4 + 8 h
+      const int row = (lane >> 2) + 8 * h, x = (row >> 1) & 3;
+      if (p.out_fp32) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float* a = &acc[h >> 1][u / 8 + j][2 * (h & 1)];
+          *reinterpret_cast<float2*>(box + row * 64 + 16 * ((2 * j + (t4 >> 1)) ^ x) +
+                                     8 * (t4 & 1)) = make_float2(a[0], a[1]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float* a = &acc[h >> 1][(u & ~31) / 8 + j][2 * (h & 1)];
+          *reinterpret_cast<uint32_t*>(box + row * 64 + 16 * (j ^ x) + 4 * t4) =
+              cvt_bf16x2(a[1], a[0]);
+        }
+      }
+    }
+    out.send(c0 + u, row0, lane);
+  }
+}
+
+// Adds CTA `part`'s share of a tile over the kSplit CTAs of the cluster, in rank order, and
+// stores it: four neighbours of an output row at a time, the loads of several of them (eight
+// in all) under way together, because a load from another SM takes about a microsecond.
+template <typename C, int kMode, int kSplit>
+__device__ __forceinline__ void join_parts(const Params& p, uint32_t sums, int64_t row0,
+                                           int64_t col0, uint32_t part) {
+  constexpr bool kT = kMode == kSwapped;
+  constexpr int kLines = kT ? 2 * C::kNC : BM;        // output rows in the tile
+  constexpr int kFours = (kT ? BM : 2 * C::kNC) / 4;  // groups of four in each
+  constexpr int kAhead = 8 / kSplit;
+  constexpr int kShare = kLines * kFours / kSplit;
+  const int lo = kShare * static_cast<int>(part);
+  for (int i0 = threadIdx.x; i0 < kShare; i0 += kAhead * C::kThreads) {
+    float4 v[kAhead][kSplit];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = lo + i0 + u * C::kThreads;
+      const uint32_t at = sums + 4 * (i / kFours * C::kPartPitch + i % kFours * 4);
+#pragma unroll
+      for (int k = 0; k < kSplit; ++k) {
+        if (i0 + u * C::kThreads >= kShare) continue;
+        uint32_t from;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(k));
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[u][k].x), "=f"(v[u][k].y), "=f"(v[u][k].z), "=f"(v[u][k].w)
+                     : "r"(from) : "memory");
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (i0 + u * C::kThreads >= kShare) continue;
+      const int i = lo + i0 + u * C::kThreads;
+      float4 s = v[u][0];
+#pragma unroll
+      for (int k = 1; k < kSplit; ++k) {
+        s.x += v[u][k].x;
+        s.y += v[u][k].y;
+        s.z += v[u][k].z;
+        s.w += v[u][k].w;
+      }
+      // the output's row, and the first of four places in it (rows of N values, N % 8 == 0)
+      const int64_t line = (kT ? col0 : row0) + i / kFours;
+      const int64_t place = (kT ? row0 : col0) + i % kFours * 4;
+      if (line >= (kT ? p.nc : p.nr) || place >= (kT ? p.nr : p.nc)) continue;
+      if (p.out_fp32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.C) + line * p.ldo + place) = s;
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.C) + line * p.ldo + place) =
+            make_uint2(cvt_bf16x2(s.y, s.x), cvt_bf16x2(s.w, s.z));
     }
   }
 }
 
 template <int BN, int kMode, bool kPair>
-__global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, Cfg<BN, kPair>::kMinCtas)
+__global__ void __launch_bounds__(Cfg<BN, kMode, kPair>::kThreads, Cfg<BN, kMode, kPair>::kMinCtas)
 blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
                       const __grid_constant__ CUtensorMap map_c,
                       const __grid_constant__ CUtensorMap map_o, const Params p) {
-  using C = Cfg<BN, kPair>;
+  using C = Cfg<BN, kMode, kPair>;
   constexpr int kStages = C::kStages, kNC = C::kNC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // pair: the leader's
   uint64_t* empty = full + kStages;
-  uint64_t* sc_full = empty + kStages;
-  uint64_t* sc_free = sc_full + kScaleRing;
-  uint64_t* acc_full = sc_free + kScaleRing;  // [2]
-  uint64_t* acc_empty = acc_full + 2;         // [2]; pair: the leader's
+  uint64_t* acc_full = empty + kStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;    // [2]; pair: the leader's
   uint64_t* mma_done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -327,8 +454,6 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
   // single CTA writes both), [2] stage uses consumed by the MMA issuer (one accumulator
   // commit each), [3] this CTA's producer tail completed
   volatile uint32_t* rec = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 8);
-
-  float* scales = reinterpret_cast<float*>(smem + C::kOffScale);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = kPair ? cluster_ctarank() : 0;
@@ -346,10 +471,6 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-    }
-    for (int i = 0; i < kScaleRing; ++i) {
-      mbar_init(&sc_full[i], 32);
-      mbar_init(&sc_free[i], C::kFoldWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -377,7 +498,7 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
 
   // each role sets its own register limit, inside its branch
   if (warp == 0) {
-    if constexpr (kPair) set_max_regs_dec<C::kOtherRegs>();
+    if constexpr (kPair) set_max_regs_dec<kOtherRegs>();
     // ------------------------------------------------------------- TMA producer
     const bool issuer = elect_one();
     const uint32_t full0 = kPair ? cluster_map(&full[0], 0) : smem_u32(&full[0]);
@@ -425,60 +546,10 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       tail_ok = wait_phase(&empty[i % kStages], (i / kStages) & 1, abort_flag, p.wait_ns);
     if (issuer) rec[3] = tail_ok ? 1u : 0u;
     __syncwarp();
-  } else if (kMode != kFprop && warp == 2) {
-    if constexpr (kPair) set_max_regs_dec<C::kOtherRegs>();
-    // ------------------------------------------------------------- scales
-    // Up to kScaleRing blocks ahead of the fold, because a load from L2 takes longer than a
-    // block: the row scales (kSwapped: the row tile's one) and column scales (kFprop: one
-    // for each 128 columns) of a block, copied asynchronously. What lies past the matrix is
-    // left as it is: the products there are zero and their sums are not stored.
-    uint32_t it = 0;
-    bool ok = true;
-    for (uint32_t id = first_id; ok && id < p.tiles; id += id_step) {
-      int64_t rt, ct;
-      tile_at(p, id, rt, ct);
-      const int64_t r0 = (kPair ? 2 * rt + crank : rt) * BM, c0 = ct * BN;
-      const int rows = static_cast<int>(p.nr - r0 < BM ? p.nr - r0 : BM);
-      const int cols = static_cast<int>(p.nc - c0 < BN ? p.nc - c0 : BN);
-      const float* sr = kMode == kSwapped ? p.sr + rt * p.nkb + kb0
-                                          : p.sr + kb0 * p.ldr + r0 + lane;
-      const float* sc = kMode == kFprop ? p.sc + (c0 / 128 + lane) * p.nkb + kb0
-                                        : p.sc + kb0 * p.ldc + c0 + lane;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t n = it % kScaleRing, ph = (it / kScaleRing) & 1;
-        if (!wait_phase(&sc_free[n], ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
-        float* slot = scales + n * C::kScaleFloats;
-        if constexpr (kMode == kSwapped) {
-          if (lane == 0) cp_async4(slot, sr);
-          ++sr;
-        } else {
-#pragma unroll
-          for (int i = 0; i < BM; i += 32)
-            if (i + lane < rows) cp_async4(slot + i + lane, sr + i);
-          sr += p.ldr;
-        }
-        if constexpr (kMode == kFprop) {
-          if (128 * lane < cols) cp_async4(slot + BM + lane, sc);
-          ++sc;
-        } else {
-#pragma unroll
-          for (int i = 0; i < BN; i += 32)
-            if (i + lane < cols) cp_async4(slot + BM + i + lane, sc + i);
-          sc += p.ldc;
-        }
-        cp_async_arrive(&sc_full[n]);
-      }
-    }
-    if (!ok && lane == 0) {
-      *abort_flag = 1;
-      latch_error(p.status, MXFP8_ERR_TIMEOUT);
-    }
-    cp_async_wait_all();
-    __syncwarp();
-  } else if (warp < kFoldFirst && !(warp == 1 && leader)) {
-    if constexpr (kPair) set_max_regs_dec<C::kOtherRegs>();
+  } else if (warp < C::kFoldFirst && !(warp == 1 && leader)) {
+    if constexpr (kPair) set_max_regs_dec<kOtherRegs>();
   } else if (warp == 1) {
-    if constexpr (kPair) set_max_regs_dec<C::kOtherRegs>();
+    if constexpr (kPair) set_max_regs_dec<kOtherRegs>();
     // ------------------------------------------------------------- MMA issuer
     const bool issuer = elect_one();
     uint32_t it = 0;
@@ -531,45 +602,77 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     }
     __syncwarp();
   } else {
-    if constexpr (kPair) set_max_regs_inc<C::kFoldRegs>();
+    if constexpr (kPair) set_max_regs_inc<kFoldRegs<BN>>();
     // ------------------------------------------------------------- fold and store
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
-    const int half = (warp - kFoldFirst) >> 2;  // which group of the columns
-    uint8_t* box = smem + C::kOffBox + (warp - kFoldFirst) * C::kBoxBytes;
+    const int half = (warp - C::kFoldFirst) >> 2;  // which group of the columns
+    BoxStore out{&map_o, smem + C::kOffBox + (warp - C::kFoldFirst) * 2 * C::kBoxBytes, 0};
     const uint32_t acc_empty0 = kPair ? cluster_map(&acc_empty[0], 0) : smem_u32(&acc_empty[0]);
     constexpr bool kColVec = kMode != kFprop;
-    constexpr int G = BN == 192 ? 32 : kNC < 64 ? kNC : 64;  // columns a TMEM read
+    constexpr bool kQuads = kMode == kWgrad;
+    static_assert(!kQuads || kNC == 64, "a warp of the weight gradient folds 64 columns");
+    // columns a TMEM read: as many as the registers allow
+    constexpr int G = kMode == kSwapped ? (kNC < 32 ? kNC : kNC / 2) : 64;
     const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * kNC;
-    // kFprop: the scales of two blocks, and those of the next two under way
-    uint32_t ahead_id = first_id;
-    int ahead_kb = kb0;
+    // Scales travel ahead of the fold, tile after tile: with the operands' copies and the MMA
+    // on it, shared memory answers in about 180 cycles, as long as the FMAs of 64 columns
+    // take, and a load from L2 takes longer than a block.
+    //   kFprop   in registers: the scales of two blocks in use (s0, s1), of the next two under
+    //            way (nr, nc)
+    //   others   in this warp's ring of slots: 32 row scales (kSwapped: one), kNC column scales
+    uint32_t ahead_id = first_id, ahead_it = 0;
+    int ahead_kb = kb0, rows_here = 0, cols_here = 0;
     const float *srp = nullptr, *scp = nullptr;
     float nr[2], nc[2];
+    float* ring = reinterpret_cast<float*>(smem + C::kOffScale) +
+                  (warp - C::kFoldFirst) * kScaleRing * C::kScaleFloats;
     auto fetch = [&]() {
-      if (ahead_id >= p.tiles) return;
-      if (ahead_kb == kb0) {
-        int64_t rt, ct;
-        tile_at(p, ahead_id, rt, ct);
-        const int64_t row = (kPair ? 2 * rt + crank : rt) * BM + 32 * q + lane;
-        const int64_t col = ct * BN + half * kNC;
-        srp = p.sr + kb0 * p.ldr + (row < p.nr ? row : p.nr - 1);
-        scp = p.sc + (col < p.nc ? col : p.nc - 1) / 128 * p.nkb + kb0;
+      if (ahead_id < p.tiles) {
+        if (ahead_kb == kb0) {
+          int64_t rt, ct;
+          tile_at(p, ahead_id, rt, ct);
+          const int64_t row = (kPair ? 2 * rt + crank : rt) * BM + 32 * q;
+          const int64_t col = ct * BN + half * kNC;
+          if constexpr (kColVec) {
+            rows_here = static_cast<int>(p.nr - row < 32 ? p.nr - row : 32);
+            cols_here = static_cast<int>(p.nc - col < kNC ? p.nc - col : kNC);
+            srp = kMode == kSwapped ? p.sr + rt * p.nkb + kb0 : p.sr + kb0 * p.ldr + row + lane;
+            scp = p.sc + kb0 * p.ldc + col + lane;
+          } else {
+            srp = p.sr + kb0 * p.ldr + (row + lane < p.nr ? row + lane : p.nr - 1);
+            scp = p.sc + (col < p.nc ? col : p.nc - 1) / 128 * p.nkb + kb0;
+          }
+        }
+        if constexpr (kColVec) {  // what lies past the matrix meets zero products, unstored
+          float* slot = ring + (ahead_it % kScaleRing) * C::kScaleFloats;
+          if (kMode == kSwapped ? lane == 0 : lane < rows_here) cp_async4(slot + lane, srp);
+#pragma unroll
+          for (int i = 0; i < kNC; i += 32)
+            if (i + lane < cols_here) cp_async4(slot + 32 + i + lane, scp + i);
+          srp += kMode == kSwapped ? 1 : p.ldr;
+          scp += p.ldc;
+          ++ahead_kb;
+          ++ahead_it;
+        } else {
+          nr[0] = __ldg(srp);
+          nc[0] = __ldg(scp);
+          if (ahead_kb + 1 < kb1) {
+            nr[1] = __ldg(srp + p.ldr);
+            nc[1] = __ldg(scp + 1);
+          }
+          srp += 2 * p.ldr;
+          scp += 2;
+          ahead_kb += 2;
+        }
+        if (ahead_kb >= kb1) {
+          ahead_kb = kb0;
+          ahead_id += id_step;
+        }
       }
-      nr[0] = __ldg(srp);
-      nc[0] = __ldg(scp);
-      if (ahead_kb + 1 < kb1) {
-        nr[1] = __ldg(srp + p.ldr);
-        nc[1] = __ldg(scp + 1);
-      }
-      srp += 2 * p.ldr;
-      scp += 2;
-      ahead_kb += 2;
-      if (ahead_kb >= kb1) {
-        ahead_kb = kb0;
-        ahead_id += id_step;
-      }
+      if constexpr (kColVec) cp_async_commit();  // one group a block, empty past the last
     };
-    if constexpr (!kColVec) fetch();
+#pragma unroll
+    for (int i = 0; i < (kColVec ? kScaleRing - 1 : 1); ++i) fetch();
     uint32_t it = 0;
     bool ok = true;
     for (uint32_t id = first_id; ok && id < p.tiles; id += id_step) {
@@ -578,20 +681,22 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       const int64_t row0 = (kPair ? 2 * rt + crank : rt) * BM + 32 * q;
       const int64_t col = ct * BN + half * kNC;  // this warp's first column
       const bool row_ok = row0 + lane < p.nr;
-      float acc[kNC];
+      float acc[kQuads ? 1 : kNC], quads[2][8][4];
 #pragma unroll
-      for (int i = 0; i < kNC; ++i) acc[i] = 0.f;
+      for (int i = 0; i < (kQuads ? 1 : kNC); ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) (&quads[0][0][0])[i] = 0.f;
       float s0 = 0.f, s1 = 0.f;
 #pragma unroll 1
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t n = it % kScaleRing, b = it & 1;
-        float s;
-        const float* cs = nullptr;
+        const uint32_t b = it & 1;
+        const float* slot = ring + (it % kScaleRing) * C::kScaleFloats;
+        float s = 0.f;
         if constexpr (kColVec) {
-          ok = wait_phase(&sc_full[n], (it / kScaleRing) & 1, abort_flag, p.wait_ns);
-          const float* slot = scales + n * C::kScaleFloats;
-          s = kMode == kSwapped ? slot[0] : row_ok ? slot[32 * q + lane] : 1.f;
-          cs = slot + BM + half * kNC;
+          cp_async_wait<kScaleRing - 2>();
+          __syncwarp();  // this block's scales are in; the slot before it is free again
+          fetch();
+          if constexpr (kMode == kSwapped) s = slot[0];
         } else {
           if (((kb - kb0) & 1) == 0) {
             s0 = nr[0] * nc[0];
@@ -600,32 +705,69 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
           }
           s = ((kb - kb0) & 1) ? s1 : s0;
         }
-        ok = ok && wait_phase(&acc_full[b], (it >> 1) & 1, abort_flag, p.wait_ns);
+        float rq[4];
+        if constexpr (kQuads) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) rq[h] = slot[(lane >> 2) + 8 * h];
+        }
+        ok = wait_phase(&acc_full[b], (it >> 1) & 1, abort_flag, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
+        if constexpr (kQuads) {
+          float2 cq[8];
 #pragma unroll
-        for (int g = 0; g < kNC; g += G) {
-          uint32_t r[G];
-          tmem_ld(tbase + b * BN + g, r);
-          tmem_wait(r);
-          if (g + G == kNC) {  // the block has left TMEM
-            tc_fence_before();
-            arrive_if(lane == 0, acc_empty0 + 8 * b);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_ld_quads(tbase + b * BN + (static_cast<uint32_t>(16 * h) << 16), r);
+            if (h == 0) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                cq[j] = *reinterpret_cast<const float2*>(slot + 32 + 8 * j + 2 * (lane & 3));
+            }
+            tmem_wait(r);
+            if (h == 1) {  // the block has left TMEM
+              tc_fence_before();
+              arrive_if(lane == 0, acc_empty0 + 8 * b);
+            }
+            fold_quads(quads[h], r, rq[2 * h], rq[2 * h + 1], cq);
           }
-          fold<G, kColVec>(acc + g, r, s, cs + g);
-        }
-        if constexpr (kColVec) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive_relaxed(&sc_free[n]);
+        } else {
+#pragma unroll
+          for (int g = 0; g < kNC; g += G) {
+            uint32_t r[G];
+            tmem_ld(tbase + b * BN + g, r);
+            tmem_wait(r);
+            if (g + G == kNC) {  // the block has left TMEM
+              tc_fence_before();
+              arrive_if(lane == 0, acc_empty0 + 8 * b);
+            }
+            fold<G, kColVec>(acc + g, r, s, slot + 32 + g);
+          }
         }
       }
       if (!ok) break;
       if (!kPair && p.split > 1) {
-        // partial sums into the (now idle) stages, [column][row]
+        // partial sums into the (now idle) stages
         float* part_sum = reinterpret_cast<float*>(smem);
+        if constexpr (kMode == kSwapped) {
 #pragma unroll
-        for (int i = 0; i < kNC; ++i)
-          part_sum[(half * kNC + i) * BM + 32 * q + lane] = acc[i];
+          for (int i = 0; i < kNC; ++i)
+            part_sum[(half * kNC + i) * C::kPartPitch + 32 * q + lane] = acc[i];
+        } else if constexpr (kQuads) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float2*>(
+                  part_sum + (32 * q + (lane >> 2) + 8 * h) * C::kPartPitch + half * kNC + 8 * j +
+                  2 * (lane & 3)) =
+                  make_float2(quads[h >> 1][j][2 * (h & 1)], quads[h >> 1][j][2 * (h & 1) + 1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kNC; i += 4)
+            *reinterpret_cast<float4*>(part_sum + (32 * q + lane) * C::kPartPitch + half * kNC + i) =
+                make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        }
       } else if constexpr (kMode == kSwapped) {
         if (row_ok) {
 #pragma unroll
@@ -633,11 +775,14 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
             if (col + i < p.nc) store_one(p, (col + i) * p.ldo + row0 + lane, acc[i]);
         }
       } else {
-        store_tile<kNC>(&map_o, p, acc, box, row0, col, lane);
+        if constexpr (kQuads) store_quads(out, p, quads, row0, col, lane);
+        else store_rows<kNC>(out, p, acc, row0, col, lane);
       }
     }
-    // its stores must have finished reading shared memory before the CTA exits
+    // its stores must have finished reading shared memory before the CTA exits, and its copies
+    // writing it
     if (lane == 0) bulk_wait_read_all();
+    cp_async_wait<0>();
     __syncwarp();
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -673,28 +818,15 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
   if constexpr (kPair) {
     if (issued > consumed) cluster_sync();  // the leader's drain covered the peer's copies too
   } else if (p.split > 1) {
-    // Join the parts: CTA `part` adds its share of the tile's columns over all parts, in
-    // rank order, and stores them. One tile per cluster.
+    // Join the parts: CTA `part` adds its share of the tile over all parts, in rank order, and
+    // stores it. One tile per cluster.
     cluster_sync();
     int64_t rt, ct;
     tile_at(p, first_id, rt, ct);
-    const int c_lo = BN * static_cast<int>(part) / p.split;
-    const int c_hi = BN * static_cast<int>(part + 1) / p.split;
-    const uint32_t base = smem_u32(smem);
-    for (int i = c_lo * BM + static_cast<int>(threadIdx.x); i < c_hi * BM;
-         i += C::kThreads) {
-      const int64_t row = rt * BM + i % BM, col = ct * BN + i / BM;
-      if (row >= p.nr || col >= p.nc) continue;
-      float sum = 0.f;
-      for (int r = 0; r < p.split; ++r) {
-        uint32_t from;
-        float v;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(base + 4 * i), "r"(r));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from) : "memory");
-        sum += v;
-      }
-      store_one(p, kMode == kSwapped ? col * p.ldo + row : row * p.ldo + col, sum);
-    }
+    const uint32_t sums = smem_u32(smem);
+    if (p.split == 2) join_parts<C, kMode, 2>(p, sums, rt * BM, ct * BN, part);
+    else if (p.split == 4) join_parts<C, kMode, 4>(p, sums, rt * BM, ct * BN, part);
+    else join_parts<C, kMode, 8>(p, sums, rt * BM, ct * BN, part);
     cluster_sync();  // no CTA leaves while its shared memory is being read
   }
   tc_fence_after();
@@ -774,7 +906,7 @@ template <int BN, int kMode, bool kPair>
 int launch(const CUtensorMap& mr, const CUtensorMap& mc, const CUtensorMap& mo, const Params& p,
            int64_t grid, int cluster, cudaStream_t stream) {
   auto k = blockwise_gemm_kernel<BN, kMode, kPair>;
-  constexpr int kSmem = Cfg<BN, kPair>::kSmemBytes;
+  constexpr int kSmem = Cfg<BN, kMode, kPair>::kSmemBytes;
   static std::atomic<bool> attr_set[64] = {};  // per device; setting it twice is harmless
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MXFP8_ERR_CUDA;
@@ -786,7 +918,7 @@ int launch(const CUtensorMap& mr, const CUtensorMap& mc, const CUtensorMap& mo, 
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(Cfg<BN, kPair>::kThreads, 1, 1);
+  cfg.blockDim = dim3(Cfg<BN, kMode, kPair>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -805,7 +937,7 @@ int launch(const CUtensorMap& mr, const CUtensorMap& mc, const CUtensorMap& mo, 
 // 256 x BN tiles on CTA pairs. `a` is the row operand.
 template <int BN, int kMode>
 int launch_pairs(const BlockwiseGemmArgs& a, Params p, cudaStream_t stream) {
-  using C = Cfg<BN, true>;
+  using C = Cfg<BN, kMode, true>;
   CUtensorMap mr, mc, mo;
   if (!make_operand_map(&mr, a.A, a.K, a.M, BM) ||
       !make_operand_map(&mc, a.B, a.K, a.N, C::kBRows) ||
@@ -840,16 +972,37 @@ int launch_single(const void* R, int64_t nr, const void* Cop, int64_t nc, int64_
   p.band = kMode == kSwapped ? 1 : (p.row_tiles < 8 ? p.row_tiles : 8);
   p.split = split;
   int64_t grid = tiles * split;
-  const int64_t fit = static_cast<int64_t>(num_sms()) * Cfg<BN, false>::kMinCtas;
+  const int64_t fit = static_cast<int64_t>(num_sms()) * Cfg<BN, kMode, false>::kMinCtas;
   if (split == 1 && grid > fit) grid = fit;  // persistent
   return launch<BN, kMode, false>(mr, mc, mo, p, grid, split, stream);
 }
 
-// Parts of the reduction: enough to give every SM a CTA, at least 4 blocks each.
-int split_for(int64_t tiles, int64_t nkb) {
-  int s = 1;
-  while (s < 8 && tiles * s * 2 <= num_sms() && nkb >= 8 * s) s *= 2;
-  return s;
+// Estimated microseconds, from which shapes and splits are chosen. Measured on GB300 (K = 4096
+// and 12288): a block takes a 128-row CTA 0.43 us whatever its columns (0.55 with a scale for
+// each column of a wide tile), a 256 x 256 pair tile 0.45 us, a 256 x 192 pair tile of the
+// weight gradient 0.69 us; a tile costs 1.2 to 2 us more for its first operands and its
+// store, 4.5 us when its parts are joined over a cluster.
+struct Plan {
+  double us;
+  int split;
+};
+
+Plan single_plan(int64_t tiles, int64_t nkb, int per_sm, double block_us) {
+  Plan best{1e30, 1};
+  const int64_t places = static_cast<int64_t>(num_sms()) * per_sm;
+  for (int s = 1; s <= 8 && (s == 1 || nkb >= 4 * s); s *= 2) {
+    const double waves = static_cast<double>((tiles * s + places - 1) / places);
+    const double us = waves * (static_cast<double>((nkb + s - 1) / s) * block_us +
+                               (s > 1 ? 4.5 : 2.0));
+    if (us < best.us) best = Plan{us, s};
+  }
+  return best;
+}
+
+double pair_us(int64_t tiles, int64_t nkb, bool wgrad) {
+  const int64_t pairs = num_sms() / 2;
+  return static_cast<double>((tiles + pairs - 1) / pairs) *
+             (static_cast<double>(nkb) * (wgrad ? 0.69 : 0.45) + 1.2) + 2.0;
 }
 
 // From this many operations on, the gain of the block-scaled MMA for power-of-two scales
@@ -882,7 +1035,7 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
     p.nr = a.N;
     p.nc = a.M;
     const int64_t rt = (a.N + BM - 1) / BM;
-    const int split = split_for(rt, p.nkb);
+    const int split = single_plan(rt, p.nkb, a.M <= 64 ? 2 : 1, 0.43).split;
     if (a.M <= 16) return launch_single<16, kSwapped>(a.B, a.N, a.A, a.M, a.K, p, split, stream);
     if (a.M <= 32) return launch_single<32, kSwapped>(a.B, a.N, a.A, a.M, a.K, p, split, stream);
     if (a.M <= 64) return launch_single<64, kSwapped>(a.B, a.N, a.A, a.M, a.K, p, split, stream);
@@ -928,12 +1081,15 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
     p.only_if = c.other;
     p.num_only_if = kConvertCtas;
   }
-  const int64_t pair_tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (pair_tiles >= num_sms() / 4)
-    return a.wgrad ? launch_pairs<192, kWgrad>(a, p, stream) : launch_pairs<256, kFprop>(a, p, stream);
-  const int split = split_for(((a.M + 127) / 128) * ((a.N + 127) / 128), p.nkb);
-  return a.wgrad ? launch_single<128, kWgrad>(a.A, a.M, a.B, a.N, a.K, p, split, stream)
-                 : launch_single<128, kFprop>(a.A, a.M, a.B, a.N, a.K, p, split, stream);
+  const int bn = a.wgrad ? 192 : 256;  // columns of a pair tile
+  const Plan single = single_plan(((a.M + 127) / 128) * ((a.N + 127) / 128), p.nkb, 1,
+                                  a.wgrad ? 0.55 : 0.43);
+  if (pair_us(((a.M + 255) / 256) * ((a.N + bn - 1) / bn), p.nkb, a.wgrad) < single.us)
+    return a.wgrad ? launch_pairs<192, kWgrad>(a, p, stream)
+                   : launch_pairs<256, kFprop>(a, p, stream);
+  return a.wgrad
+             ? launch_single<128, kWgrad>(a.A, a.M, a.B, a.N, a.K, p, single.split, stream)
+             : launch_single<128, kFprop>(a.A, a.M, a.B, a.N, a.K, p, single.split, stream);
 }
 
 }  // namespace mxfp8
