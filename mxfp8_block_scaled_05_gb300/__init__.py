@@ -111,15 +111,17 @@ def _ptr(t: torch.Tensor):
 def _require(t: torch.Tensor, dtype, name: str):
     """A tensor handed to the library: CUDA, of this dtype, contiguous, and on the current
     device (the library runs every call on the current device)."""
+    if (t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and t.get_device() == torch._C._cuda_getDevice()):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}; the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name} is on {t.device}; the current device is "
+                     f"cuda:{torch.cuda.current_device()}")
 
 
 def _buffer(t: torch.Tensor, dtype, numel: int, name: str):
@@ -638,8 +640,14 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: 
         _buffer(grad_top, torch.float32, rows * top, "grad_top")
         _buffer(top_id, torch.int64, rows * top, "top_id")
     if out is None:
-        out = _new((rows, pitch), logits.dtype, logits.device, stream)[:, :vocab]
         out_pitch = pitch
+        if stream is None:
+            out = torch.empty_strided((rows, vocab), (pitch, 1), dtype=logits.dtype,
+                                      device=logits.device)
+        else:
+            with torch.cuda.stream(stream):
+                out = torch.empty_strided((rows, vocab), (pitch, 1), dtype=logits.dtype,
+                                          device=logits.device)
     else:
         odt, orows, ovocab, out_pitch = _logits(out, "out")
         if (odt, orows, ovocab) != (dt, rows, vocab):
