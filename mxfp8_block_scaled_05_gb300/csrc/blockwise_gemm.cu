@@ -230,6 +230,12 @@ __device__ __forceinline__ void set_max_regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// acc[0], acc[1] += s (two packed) times v0, v1
+__device__ __forceinline__ void add_scaled(float* acc, uint32_t v0, uint32_t v1, uint64_t s) {
+  const uint64_t a = fma2(pack2(__uint_as_float(v0), __uint_as_float(v1)), s, pack2(acc[0], acc[1]));
+  unpack2(a, acc[0], acc[1]);
+}
+
 // acc[i] += s v[i] for G columns of one block, or += s c[i] v[i] with a scale for each column
 // (kColVec), which all lanes read from the same place in shared memory.
 template <int G, bool kColVec>
@@ -239,13 +245,11 @@ __device__ __forceinline__ void fold(float* acc, const uint32_t (&v)[G], float s
   for (int i = 0; i < G; i += 4) {
     if constexpr (kColVec) {
       const float4 c4 = *reinterpret_cast<const float4*>(c + i);
-      acc[i] = fmaf(__uint_as_float(v[i]), s * c4.x, acc[i]);
-      acc[i + 1] = fmaf(__uint_as_float(v[i + 1]), s * c4.y, acc[i + 1]);
-      acc[i + 2] = fmaf(__uint_as_float(v[i + 2]), s * c4.z, acc[i + 2]);
-      acc[i + 3] = fmaf(__uint_as_float(v[i + 3]), s * c4.w, acc[i + 3]);
+      add_scaled(acc + i, v[i], v[i + 1], mul2(pack2(s, s), pack2(c4.x, c4.y)));
+      add_scaled(acc + i + 2, v[i + 2], v[i + 3], mul2(pack2(s, s), pack2(c4.z, c4.w)));
     } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i + k] = fmaf(__uint_as_float(v[i + k]), s, acc[i + k]);
+      add_scaled(acc + i, v[i], v[i + 1], pack2(s, s));
+      add_scaled(acc + i + 2, v[i + 2], v[i + 3], pack2(s, s));
     }
   }
 }
@@ -271,12 +275,16 @@ __device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t (&r)[32])
 }
 __device__ __forceinline__ void fold_quads(float (&acc)[8][4], const uint32_t (&r)[32], float s0,
                                            float s1, const float2 (&c)[8]) {
+  const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    acc[j][0] = fmaf(__uint_as_float(r[4 * j]), s0 * c[j].x, acc[j][0]);
-    acc[j][1] = fmaf(__uint_as_float(r[4 * j + 1]), s0 * c[j].y, acc[j][1]);
-    acc[j][2] = fmaf(__uint_as_float(r[4 * j + 2]), s1 * c[j].x, acc[j][2]);
-    acc[j][3] = fmaf(__uint_as_float(r[4 * j + 3]), s1 * c[j].y, acc[j][3]);
+    const uint64_t cc = pack2(c[j].x, c[j].y);
+    const uint64_t a = fma2(pack2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])),
+                            mul2(p0, cc), pack2(acc[j][0], acc[j][1]));
+    const uint64_t b = fma2(pack2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])),
+                            mul2(p1, cc), pack2(acc[j][2], acc[j][3]));
+    unpack2(a, acc[j][0], acc[j][1]);
+    unpack2(b, acc[j][2], acc[j][3]);
   }
 }
 
