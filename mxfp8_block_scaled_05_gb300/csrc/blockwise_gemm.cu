@@ -21,8 +21,9 @@
 // Modes, by which operand lies along the 128 TMEM lanes ("rows") and the columns:
 //   kFprop    rows = A (a scale per row and block), columns = B (128 x 128 blocks)
 //   kWgrad    both with a scale per row / column and block
-//   kSwapped  rows = B, columns = A, C stored transposed: for few rows of A, where a
-//             128-row tile of A would be mostly empty
+//   kSwapped  rows = B, columns = A, C stored transposed: for up to 64 rows of A, where a
+//             128-row tile of A would be mostly empty. 64 x 4096 x 4096: 7.9 us, 9.1 in 128-row
+//             tiles of A; 128 x 4096 x 4096: 10.4 us so, 9.1 in 128-row tiles
 // and by size: pairs of CTAs (cta_group::2, 256 x 256 tiles, each SM stages half of the
 // column operand), or single CTAs (128 x BN tiles) whose reduction may be split over a
 // cluster, the parts joined through distributed shared memory in rank order.
@@ -910,24 +911,31 @@ __global__ void __launch_bounds__(kConvertThreads) convert_scales_kernel(const C
 
 // ------------------------------------------------------------------------- host side
 
+// The kernel, allowed its shared memory; nullptr after a CUDA error.
+template <int BN, int kMode, bool kPair>
+auto ready_kernel() -> decltype(&blockwise_gemm_kernel<BN, kMode, kPair>) {
+  auto k = blockwise_gemm_kernel<BN, kMode, kPair>;
+  static std::atomic<bool> attr_set[64] = {};  // per device; setting it twice is harmless
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<BN, kMode, kPair>::kSmemBytes) != cudaSuccess)
+      return nullptr;
+    if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
+  }
+  return k;
+}
+
 template <int BN, int kMode, bool kPair>
 int launch(const CUtensorMap& mr, const CUtensorMap& mc, const CUtensorMap& mo, const Params& p,
            int64_t grid, int cluster, cudaStream_t stream) {
-  auto k = blockwise_gemm_kernel<BN, kMode, kPair>;
-  constexpr int kSmem = Cfg<BN, kMode, kPair>::kSmemBytes;
-  static std::atomic<bool> attr_set[64] = {};  // per device; setting it twice is harmless
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MXFP8_ERR_CUDA;
-  if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
-        cudaSuccess)
-      return MXFP8_ERR_CUDA;
-    if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
-  }
+  auto k = ready_kernel<BN, kMode, kPair>();
+  if (!k) return MXFP8_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(Cfg<BN, kMode, kPair>::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = Cfg<BN, kMode, kPair>::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
@@ -985,32 +993,76 @@ int launch_single(const void* R, int64_t nr, const void* Cop, int64_t nc, int64_
   return launch<BN, kMode, false>(mr, mc, mo, p, grid, split, stream);
 }
 
-// Estimated microseconds, from which shapes and splits are chosen. Measured on GB300 (K = 4096
-// and 12288): a block takes a 128-row CTA 0.43 us whatever its columns (0.55 with a scale for
-// each column of a wide tile), a 256 x 256 pair tile 0.45 us, a 256 x 192 pair tile of the
-// weight gradient 0.69 us; a tile costs 1.2 to 2 us more for its first operands and its
-// store, 4.5 us when its parts are joined over a cluster.
+// Clusters of `split` single CTAs that the device runs at a time. Fewer than its SMs would hold,
+// because a cluster lies within a group of SMs whose size is no multiple of it: 76, 36 and 15
+// of 2, 4 and 8 on 152 SMs. The query counts one CTA an SM; narrow tiles have two.
+template <int BN, int kMode>
+int64_t clusters_at_once(int split) {
+  using C = Cfg<BN, kMode, false>;
+  if (split == 1) return static_cast<int64_t>(num_sms()) * C::kMinCtas;
+  static std::atomic<int> known[64][9] = {};  // per device and split; 0: not asked yet
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev >= 0 && dev < 64 && (n = known[dev][split].load(std::memory_order_relaxed)) > 0) return n;
+  auto k = ready_kernel<BN, kMode, false>();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(split), 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (!k || cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) return 1;
+  n *= C::kMinCtas;
+  if (dev >= 0 && dev < 64) known[dev][split].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Estimated microseconds, from which shapes and splits are chosen. Measured on GB300 (16 to 96
+// blocks of K, splits of 1 to 8, 16 to 192 row tiles): what a block takes, a tile's first
+// operands and store, and the join of two or four parts, or of eight.
+struct Cost {
+  double block, tile, join, join8;
+};
+template <int BN, int kMode>
+constexpr Cost kCost = BN == 16   ? Cost{0.275, 2.4, 1.2, 3.0}
+                       : BN == 32 ? Cost{0.29, 3.1, 1.1, 3.7}
+                       : BN == 64 ? Cost{0.345, 3.8, 1.3, 5.8}
+                       : kMode == kFprop ? Cost{0.32, 3.2, 3.2, 6.0}
+                                         : Cost{0.445, 3.3, 3.0, 6.0};
 struct Plan {
   double us;
   int split;
 };
 
-Plan single_plan(int64_t tiles, int64_t nkb, int per_sm, double block_us) {
+template <int BN, int kMode>
+Plan single_plan(int64_t tiles, int64_t nkb) {
+  constexpr Cost c = kCost<BN, kMode>;
   Plan best{1e30, 1};
-  const int64_t places = static_cast<int64_t>(num_sms()) * per_sm;
   for (int s = 1; s <= 8 && (s == 1 || nkb >= 4 * s); s *= 2) {
-    const double waves = static_cast<double>((tiles * s + places - 1) / places);
-    const double us = waves * (static_cast<double>((nkb + s - 1) / s) * block_us +
-                               (s > 1 ? 4.5 : 2.0));
+    const int64_t at_once = clusters_at_once<BN, kMode>(s);
+    const double waves = static_cast<double>((tiles + at_once - 1) / at_once);
+    const double us = waves * (static_cast<double>((nkb + s - 1) / s) * c.block + c.tile +
+                               (s == 8 ? c.join8 : s > 1 ? c.join : 0.0));
     if (us < best.us) best = Plan{us, s};
   }
   return best;
 }
 
+// A block takes a 256 x 256 pair tile 0.45 us, a 256 x 192 one of the weight gradient 0.56.
 double pair_us(int64_t tiles, int64_t nkb, bool wgrad) {
   const int64_t pairs = num_sms() / 2;
   return static_cast<double>((tiles + pairs - 1) / pairs) *
-             (static_cast<double>(nkb) * (wgrad ? 0.69 : 0.45) + 1.2) + 2.0;
+             (static_cast<double>(nkb) * (wgrad ? 0.56 : 0.45) + 1.2) + 2.0;
+}
+
+template <int BN>
+int launch_swapped(const BlockwiseGemmArgs& a, const Params& p, cudaStream_t stream) {
+  const Plan plan = single_plan<BN, kSwapped>((a.N + BM - 1) / BM, p.nkb);
+  return launch_single<BN, kSwapped>(a.B, a.N, a.A, a.M, a.K, p, plan.split, stream);
 }
 
 // From this many operations on, the gain of the block-scaled MMA for power-of-two scales
@@ -1036,18 +1088,15 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
   p.status = a.status;
   p.wait_ns = pipeline_wait_ns();
   p.drain_ns = pipeline_drain_ns();
-  if (!a.wgrad && a.M <= 128) {
+  if (!a.wgrad && a.M <= 64) {
     p.sr = a.sB;
     p.sc = a.sA;
     p.ldc = a.M;
     p.nr = a.N;
     p.nc = a.M;
-    const int64_t rt = (a.N + BM - 1) / BM;
-    const int split = single_plan(rt, p.nkb, a.M <= 64 ? 2 : 1, 0.43).split;
-    if (a.M <= 16) return launch_single<16, kSwapped>(a.B, a.N, a.A, a.M, a.K, p, split, stream);
-    if (a.M <= 32) return launch_single<32, kSwapped>(a.B, a.N, a.A, a.M, a.K, p, split, stream);
-    if (a.M <= 64) return launch_single<64, kSwapped>(a.B, a.N, a.A, a.M, a.K, p, split, stream);
-    return launch_single<128, kSwapped>(a.B, a.N, a.A, a.M, a.K, p, split, stream);
+    if (a.M <= 16) return launch_swapped<16>(a, p, stream);
+    if (a.M <= 32) return launch_swapped<32>(a, p, stream);
+    return launch_swapped<64>(a, p, stream);
   }
   p.sr = a.sA;
   p.sc = a.sB;
@@ -1090,8 +1139,9 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
     p.num_only_if = kConvertCtas;
   }
   const int bn = a.wgrad ? 192 : 256;  // columns of a pair tile
-  const Plan single = single_plan(((a.M + 127) / 128) * ((a.N + 127) / 128), p.nkb, 1,
-                                  a.wgrad ? 0.55 : 0.43);
+  const int64_t tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+  const Plan single =
+      a.wgrad ? single_plan<128, kWgrad>(tiles, p.nkb) : single_plan<128, kFprop>(tiles, p.nkb);
   if (pair_us(((a.M + 255) / 256) * ((a.N + bn - 1) / bn), p.nkb, a.wgrad) < single.us)
     return a.wgrad ? launch_pairs<192, kWgrad>(a, p, stream)
                    : launch_pairs<256, kFprop>(a, p, stream);
