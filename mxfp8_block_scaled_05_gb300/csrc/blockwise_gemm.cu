@@ -7,16 +7,23 @@
 //   C[r][c] = sum_b sr(b, r) sc(b, c) P_b[r][c],  P_b = sum over the 128 k of block b of
 //   a[r][k] w[c][k]
 // The tensor cores apply no FP32 scale, so each 128-deep product P_b is a separate FP32
-// accumulation in TMEM (tcgen05.mma kind::f8f6f4, four K = 32 steps) and the epilogue warps
-// fold it into FP32 registers: acc += (sr sc) P_b. Two TMEM accumulators alternate, so the
-// tensor cores work on block b + 1 while the warps fold block b.
+// accumulation in TMEM (tcgen05.mma kind::f8f6f4, four K = 32 steps) and the fold warps add it
+// into FP32 registers: acc += (sr sc) P_b, the product of the two scales rounded to FP32 once.
+// Two TMEM accumulators alternate, so the tensor cores work on the next block while the warps
+// fold this one. (Scales that are powers of two take another way, see the conversion
+// kernel below.)
 //
-// What bounds it: the tensor cores take 512 cycles for a 128 x 256 x 128 block per SM, the
-// fold 256 (one FMA per element, 128 lanes; 512 with a scale for every column), TMEM reads
-// 256. All overlap.
+// What bounds it: not the tensor cores (512 cycles for a 256 x 256 x 128 block of a CTA pair) nor
+// the FMAs (256), but the chain of one block: barrier wait, TMEM read, fold, barrier arrival,
+// the next block's MMA. Each hand-over through shared memory answers in 150 to 180 cycles
+// beside the TMA and MMA traffic, and a pair's block takes about 850 cycles in all. Measured
+// on GB300, BF16 results: 4096 x 24576 x 4096 315 us (2.62 PFLOP/s), 4096^3 61 us (2.25);
+// weight gradient 6144 x 4096 x 4096 135 us (1.53), with FP32 results and K = 4016 146 us.
+// Few rows are bound by the weights' bytes: 1 x 24576 x 4096 14.6 us (6.9 TB/s, part of it
+// from L2), 37 rows 22.5 us; 1 x 4096 x 4096 takes 6.0 us, mostly launch and latency.
 //
-// Roles: warp 0 TMA producer, warp 1 MMA issuer (and TMEM allocation), the last eight warps
-// fold and store, two per TMEM lane quarter, each half the columns.
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (and TMEM allocation), the last 8 or 12 warps
+// fold and store: one per TMEM lane quarter and group of columns.
 //
 // Modes, by which operand lies along the 128 TMEM lanes ("rows") and the columns:
 //   kFprop    rows = A (a scale per row and block), columns = B (128 x 128 blocks)
@@ -24,9 +31,10 @@
 //   kSwapped  rows = B, columns = A, C stored transposed: for up to 64 rows of A, where a
 //             128-row tile of A would be mostly empty. 64 x 4096 x 4096: 7.9 us, 9.1 in 128-row
 //             tiles of A; 128 x 4096 x 4096: 10.4 us so, 9.1 in 128-row tiles
-// and by size: pairs of CTAs (cta_group::2, 256 x 256 tiles, each SM stages half of the
-// column operand), or single CTAs (128 x BN tiles) whose reduction may be split over a
-// cluster, the parts joined through distributed shared memory in rank order.
+// and by size: pairs of CTAs (cta_group::2, 256 x 256 tiles, 256 x 192 of the weight gradient,
+// each SM stages half of the column operand), or single CTAs (128 x BN tiles) whose reduction
+// may be split over a cluster, the parts joined through distributed shared memory in rank
+// order. Which of them, and how many parts, is chosen by estimated time (see Cost).
 //
 // Every wait is bounded as in gemm.cu: past the limit the CTA latches MXFP8_ERR_TIMEOUT,
 // every role leaves its loop, outstanding copies and MMAs are waited for, TMEM is freed.
@@ -58,7 +66,9 @@ struct Cfg {
   static constexpr int kStageBytes = kABytes + kBBytes;
   // narrow tiles leave room for two CTAs on an SM
   static constexpr int kStages = BN < 128 ? 4 : kMode == kWgrad ? 5 : 6;
-  // four folding warps (a TMEM lane quarter each) for each group of columns
+  // four folding warps (a TMEM lane quarter each) for each group of columns. The weight
+  // gradient's pairs take 192 columns so that a warp's 64 stay in registers with their scales:
+  // 256 spilled (6144 x 4096 x 4016 FP32: 208 us; 146 with 192)
   static constexpr int kColGroups = BN == 192 ? 3 : 2;
   static constexpr int kNC = BN / kColGroups;         // columns per folding warp
   static constexpr int kFoldWarps = 4 * kColGroups;
@@ -854,7 +864,9 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
 // scales are powers of two is known on the device only: this kernel writes the scales in the
 // MMA's 128 x 4 tile layout and, for each CTA, a word that says whether it met another one.
 // The block-scaled kernel then returns at once if any word is set, the folding one if none
-// is. Measured at 4096 x 24576 x 4096: 328 us folded; the two extra launches cost 4 us.
+// is. Measured at 4096 x 24576 x 4096, BF16: 235 us (3.5 PFLOP/s), 315 folded. Scales that
+// turn out not to be powers of two pay the two other launches: 325 us; 57 and 48 at 1021 x
+// 12288 x 4096.
 constexpr int kConvertCtas = 608;  // four on each SM
 constexpr int kConvertThreads = 256;
 
@@ -1066,7 +1078,8 @@ int launch_swapped(const BlockwiseGemmArgs& a, const Params& p, cudaStream_t str
 }
 
 // From this many operations on, the gain of the block-scaled MMA for power-of-two scales
-// (a fifth to a quarter of the time) is worth what the conversion and the check cost others.
+// (1021 x 12288 x 4096: 41 us, 48 folded; larger products a quarter of the time) is worth what
+// the conversion and the check cost others.
 constexpr double kMxMinFlops = 1e11;
 
 }  // namespace

@@ -381,7 +381,9 @@ __device__ __forceinline__ void cluster_wait() {
 
 // One cluster of `split` CTAs per row; each CTA streams a contiguous part of it once.
 //
-// Bound by memory (2 or 4 bytes a logit): 16-byte loads, eight of them in flight a thread.
+// Bound by memory (2 or 4 bytes a logit): 16-byte loads, four of them in flight a thread, each
+// logit read once. 4096 x 131072 BF16: 159 us (6.7 TB/s), 180 with the 8 likeliest tokens. One
+// row of 131072 takes 3.5 us, 6.8 with the 5 likeliest.
 // Rows are split over a cluster only when there are too few of them to fill the GPU; each
 // CTA then hands its sums and best keys to the first through distributed shared memory,
 // without a workspace.
@@ -552,6 +554,7 @@ struct GradParams {
 
 // dx_v = (1/T) [ g 1(v = target) + sum_j gt_j 1(v = id_j)
 //                - p_v (g + sum gt + h (log p_v + H)) ]
+// Bound by memory: 4096 x 131072 BF16 takes 321 us, 6.7 TB/s read and written.
 // One pass: p_v comes from the saved maximum and log S, so a logit is read once and its
 // gradient written once. The few columns that a token or an alternative names are written
 // a second time, complete, by the CTA that owns them; their logits are read before

@@ -654,7 +654,9 @@ blockwise_quantize_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_
 // the 8 codes of a column in 8 consecutive bytes. They pass through shared memory (16 KB,
 // 8-byte units XOR-swizzled by the patch column) to leave as 16-byte stores. The scales of
 // the 8 rows a half-warp shares are computed by 8 of its lanes, one division each, instead
-// of 8 divisions in every lane.
+// of 8 divisions in every lane. 4096 x 12288, both copies: 35.6 us (5.6
+// TB/s; 33.2 with one scale a tile); the row-wise copy alone 21.4, the transposed one 22.2
+// (7 TB/s, part of it in L2).
 template <bool kRow, bool kCol, bool k2D>
 __global__ void __launch_bounds__(kThreads)
 blockwise_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t cols,
