@@ -376,8 +376,9 @@ size_t mxfp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int op, int o
  *                   tokens, padded as the COL copies are)
  *   C_dev           [M][N], BF16 or FP32, fully overwritten
  * Requires K % 16 == 0 and N % 8 == 0; any M (WGRAD too). Accuracy: |C - C_exact| <=
- * 2^-9 * sum_k |a_k b_k| per element before the output rounding. A NaN scale or code gives
- * NaN in the elements it reaches. Deterministic.
+ * 2^-9 * sum_k |a_k b_k| per element before the output rounding, as long as the products of
+ * its blocks' two scales, which are formed in FP32, are normal numbers or zero. A NaN scale or
+ * code gives NaN in the elements it reaches. Deterministic.
  * Empty sizes: M == 0 or N == 0 writes nothing, K == 0 zero-fills C (the operands may then
  * be NULL).
  * Errors: MXFP8_ERR_INVALID_ARG (negative or too large sizes, unknown enums, null
