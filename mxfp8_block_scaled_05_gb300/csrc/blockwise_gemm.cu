@@ -271,24 +271,20 @@ __device__ __forceinline__ void fold(float* acc, const uint32_t (&v)[G], float s
 // a lane few columns of several rows: of columns 8 j + 2 (lane % 4) and the next, rows lane / 4
 // (r[4 j], r[4 j + 1]) and lane / 4 + 8 (r[4 j + 2], r[4 j + 3]), of 16 rows and 64 columns a
 // read; column scales are read two at a time and serve four rows.
-__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32"
-      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
-      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void fold_quads(float (&acc)[8][4], const uint32_t (&r)[32], float s0,
-                                           float s1, const float2 (&c)[8]) {
+__device__ __forceinline__ void fold_quads(float (*acc)[4], const uint32_t (&r)[16], float s0,
+                                           float s1, const float2 (&c)[4]) {
   const uint64_t p0 = pack2(s0, s0), p1 = pack2(s1, s1);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     const uint64_t cc = pack2(c[j].x, c[j].y);
     const uint64_t a = fma2(pack2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])),
                             mul2(p0, cc), pack2(acc[j][0], acc[j][1]));
@@ -729,26 +725,35 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
 #pragma unroll
           for (int h = 0; h < 4; ++h) rq[h] = slot[(lane >> 2) + 8 * h];
         }
+        float2 cq[4];  // the scales of 32 of the columns
+        auto load_cq = [&](int u) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            cq[j] = *reinterpret_cast<const float2*>(slot + 32 + 32 * u + 8 * j + 2 * (lane & 3));
+        };
         ok = wait_phase(&acc_full[b], (it >> 1) & 1, abort_flag, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
         if constexpr (kQuads) {
-          float2 cq[8];
+          // four reads of 16 rows and 32 columns; the next one is under way during the fold
+          uint32_t r[2][16];
+          auto read = [&](int i) {
+            tmem_ld_quads(tbase + b * BN + (static_cast<uint32_t>(16 * (i & 1)) << 16) + 16 * (i & 2),
+                          r[i & 1]);
+          };
+          read(0);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t r[32];
-            tmem_ld_quads(tbase + b * BN + (static_cast<uint32_t>(16 * h) << 16), r);
-            if (h == 0) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                cq[j] = *reinterpret_cast<const float2*>(slot + 32 + 8 * j + 2 * (lane & 3));
-            }
-            tmem_wait(r);
-            if (h == 1) {  // the block has left TMEM
+          for (int i = 0; i < 4; ++i) {
+            if (i == 0) load_cq(0);
+            if (i == 2) load_cq(1);
+            tmem_wait(r[i & 1]);
+            if (i < 3) {
+              read(i + 1);
+            } else {  // the block has left TMEM
               tc_fence_before();
               arrive_if(lane == 0, acc_empty0 + 8 * b);
             }
-            fold_quads(quads[h], r, rq[2 * h], rq[2 * h + 1], cq);
+            fold_quads(&quads[i & 1][2 * (i & 2)], r[i & 1], rq[2 * (i & 1)], rq[2 * (i & 1) + 1], cq);
           }
         } else {
 #pragma unroll
