@@ -16,14 +16,17 @@
 // What bounds it: not the tensor cores (512 cycles for a 256 x 256 x 128 block of a CTA pair) nor
 // the FMAs (256), but the chain of one block: barrier wait, TMEM read, fold, barrier arrival,
 // the next block's MMA. Each hand-over through shared memory answers in 150 to 180 cycles
-// beside the TMA and MMA traffic, and a pair's block takes about 850 cycles in all. Measured
-// on GB300, BF16 results: 4096 x 24576 x 4096 315 us (2.62 PFLOP/s), 4096^3 61 us (2.25);
-// weight gradient 6144 x 4096 x 4096 135 us (1.53), with FP32 results and K = 4016 146 us.
-// Few rows are bound by the weights' bytes: 1 x 24576 x 4096 14.6 us (6.9 TB/s, part of it
-// from L2), 37 rows 22.5 us; 1 x 4096 x 4096 takes 6.0 us, mostly launch and latency.
+// beside the TMA and MMA traffic, and a pair's block takes about 800 cycles in all. What can
+// leave the chain does: the producer copies the scales (with each fold warp fetching its own:
+// 4096 x 24576 x 4096 317 us, 299 now; weight gradient 6144 x 4096 x 4096 132 and 112), and
+// one barrier a block says that both its product and its scales are there.
+// Measured on GB300, BF16 results: 4096 x 24576 x 4096 299 us (2.76 PFLOP/s), 4096^3 58 us
+// (2.38); weight gradient 6144 x 4096 x 4096 112 us (1.83), with FP32 results and K = 4016
+// 122 us. Few rows are bound by the weights' bytes: 1 x 24576 x 4096 14.4 us (7.0 TB/s, part
+// of it from L2), 37 rows 21 us; 1 x 4096 x 4096 takes 6.1 us, mostly launch and latency.
 //
-// Roles: warp 0 TMA producer, warp 1 MMA issuer (and TMEM allocation), the last 8 or 12 warps
-// fold and store: one per TMEM lane quarter and group of columns.
+// Roles: warp 0 TMA producer and scales, warp 1 MMA issuer (and TMEM allocation), the last 8 or
+// 12 warps fold and store: one per TMEM lane quarter and group of columns.
 //
 // Modes, by which operand lies along the 128 TMEM lanes ("rows") and the columns:
 //   kFprop    rows = A (a scale per row and block), columns = B (128 x 128 blocks)
@@ -54,7 +57,9 @@ namespace {
 
 constexpr int BM = 128;        // tile rows per CTA = TMEM lanes
 constexpr int BK = 128;        // K per block and pipeline stage
-constexpr int kScaleRing = 4;  // blocks whose scales a warp has in shared memory or on their way
+// Blocks whose scales have a place in shared memory, in groups that the fold warps hand back
+// together (one block at a time: weight gradient 6144 x 4096 x 4096 114.5 us, 112.4 by fours).
+constexpr int kScaleRing = 16, kScaleGroup = 4, kScaleGroups = kScaleRing / kScaleGroup;
 
 enum Mode : int { kFprop = 0, kWgrad = 1, kSwapped = 2 };
 
@@ -65,10 +70,10 @@ struct Cfg {
   static constexpr int kBBytes = kBRows * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   // narrow tiles leave room for two CTAs on an SM
-  static constexpr int kStages = BN < 128 ? 4 : kMode == kWgrad ? 5 : 6;
+  static constexpr int kStages = BN < 128 ? 4 : 5;
   // four folding warps (a TMEM lane quarter each) for each group of columns. The weight
   // gradient's pairs take 192 columns so that a warp's 64 stay in registers with their scales:
-  // 256 spilled (6144 x 4096 x 4016 FP32: 208 us; 146 with 192)
+  // 256 spilled (6144 x 4096 x 4016 FP32: 208 us; 159 with 192, both before other steps)
   static constexpr int kColGroups = BN == 192 ? 3 : 2;
   static constexpr int kNC = BN / kColGroups;         // columns per folding warp
   static constexpr int kFoldWarps = 4 * kColGroups;
@@ -82,10 +87,11 @@ struct Cfg {
   static constexpr int kBoxBytes = 32 * 64;
   static constexpr int kOffBox = kOffB + kStages * kBBytes;
   static constexpr int kOffScale = kOffBox + (kMode == kSwapped ? 0 : 2 * kFoldWarps * kBoxBytes);
-  static constexpr int kScaleFloats = 32 + kNC;  // a warp's row and column scales of a block
-  static constexpr int kOffBar =
-      kOffScale + (kMode == kFprop ? 0 : kFoldWarps * kScaleRing * kScaleFloats * 4);
-  static constexpr int kNumBars = 2 * kStages + 5;  // full, empty, acc_full, acc_empty, done
+  static constexpr int kRowScales = kMode == kSwapped ? 4 : BM;  // (kSwapped: one)
+  static constexpr int kColScales = kMode == kFprop ? 4 : BN;    // (kFprop: one for 128 columns)
+  static constexpr int kScaleFloats = kRowScales + kColScales;   // a tile's scales of a block
+  static constexpr int kOffBar = kOffScale + kScaleRing * kScaleFloats * 4;
+  static constexpr int kNumBars = 2 * kStages + kScaleRing + kScaleGroups + 3;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + slack for 1024-byte alignment
   static constexpr int kTmemCols = BN == 192 ? 512 : 2 * BN;  // two accumulators
@@ -183,17 +189,17 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[G]) {
   for (int i = 0; i < G; ++i) asm volatile("" : "+r"(r[i]) :: "memory");
 }
 
-// 4 bytes global -> shared, in this thread's current group of copies.
+// 4 bytes global -> shared.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
+// This thread's arrival on a barrier, once its copies so far are in.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-template <int kPending>
-__device__ __forceinline__ void cp_async_wait() {  // all but the last kPending groups are in
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // A whole warp waits for a phase, every lane for itself (one lane and a shuffle or vote took
@@ -228,6 +234,15 @@ __device__ __forceinline__ void arrive_if(bool one, uint32_t cluster_addr) {
       "setp.ne.b32 p, %1, 0;\n\t"
       "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}"
       ::"r"(cluster_addr), "r"(one ? 1 : 0)
+      : "memory");
+}
+
+__device__ __forceinline__ void arrive_if(bool one, uint64_t* bar) {  // of this CTA
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(one ? 1 : 0)
       : "memory");
 }
 
@@ -460,8 +475,9 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // pair: the leader's
   uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;  // [2]
-  uint64_t* acc_empty = acc_full + 2;    // [2]; pair: the leader's
+  uint64_t* ready = empty + kStages;            // [kScaleRing]: a block's product and scales
+  uint64_t* scale_empty = ready + kScaleRing;   // [kScaleGroups]
+  uint64_t* acc_empty = scale_empty + kScaleGroups;  // [2]; pair: the leader's
   uint64_t* mma_done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -482,22 +498,24 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
                         : static_cast<int>(static_cast<int64_t>(p.nkb) * (part + 1) / p.split);
 
   if (p.only_if && !any_word_set(p.only_if, p.num_only_if)) return;  // the whole cluster does
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+  if (warp == 0) {
+    for (int i = lane; i < C::kNumBars; i += 32) {
+      uint64_t* bar = full + i;
+      mbar_init(bar, bar < ready         ? 1
+                     : bar < scale_empty ? 1 + 32  // the MMA's commit, the producer's copies of scales
+                     : bar < acc_empty   ? C::kFoldWarps
+                     : bar < mma_done    ? (kPair ? 2 : 1) * C::kFoldWarps
+                                         : 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], (kPair ? 2 : 1) * C::kFoldWarps);
+    if (lane == 0) {
+      *abort_flag = 0;
+      for (int i = 0; i < 4; ++i) rec[i] = 0;
+      tma_prefetch_desc(&map_r);
+      tma_prefetch_desc(&map_c);
+      tma_prefetch_desc(&map_o);
     }
-    mbar_init(mma_done, 1);
-    *abort_flag = 0;
-    for (int i = 0; i < 4; ++i) rec[i] = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&map_r);
-    tma_prefetch_desc(&map_c);
-    tma_prefetch_desc(&map_o);
+    __syncwarp();
   }
   if (warp == 1) {
     if constexpr (kPair) tmem_alloc_2sm(tmem_slot, C::kTmemCols);
@@ -514,7 +532,7 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
   // each role sets its own register limit, inside its branch
   if (warp == 0) {
     if constexpr (kPair) set_max_regs_dec<kOtherRegs>();
-    // ------------------------------------------------------------- TMA producer
+    // ------------------------------------------------------------- TMA producer, scales
     const bool issuer = elect_one();
     const uint32_t full0 = kPair ? cluster_map(&full[0], 0) : smem_u32(&full[0]);
     uint32_t it = 0;
@@ -524,9 +542,17 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       tile_at(p, id, rt, ct);
       const int32_t r0 = static_cast<int32_t>(kPair ? (2 * rt + crank) * BM : rt * BM);
       const int32_t c0 = static_cast<int32_t>(ct * BN);
+      const int64_t rows_here = p.nr - r0, cols_here = p.nc - c0;
+      const float* srp = kMode == kSwapped ? p.sr + rt * p.nkb + kb0 : p.sr + kb0 * p.ldr + r0 + lane;
+      const float* scp = kMode == kFprop ? p.sc + (c0 / 128 + lane) * static_cast<int64_t>(p.nkb) + kb0
+                                         : p.sc + kb0 * p.ldc + c0 + lane;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-        if (!wait_phase(&empty[s], ph ^ 1, abort_flag, p.wait_ns)) { ok = false; break; }
+        const uint32_t sl = it % kScaleRing;
+        ok = wait_phase(&empty[s], ph ^ 1, abort_flag, p.wait_ns) &&
+             (it % kScaleGroup != 0 || wait_phase(&scale_empty[sl / kScaleGroup],
+                                                  ((it / kScaleRing) & 1) ^ 1, abort_flag, p.wait_ns));
+        if (!ok) break;
         if (issuer) {
           uint8_t* as = smem + C::kOffA + s * C::kABytes;
           uint8_t* bs = smem + C::kOffB + s * C::kBBytes;
@@ -541,8 +567,29 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
           }
         }
         __syncwarp();
+        // the block's scales; what lies past the matrix is not read: it meets zero products,
+        // unstored
+        float* slot = reinterpret_cast<float*>(smem + C::kOffScale) + sl * C::kScaleFloats;
+        if constexpr (kMode == kSwapped) {
+          if (lane == 0) cp_async4(slot, srp);
+        } else {
+#pragma unroll
+          for (int i = 0; i < BM; i += 32)
+            if (i + lane < rows_here) cp_async4(slot + i + lane, srp + i);
+        }
+        if constexpr (kMode == kFprop) {
+          if (lane < BN / 128 && 128 * lane < cols_here) cp_async4(slot + C::kRowScales + lane, scp);
+        } else {
+#pragma unroll
+          for (int i = 0; i < BN; i += 32)
+            if (i + lane < cols_here) cp_async4(slot + C::kRowScales + i + lane, scp + i);
+        }
+        srp += kMode == kSwapped ? 1 : p.ldr;
+        scp += kMode == kFprop ? 1 : p.ldc;
+        cp_async_arrive(&ready[sl]);
       }
     }
+    cp_async_wait_all();
     if (!ok && issuer) {
       *abort_flag = 1;
       latch_error(p.status, MXFP8_ERR_TIMEOUT);
@@ -590,10 +637,10 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
             else mma_f8(d, ad + 2 * k, bd + 2 * k, kId, k > 0);
           }
           if constexpr (kPair) {
-            mma_commit_2sm_mc(&acc_full[b], 3);
+            mma_commit_2sm_mc(&ready[it % kScaleRing], 3);
             mma_commit_2sm_mc(&empty[s], 3);
           } else {
-            mma_commit(&acc_full[b]);
+            mma_commit(&ready[it % kScaleRing]);
             mma_commit(&empty[s]);
           }
         }
@@ -629,65 +676,7 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     // columns a TMEM read: as many as the registers allow
     constexpr int G = kMode == kSwapped ? (kNC < 32 ? kNC : kNC / 2) : 64;
     const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * kNC;
-    // Scales travel ahead of the fold, tile after tile: with the operands' copies and the MMA
-    // on it, shared memory answers in about 180 cycles, as long as the FMAs of 64 columns
-    // take, and a load from L2 takes longer than a block.
-    //   kFprop   in registers: the scales of two blocks in use (s0, s1), of the next two under
-    //            way (nr, nc)
-    //   others   in this warp's ring of slots: 32 row scales (kSwapped: one), kNC column scales
-    uint32_t ahead_id = first_id, ahead_it = 0;
-    int ahead_kb = kb0, rows_here = 0, cols_here = 0;
-    const float *srp = nullptr, *scp = nullptr;
-    float nr[2], nc[2];
-    float* ring = reinterpret_cast<float*>(smem + C::kOffScale) +
-                  (warp - C::kFoldFirst) * kScaleRing * C::kScaleFloats;
-    auto fetch = [&]() {
-      if (ahead_id < p.tiles) {
-        if (ahead_kb == kb0) {
-          int64_t rt, ct;
-          tile_at(p, ahead_id, rt, ct);
-          const int64_t row = (kPair ? 2 * rt + crank : rt) * BM + 32 * q;
-          const int64_t col = ct * BN + half * kNC;
-          if constexpr (kColVec) {
-            rows_here = static_cast<int>(p.nr - row < 32 ? p.nr - row : 32);
-            cols_here = static_cast<int>(p.nc - col < kNC ? p.nc - col : kNC);
-            srp = kMode == kSwapped ? p.sr + rt * p.nkb + kb0 : p.sr + kb0 * p.ldr + row + lane;
-            scp = p.sc + kb0 * p.ldc + col + lane;
-          } else {
-            srp = p.sr + kb0 * p.ldr + (row + lane < p.nr ? row + lane : p.nr - 1);
-            scp = p.sc + (col < p.nc ? col : p.nc - 1) / 128 * p.nkb + kb0;
-          }
-        }
-        if constexpr (kColVec) {  // what lies past the matrix meets zero products, unstored
-          float* slot = ring + (ahead_it % kScaleRing) * C::kScaleFloats;
-          if (kMode == kSwapped ? lane == 0 : lane < rows_here) cp_async4(slot + lane, srp);
-#pragma unroll
-          for (int i = 0; i < kNC; i += 32)
-            if (i + lane < cols_here) cp_async4(slot + 32 + i + lane, scp + i);
-          srp += kMode == kSwapped ? 1 : p.ldr;
-          scp += p.ldc;
-          ++ahead_kb;
-          ++ahead_it;
-        } else {
-          nr[0] = __ldg(srp);
-          nc[0] = __ldg(scp);
-          if (ahead_kb + 1 < kb1) {
-            nr[1] = __ldg(srp + p.ldr);
-            nc[1] = __ldg(scp + 1);
-          }
-          srp += 2 * p.ldr;
-          scp += 2;
-          ahead_kb += 2;
-        }
-        if (ahead_kb >= kb1) {
-          ahead_kb = kb0;
-          ahead_id += id_step;
-        }
-      }
-      if constexpr (kColVec) cp_async_commit();  // one group a block, empty past the last
-    };
-#pragma unroll
-    for (int i = 0; i < (kColVec ? kScaleRing - 1 : 1); ++i) fetch();
+    const float* ring = reinterpret_cast<const float*>(smem + C::kOffScale);
     uint32_t it = 0;
     bool ok = true;
     for (uint32_t id = first_id; ok && id < p.tiles; id += id_step) {
@@ -701,37 +690,20 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       for (int i = 0; i < (kQuads ? 1 : kNC); ++i) acc[i] = 0.f;
 #pragma unroll
       for (int i = 0; i < 64; ++i) (&quads[0][0][0])[i] = 0.f;
-      float s0 = 0.f, s1 = 0.f;
 #pragma unroll 1
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t b = it & 1;
-        const float* slot = ring + (it % kScaleRing) * C::kScaleFloats;
-        float s = 0.f;
-        if constexpr (kColVec) {
-          cp_async_wait<kScaleRing - 2>();
-          __syncwarp();  // this block's scales are in; the slot before it is free again
-          fetch();
-          if constexpr (kMode == kSwapped) s = slot[0];
-        } else {
-          if (((kb - kb0) & 1) == 0) {
-            s0 = nr[0] * nc[0];
-            s1 = nr[1] * nc[1];
-            fetch();
-          }
-          s = ((kb - kb0) & 1) ? s1 : s0;
-        }
+        const float* rows = ring + (it % kScaleRing) * C::kScaleFloats;
+        const float* cols = rows + C::kRowScales + (kMode == kFprop ? half * kNC / 128 : half * kNC);
         float rq[4];
-        if constexpr (kQuads) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) rq[h] = slot[(lane >> 2) + 8 * h];
-        }
         float2 cq[4];  // the scales of 32 of the columns
         auto load_cq = [&](int u) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            cq[j] = *reinterpret_cast<const float2*>(slot + 32 + 32 * u + 8 * j + 2 * (lane & 3));
+            cq[j] = *reinterpret_cast<const float2*>(cols + 32 * u + 8 * j + 2 * (lane & 3));
         };
-        ok = wait_phase(&acc_full[b], (it >> 1) & 1, abort_flag, p.wait_ns);
+        const uint32_t sl = it % kScaleRing;
+        ok = wait_phase(&ready[sl], (it / kScaleRing) & 1, abort_flag, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
         if constexpr (kQuads) {
@@ -742,6 +714,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
                           r[i & 1]);
           };
           read(0);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) rq[h] = rows[32 * q + (lane >> 2) + 8 * h];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (i == 0) load_cq(0);
@@ -756,18 +730,22 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
             fold_quads(&quads[i & 1][2 * (i & 2)], r[i & 1], rq[2 * (i & 1)], rq[2 * (i & 1) + 1], cq);
           }
         } else {
+          float s = 0.f;
 #pragma unroll
           for (int g = 0; g < kNC; g += G) {
             uint32_t r[G];
             tmem_ld(tbase + b * BN + g, r);
+            if (g == 0) s = kMode == kSwapped ? rows[0] : rows[32 * q + lane] * cols[0];
             tmem_wait(r);
             if (g + G == kNC) {  // the block has left TMEM
               tc_fence_before();
               arrive_if(lane == 0, acc_empty0 + 8 * b);
             }
-            fold<G, kColVec>(acc + g, r, s, slot + 32 + g);
+            fold<G, kColVec>(acc + g, r, s, cols + g);
           }
         }
+        __syncwarp();  // every lane has read the block's scales
+        arrive_if(lane == 0 && it % kScaleGroup == kScaleGroup - 1, &scale_empty[sl / kScaleGroup]);
       }
       if (!ok) break;
       if (!kPair && p.split > 1) {
@@ -803,10 +781,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
         else store_rows<kNC>(out, p, acc, row0, col, lane);
       }
     }
-    // its stores must have finished reading shared memory before the CTA exits, and its copies
-    // writing it
+    // its stores must have finished reading shared memory before the CTA exits
     if (lane == 0) bulk_wait_read_all();
-    cp_async_wait<0>();
     __syncwarp();
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -836,7 +812,7 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     for (uint32_t i = consumed > kStages ? consumed - kStages : 0; i < consumed; ++i)
       mbar_wait_timed(&empty[i % kStages], (i / kStages) & 1, p.drain_ns);
     for (uint32_t i = consumed > 2 ? consumed - 2 : 0; i < consumed; ++i)
-      mbar_wait_timed(&acc_full[i & 1], (i >> 1) & 1, p.drain_ns);
+      mbar_wait_timed(&ready[i % kScaleRing], (i / kScaleRing) & 1, p.drain_ns);
   }
   __syncthreads();
   if constexpr (kPair) {
@@ -869,9 +845,9 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
 // scales are powers of two is known on the device only: this kernel writes the scales in the
 // MMA's 128 x 4 tile layout and, for each CTA, a word that says whether it met another one.
 // The block-scaled kernel then returns at once if any word is set, the folding one if none
-// is. Measured at 4096 x 24576 x 4096, BF16: 235 us (3.5 PFLOP/s), 315 folded. Scales that
-// turn out not to be powers of two pay the two other launches: 325 us; 57 and 48 at 1021 x
-// 12288 x 4096.
+// is. Measured, BF16: 4096 x 24576 x 4096 240 us (3.4 PFLOP/s), 299 folded; weight gradient
+// 6144 x 4096 x 4096 67 and 112. Scales that turn out not to be powers of two pay the two other
+// launches: 311 us there, 54 instead of 46 at 1021 x 12288 x 4096.
 constexpr int kConvertCtas = 608;  // four on each SM
 constexpr int kConvertThreads = 256;
 
@@ -1047,9 +1023,9 @@ struct Cost {
 template <int BN, int kMode>
 constexpr Cost kCost = BN == 16   ? Cost{0.275, 2.4, 1.2, 3.0}
                        : BN == 32 ? Cost{0.29, 3.1, 1.1, 3.7}
-                       : BN == 64 ? Cost{0.345, 3.8, 1.3, 5.8}
-                       : kMode == kFprop ? Cost{0.32, 3.2, 3.2, 6.0}
-                                         : Cost{0.445, 3.3, 3.0, 6.0};
+                       : BN == 64 ? Cost{0.33, 3.8, 1.3, 5.8}
+                       : kMode == kFprop ? Cost{0.33, 3.2, 3.2, 6.0}
+                                         : Cost{0.38, 3.3, 3.0, 6.0};
 struct Plan {
   double us;
   int split;
@@ -1069,11 +1045,11 @@ Plan single_plan(int64_t tiles, int64_t nkb) {
   return best;
 }
 
-// A block takes a 256 x 256 pair tile 0.45 us, a 256 x 192 one of the weight gradient 0.56.
+// A block takes a 256 x 256 pair tile 0.42 us, a 256 x 192 one of the weight gradient 0.47.
 double pair_us(int64_t tiles, int64_t nkb, bool wgrad) {
   const int64_t pairs = num_sms() / 2;
   return static_cast<double>((tiles + pairs - 1) / pairs) *
-             (static_cast<double>(nkb) * (wgrad ? 0.56 : 0.45) + 1.2) + 2.0;
+             (static_cast<double>(nkb) * (wgrad ? 0.47 : 0.42) + 1.2) + 2.0;
 }
 
 template <int BN>
@@ -1083,8 +1059,8 @@ int launch_swapped(const BlockwiseGemmArgs& a, const Params& p, cudaStream_t str
 }
 
 // From this many operations on, the gain of the block-scaled MMA for power-of-two scales
-// (1021 x 12288 x 4096: 41 us, 48 folded; larger products a quarter of the time) is worth what
-// the conversion and the check cost others.
+// (1021 x 12288 x 4096: 41 us, 46 folded; more for larger products) is about what the
+// conversion and the check cost others (54 us), or more.
 constexpr double kMxMinFlops = 1e11;
 
 }  // namespace
