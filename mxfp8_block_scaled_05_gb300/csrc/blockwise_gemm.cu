@@ -22,8 +22,8 @@
 // one barrier a block says that both its product and its scales are there.
 // Measured on GB300, BF16 results: 4096 x 24576 x 4096 299 us (2.76 PFLOP/s), 4096^3 58 us
 // (2.38); weight gradient 6144 x 4096 x 4096 112 us (1.83), with FP32 results and K = 4016
-// 122 us. Few rows are bound by the weights' bytes: 1 x 24576 x 4096 14.4 us (7.0 TB/s, part
-// of it from L2), 37 rows 21 us; 1 x 4096 x 4096 takes 6.1 us, mostly launch and latency.
+// 122 us. Few rows are bound by the weights' bytes: 1 x 24576 x 4096 13 us (7.8 TB/s, part of
+// it from L2), 37 rows 21 us; 1 x 4096 x 4096 takes 5.8 us, mostly launch and latency.
 //
 // Roles: warp 0 TMA producer and scales, warp 1 MMA issuer (and TMEM allocation), the last 8 or
 // 12 warps fold and store: one per TMEM lane quarter and group of columns.
@@ -32,8 +32,8 @@
 //   kFprop    rows = A (a scale per row and block), columns = B (128 x 128 blocks)
 //   kWgrad    both with a scale per row / column and block
 //   kSwapped  rows = B, columns = A, C stored transposed: for up to 64 rows of A, where a
-//             128-row tile of A would be mostly empty. 64 x 4096 x 4096: 7.9 us, 9.1 in 128-row
-//             tiles of A; 128 x 4096 x 4096: 10.4 us so, 9.1 in 128-row tiles
+//             128-row tile of A would be mostly empty: 64 x 4096 x 4096 7.8 us, 8.8 in 128-row
+//             tiles of A (128 x 4096 x 4096: 10.4 swapped, 8.8 in those)
 // and by size: pairs of CTAs (cta_group::2, 256 x 256 tiles, 256 x 192 of the weight gradient,
 // each SM stages half of the column operand), or single CTAs (128 x BN tiles) whose reduction
 // may be split over a cluster, the parts joined through distributed shared memory in rank
@@ -202,11 +202,9 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// A whole warp waits for a phase, every lane for itself (one lane and a shuffle or vote took
-// longer); true for all lanes or for none, and the warp is converged again. The clock is
-// read, and the abort flag looked at, only once 64 polls have failed: the fold's hand-overs
-// are on the critical path.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
+// Waits for a phase, within a limit. The clock is read, and the abort flag looked at, only once
+// 64 polls have failed: the hand-overs of the fold are on the critical path.
+__device__ __forceinline__ bool poll_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
                                            uint64_t limit_ns) {
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) {
@@ -222,7 +220,14 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
       }
     }
   }
-  ok = __all_sync(0xFFFFFFFFu, ok);
+  return ok;
+}
+
+// A whole warp waits, every lane for itself (one lane and a shuffle or vote took longer); true
+// for all lanes or for none, and the warp is converged again.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                           uint64_t limit_ns) {
+  const bool ok = __all_sync(0xFFFFFFFFu, poll_phase(bar, parity, abort, limit_ns));
   __syncwarp();  // a vote does not reconverge the warp, as the .aligned instructions need it
   return ok;
 }
@@ -619,12 +624,18 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     const uint64_t a_desc0 = smem_desc(smem_u32(smem + C::kOffA), 16, 1024, 2);
     const uint64_t b_desc0 = smem_desc(smem_u32(smem + C::kOffB), 16, 1024, 2);
     constexpr uint32_t kId = f8_idesc(kPair ? 2 * BM : BM, BN);
-    for (uint32_t id = first_id; ok && id < p.tiles; id += id_step) {
+    // A single CTA's blocks take half as long as a pair's, and the vote after each wait of a whole
+    // warp would be a tenth of one: there the issuing thread goes alone (512 x 4096 x 12288: 29.5
+    // us, 35.8 as a warp). Pairs lose 2% that way.
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return kPair ? wait_phase(bar, parity, abort_flag, p.wait_ns)
+                   : poll_phase(bar, parity, abort_flag, p.wait_ns);
+    };
+    for (uint32_t id = first_id; (kPair || issuer) && ok && id < p.tiles; id += id_step) {
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1;
         const uint32_t b = it & 1, aph = (it >> 1) & 1;
-        ok = wait_phase(&full[s], ph, abort_flag, p.wait_ns) &&
-             wait_phase(&acc_empty[b], aph ^ 1, abort_flag, p.wait_ns);
+        ok = wait(&full[s], ph) && wait(&acc_empty[b], aph ^ 1);
         if (!ok) break;
         tc_fence_after();
         const uint64_t ad = a_desc0 + s * (C::kABytes / 16);
@@ -644,9 +655,10 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
             mma_commit(&empty[s]);
           }
         }
-        __syncwarp();
+        if constexpr (kPair) __syncwarp();
       }
     }
+    __syncwarp();
     if (!ok && issuer) {
       *abort_flag = 1;
       latch_error(p.status, MXFP8_ERR_TIMEOUT);
@@ -1021,11 +1033,11 @@ struct Cost {
   double block, tile, join, join8;
 };
 template <int BN, int kMode>
-constexpr Cost kCost = BN == 16   ? Cost{0.275, 2.4, 1.2, 3.0}
-                       : BN == 32 ? Cost{0.29, 3.1, 1.1, 3.7}
-                       : BN == 64 ? Cost{0.33, 3.8, 1.3, 5.8}
-                       : kMode == kFprop ? Cost{0.33, 3.2, 3.2, 6.0}
-                                         : Cost{0.38, 3.3, 3.0, 6.0};
+constexpr Cost kCost = BN == 16   ? Cost{0.24, 2.7, 1.2, 3.0}
+                       : BN == 32 ? Cost{0.265, 3.1, 1.1, 3.9}
+                       : BN == 64 ? Cost{0.29, 4.0, 1.9, 5.8}
+                       : kMode == kFprop ? Cost{0.265, 3.3, 3.0, 6.0}
+                                         : Cost{0.365, 3.6, 2.8, 6.0};
 struct Plan {
   double us;
   int split;
