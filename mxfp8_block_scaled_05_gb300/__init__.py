@@ -512,7 +512,7 @@ def blockwise_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     """C[M, N] = deq(A)[M, K] . deq(B)[N, K]^T of block-wise FP8 operands (both K-major). A
     and sa as quantize_blockwise_1d writes them; B and sb as quantize_blockwise does (128 x
     128 blocks), or for WGRAD as quantize_blockwise_1d does. K % 16 == 0, N % 8 == 0. Large
-    products to BF16 take a workspace of blockwise_gemm_workspace_bytes(...) bytes, in which scales
+    products take a workspace of blockwise_gemm_workspace_bytes(...) bytes, in which scales
     are laid out for the block-scaled MMA if all are powers of two; without one given (a uint8
     CUDA tensor) it is allocated for the call."""
     _require(a, torch.uint8, "A")

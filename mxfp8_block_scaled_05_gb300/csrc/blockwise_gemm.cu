@@ -34,6 +34,9 @@
 //   kSwapped  rows = B, columns = A, C stored transposed: for up to 64 rows of A, where a
 //             128-row tile of A would be mostly empty: 64 x 4096 x 4096 7.8 us, 8.8 in 128-row
 //             tiles of A (128 x 4096 x 4096: 10.4 swapped, 8.8 in those)
+//   kMx       both with power-of-two scales, as E8M0 scales of the block-scaled MMA: FP32 results
+//             of those (see the conversion kernel). TMEM adds up four blocks, the fold warps
+//             those sums. 6144 x 4096 x 4096 80 us, 119 with the scales folded in
 // and by size: pairs of CTAs (cta_group::2, 256 x 256 tiles, 256 x 192 of the weight gradient,
 // each SM stages half of the column operand), or single CTAs (128 x BN tiles) whose reduction
 // may be split over a cluster, the parts joined through distributed shared memory in rank
@@ -61,7 +64,7 @@ constexpr int BK = 128;        // K per block and pipeline stage
 // together (one block at a time: weight gradient 6144 x 4096 x 4096 114.5 us, 112.4 by fours).
 constexpr int kScaleRing = 16, kScaleGroup = 4, kScaleGroups = kScaleRing / kScaleGroup;
 
-enum Mode : int { kFprop = 0, kWgrad = 1, kSwapped = 2 };
+enum Mode : int { kFprop = 0, kWgrad = 1, kSwapped = 2, kMx = 3 };
 
 template <int BN, int kMode, bool kPair>
 struct Cfg {
@@ -69,12 +72,16 @@ struct Cfg {
   static constexpr int kABytes = BM * BK;
   static constexpr int kBBytes = kBRows * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
+  // kMx: E8M0 scale tiles of 128 rows, one of A and two of B (192 rows start within the first)
+  static constexpr int kSfBytes = kMode == kMx ? 3 * 512 : 0;
+  static constexpr int kTxBytes = kStageBytes + kSfBytes;
+  static constexpr int kChunk = kMode == kMx ? 4 : 1;  // blocks that TMEM adds up before the fold
   // narrow tiles leave room for two CTAs on an SM
-  static constexpr int kStages = BN < 128 ? 4 : 5;
+  static constexpr int kStages = kMode == kMx ? 7 : BN < 128 ? 4 : 5;
   // four folding warps (a TMEM lane quarter each) for each group of columns. The weight
   // gradient's pairs take 192 columns so that a warp's 64 stay in registers with their scales:
   // 256 spilled (6144 x 4096 x 4016 FP32: 208 us; 159 with 192, both before other steps)
-  static constexpr int kColGroups = BN == 192 ? 3 : 2;
+  static constexpr int kColGroups = BN == 192 && kMode == kWgrad ? 3 : 2;
   static constexpr int kNC = BN / kColGroups;         // columns per folding warp
   static constexpr int kFoldWarps = 4 * kColGroups;
   // warps 0 and 1 copy and issue; a pair has two idle ones after them, because registers move
@@ -85,17 +92,22 @@ struct Cfg {
   static constexpr int kOffB = kOffA + kStages * kABytes;
   // store staging: two 32-row x 64-byte boxes per folding warp, 1024-byte aligned
   static constexpr int kBoxBytes = 32 * 64;
+  static constexpr int kBoxes = kMode == kMx ? 1 : 2;  // (kMx needs the room for its stages)
   static constexpr int kOffBox = kOffB + kStages * kBBytes;
-  static constexpr int kOffScale = kOffBox + (kMode == kSwapped ? 0 : 2 * kFoldWarps * kBoxBytes);
+  static constexpr int kOffScale = kOffBox + (kMode == kSwapped ? 0 : kBoxes * kFoldWarps * kBoxBytes);
   static constexpr int kRowScales = kMode == kSwapped ? 4 : BM;  // (kSwapped: one)
   static constexpr int kColScales = kMode == kFprop ? 4 : BN;    // (kFprop: one for 128 columns)
   static constexpr int kScaleFloats = kRowScales + kColScales;   // a tile's scales of a block
-  static constexpr int kOffBar = kOffScale + kScaleRing * kScaleFloats * 4;
+  static constexpr int kOffBar =
+      kOffScale + (kMode == kMx ? kStages * kSfBytes : kScaleRing * kScaleFloats * 4);
+  // TMEM: two accumulators; kMx: then the scales of the stages, 4 columns of A and 8 of B
+  static constexpr int kSfaCol = 2 * BN, kSfbCol = kSfaCol + 4 * kStages;
   static constexpr int kNumBars = 2 * kStages + kScaleRing + kScaleGroups + 3;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + slack for 1024-byte alignment
   static constexpr int kTmemCols = BN == 192 ? 512 : 2 * BN;  // two accumulators
   static constexpr int kMinCtas = BN <= 64 ? 2 : 1;
+  static_assert(kMode != kMx || kSfbCol + 8 * kStages <= kTmemCols, "TMEM columns");
   static_assert(kTmemCols >= 32 && kTmemCols <= 512, "TMEM columns");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory overflow");
   // split-K partial sums: [row][column], or (kSwapped) [column][row]; the padding keeps the
@@ -107,8 +119,8 @@ struct Cfg {
 
 // Pairs need more registers for their sums than an even share: the folding warpgroups take
 // some over from the first one (12 warps x 168 = 8 x 224 + 4 x 56; 16 x 128 = 12 x 152 + 4 x 56).
-template <int BN>
-constexpr int kFoldRegs = BN == 192 ? 152 : 224;
+template <int kFoldWarps>
+constexpr int kFoldRegs = kFoldWarps == 12 ? 152 : 224;
 constexpr int kOtherRegs = 56;
 
 struct Params {
@@ -128,6 +140,8 @@ struct Params {
   // the kernel returns at once unless one of these words is set (nullptr: it runs)
   const uint32_t* only_if;
   int num_only_if;
+  const uint32_t* unless;  // and at once if one of these is
+  int num_unless;
 };
 
 // Tile `id` of a banded raster: bands of `band` row tiles sweep across the columns, rows
@@ -322,11 +336,12 @@ __device__ __forceinline__ void store_one(const Params& p, int64_t at, float v) 
     static_cast<uint16_t*>(p.C)[at] = static_cast<uint16_t>(cvt_bf16x2(0.f, v));
 }
 
-// A warp's 32 rows x kNC columns of the tile leave through two staging boxes in turn: each
+// A warp's 32 rows x kNC columns of the tile leave through kBoxes staging boxes in turn: each
 // 64-byte column group is written into a box (16-byte chunks XOR-swizzled as the tensor map's
 // 64-byte swizzle expects) and sent with one TMA store, clipped at the matrix edge. Stores of
 // one row per lane touch 32 cache lines an instruction: with those, a tile's stores took 2.5
 // us, a sixth of the tile at K = 4096.
+template <int kBoxes>
 struct BoxStore {
   const CUtensorMap* map;
   uint8_t* boxes;
@@ -334,16 +349,16 @@ struct BoxStore {
 
   // the box to write into, free again
   __device__ __forceinline__ uint8_t* open(int lane) {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
     __syncwarp();
-    return boxes + (turn & 1) * (32 * 64);
+    return boxes + turn % kBoxes * (32 * 64);
   }
   // its first column and row
   __device__ __forceinline__ void send(int64_t col, int64_t row, int lane) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(map, boxes + (turn & 1) * (32 * 64), static_cast<int32_t>(col),
+      tma_store_2d(map, boxes + turn % kBoxes * (32 * 64), static_cast<int32_t>(col),
                    static_cast<int32_t>(row));
       bulk_commit_group();
     }
@@ -352,8 +367,8 @@ struct BoxStore {
 };
 
 // Sums held one row per lane (acc[i]: column i).
-template <int kNC>
-__device__ __forceinline__ void store_rows(BoxStore& out, const Params& p, const float (&acc)[kNC],
+template <int kNC, int kBoxes>
+__device__ __forceinline__ void store_rows(BoxStore<kBoxes>& out, const Params& p, const float (&acc)[kNC],
                                            int64_t row0, int64_t c0, int lane) {
   if (row0 >= p.nr) return;
 #pragma unroll
@@ -382,7 +397,7 @@ __device__ __forceinline__ void store_rows(BoxStore& out, const Params& p, const
 }
 
 // Sums held in quads (see fold_quads).
-__device__ __forceinline__ void store_quads(BoxStore& out, const Params& p,
+__device__ __forceinline__ void store_quads(BoxStore<2>& out, const Params& p,
                                             const float (&acc)[2][8][4], int64_t row0, int64_t c0,
                                             int lane) {
   if (row0 >= p.nr) return;
@@ -472,7 +487,9 @@ template <int BN, int kMode, bool kPair>
 __global__ void __launch_bounds__(Cfg<BN, kMode, kPair>::kThreads, Cfg<BN, kMode, kPair>::kMinCtas)
 blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
                       const __grid_constant__ CUtensorMap map_c,
-                      const __grid_constant__ CUtensorMap map_o, const Params p) {
+                      const __grid_constant__ CUtensorMap map_o,
+                      const __grid_constant__ CUtensorMap map_sr,  // kMx: the scales' tiles
+                      const __grid_constant__ CUtensorMap map_sc, const Params p) {
   using C = Cfg<BN, kMode, kPair>;
   constexpr int kStages = C::kStages, kNC = C::kNC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -488,7 +505,7 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   // drain records: [0] / [1] stage uses issued by the producer of CTA 0 / 1 of the pair (a
   // single CTA writes both), [2] stage uses consumed by the MMA issuer (one accumulator
-  // commit each), [3] this CTA's producer tail completed
+  // commit each), [3] this CTA's producer tail completed, [4] accumulators committed
   volatile uint32_t* rec = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 8);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -503,18 +520,23 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
                         : static_cast<int>(static_cast<int64_t>(p.nkb) * (part + 1) / p.split);
 
   if (p.only_if && !any_word_set(p.only_if, p.num_only_if)) return;  // the whole cluster does
+  if (kMode == kMx && p.unless && any_word_set(p.unless, p.num_unless)) return;
   if (warp == 0) {
     for (int i = lane; i < C::kNumBars; i += 32) {
       uint64_t* bar = full + i;
       mbar_init(bar, bar < ready         ? 1
-                     : bar < scale_empty ? 1 + 32  // the MMA's commit, the producer's copies of scales
+                     : bar < scale_empty ? (kMode == kMx ? 1 : 1 + 32)  // the MMA's commit, the scales' copies
                      : bar < acc_empty   ? C::kFoldWarps
                      : bar < mma_done    ? (kPair ? 2 : 1) * C::kFoldWarps
                                          : 1);
     }
     if (lane == 0) {
       *abort_flag = 0;
-      for (int i = 0; i < 4; ++i) rec[i] = 0;
+      for (int i = 0; i < 5; ++i) rec[i] = 0;
+      if constexpr (kMode == kMx) {
+        tma_prefetch_desc(&map_sr);
+        tma_prefetch_desc(&map_sc);
+      }
       tma_prefetch_desc(&map_r);
       tma_prefetch_desc(&map_c);
       tma_prefetch_desc(&map_o);
@@ -555,16 +577,22 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
         const uint32_t s = it % kStages, ph = (it / kStages) & 1;
         const uint32_t sl = it % kScaleRing;
         ok = wait_phase(&empty[s], ph ^ 1, abort_flag, p.wait_ns) &&
-             (it % kScaleGroup != 0 || wait_phase(&scale_empty[sl / kScaleGroup],
+             (kMode == kMx || it % kScaleGroup != 0 ||
+              wait_phase(&scale_empty[sl / kScaleGroup],
                                                   ((it / kScaleRing) & 1) ^ 1, abort_flag, p.wait_ns));
         if (!ok) break;
         if (issuer) {
           uint8_t* as = smem + C::kOffA + s * C::kABytes;
           uint8_t* bs = smem + C::kOffB + s * C::kBBytes;
           if constexpr (kPair) {
-            if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+            if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kTxBytes);
             tma_load_2d_2sm(as, &map_r, kb * BK, r0, full0 + 8 * s);
             tma_load_2d_2sm(bs, &map_c, kb * BK, c0 + crank * (BN / 2), full0 + 8 * s);
+            if constexpr (kMode == kMx) {
+              uint8_t* sf = smem + C::kOffScale + s * C::kSfBytes;
+              tma_load_3d_2sm(sf, &map_sr, 0, kb, r0 / BM, full0 + 8 * s);
+              tma_load_3d_2sm(sf + 512, &map_sc, 0, kb, c0 / BM, full0 + 8 * s);
+            }
           } else {
             mbar_arrive_expect_tx(&full[s], C::kStageBytes);
             tma_load_2d(as, &map_r, kb * BK, r0, &full[s]);
@@ -574,6 +602,7 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
         __syncwarp();
         // the block's scales; what lies past the matrix is not read: it meets zero products,
         // unstored
+        if constexpr (kMode == kMx) continue;
         float* slot = reinterpret_cast<float*>(smem + C::kOffScale) + sl * C::kScaleFloats;
         if constexpr (kMode == kSwapped) {
           if (lane == 0) cp_async4(slot, srp);
@@ -623,39 +652,65 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     bool ok = true;
     const uint64_t a_desc0 = smem_desc(smem_u32(smem + C::kOffA), 16, 1024, 2);
     const uint64_t b_desc0 = smem_desc(smem_u32(smem + C::kOffB), 16, 1024, 2);
+    const uint64_t sf_desc0 = smem_desc(smem_u32(smem + C::kOffScale), 0, 128, 0);
     constexpr uint32_t kId = f8_idesc(kPair ? 2 * BM : BM, BN);
     // A single CTA's blocks take half as long as a pair's, and the vote after each wait of a whole
     // warp would be a tenth of one: there the issuing thread goes alone (512 x 4096 x 12288: 29.5
-    // us, 35.8 as a warp). Pairs lose 2% that way.
+    // us, 35.8 as a warp), and in kMx, where the MMAs are the chain (80 us, 100 as a warp and
+    // with the tile's place worked out at every block). Other pairs lose 2% that way.
+    constexpr bool kWarpIssues = kPair && kMode != kMx;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return kPair ? wait_phase(bar, parity, abort_flag, p.wait_ns)
-                   : poll_phase(bar, parity, abort_flag, p.wait_ns);
+      return kWarpIssues ? wait_phase(bar, parity, abort_flag, p.wait_ns)
+                         : poll_phase(bar, parity, abort_flag, p.wait_ns);
     };
-    for (uint32_t id = first_id; (kPair || issuer) && ok && id < p.tiles; id += id_step) {
+    uint32_t acc_it = 0;
+    for (uint32_t id = first_id; (kWarpIssues || issuer) && ok && id < p.tiles; id += id_step) {
+      uint32_t sfb_shift = 0;
+      if constexpr (kMode == kMx) {
+        int64_t rt, ct;
+        tile_at(p, id, rt, ct);
+        sfb_shift = static_cast<uint32_t>(ct * BN % BM / 32);
+      }
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-        const uint32_t b = it & 1, aph = (it >> 1) & 1;
-        ok = wait(&full[s], ph) && wait(&acc_empty[b], aph ^ 1);
+        const uint32_t b = acc_it & 1, aph = (acc_it >> 1) & 1;
+        const bool starts = C::kChunk == 1 || (kb - kb0) % C::kChunk == 0;
+        const bool ends = C::kChunk == 1 || (kb - kb0) % C::kChunk == C::kChunk - 1 || kb == kb1 - 1;
+        ok = wait(&full[s], ph) && (!starts || wait(&acc_empty[b], aph ^ 1));
         if (!ok) break;
         tc_fence_after();
         const uint64_t ad = a_desc0 + s * (C::kABytes / 16);
         const uint64_t bd = b_desc0 + s * (C::kBBytes / 16);
         const uint32_t d = tmem + b * BN;
         if (issuer) {  // a K step of 32 starts 32 bytes further; past K the tiles are zero
+          if constexpr (kMode == kMx) {
+            // the stage's scales into TMEM; 192 columns start on or 64 rows into a tile of B's
+            const uint32_t sfa = tmem + C::kSfaCol + 4 * s, sfb = tmem + C::kSfbCol + 8 * s;
+            const uint64_t sd = sf_desc0 + s * (C::kSfBytes / 16);
+            tmem_cp_32x128b_x4_2sm(sfa, sd);
+            tmem_cp_32x128b_x4_2sm(sfb, sd + 512 / 16);
+            tmem_cp_32x128b_x4_2sm(sfb + 4, sd + 1024 / 16);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if constexpr (kPair) mma_f8_2sm(d, ad + 2 * k, bd + 2 * k, kId, k > 0);
-            else mma_f8(d, ad + 2 * k, bd + 2 * k, kId, k > 0);
+            for (int k = 0; k < 4; ++k)
+              mma_mxf8_2sm(d, ad + 2 * k, bd + 2 * k, mxf8_idesc(2 * BM, BN, k, k), sfa, sfb + sfb_shift,
+                           !starts || k > 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (kPair) mma_f8_2sm(d, ad + 2 * k, bd + 2 * k, kId, k > 0);
+              else mma_f8(d, ad + 2 * k, bd + 2 * k, kId, k > 0);
+            }
           }
           if constexpr (kPair) {
-            mma_commit_2sm_mc(&ready[it % kScaleRing], 3);
+            if (ends) mma_commit_2sm_mc(&ready[acc_it % kScaleRing], 3);
             mma_commit_2sm_mc(&empty[s], 3);
           } else {
-            mma_commit(&ready[it % kScaleRing]);
+            mma_commit(&ready[acc_it % kScaleRing]);
             mma_commit(&empty[s]);
           }
         }
-        if constexpr (kPair) __syncwarp();
+        if (ends) ++acc_it;
+        if constexpr (kWarpIssues) __syncwarp();
       }
     }
     __syncwarp();
@@ -667,26 +722,30 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       if constexpr (kPair) {
         for (uint32_t r = 0; r < 2; ++r)
           st_cluster_u32(cluster_map(const_cast<uint32_t*>(&rec[2]), r), it);
+        for (uint32_t r = 0; r < 2; ++r)
+          st_cluster_u32(cluster_map(const_cast<uint32_t*>(&rec[4]), r), acc_it);
         mma_commit_2sm_mc(mma_done, 1);
       } else {
         rec[2] = it;
+        rec[4] = acc_it;
         mma_commit(mma_done);
       }
       mbar_wait_timed(mma_done, 0, p.drain_ns);
     }
     __syncwarp();
   } else {
-    if constexpr (kPair) set_max_regs_inc<kFoldRegs<BN>>();
+    if constexpr (kPair) set_max_regs_inc<kFoldRegs<C::kFoldWarps>>();
     // ------------------------------------------------------------- fold and store
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
     const int half = (warp - C::kFoldFirst) >> 2;  // which group of the columns
-    BoxStore out{&map_o, smem + C::kOffBox + (warp - C::kFoldFirst) * 2 * C::kBoxBytes, 0};
+    BoxStore<C::kBoxes> out{
+        &map_o, smem + C::kOffBox + (warp - C::kFoldFirst) * C::kBoxes * C::kBoxBytes, 0};
     const uint32_t acc_empty0 = kPair ? cluster_map(&acc_empty[0], 0) : smem_u32(&acc_empty[0]);
-    constexpr bool kColVec = kMode != kFprop;
+    constexpr bool kColVec = kMode == kWgrad || kMode == kSwapped;
     constexpr bool kQuads = kMode == kWgrad;
     static_assert(!kQuads || kNC == 64, "a warp of the weight gradient folds 64 columns");
     // columns a TMEM read: as many as the registers allow
-    constexpr int G = kMode == kSwapped ? (kNC < 32 ? kNC : kNC / 2) : 64;
+    constexpr int G = kMode == kSwapped ? (kNC < 32 ? kNC : kNC / 2) : kMode == kMx ? 32 : 64;
     const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * kNC;
     const float* ring = reinterpret_cast<const float*>(smem + C::kOffScale);
     uint32_t it = 0;
@@ -703,7 +762,7 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
 #pragma unroll
       for (int i = 0; i < 64; ++i) (&quads[0][0][0])[i] = 0.f;
 #pragma unroll 1
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      for (int kb = kb0; kb < kb1; kb += C::kChunk, ++it) {  // `it` counts accumulators
         const uint32_t b = it & 1;
         const float* rows = ring + (it % kScaleRing) * C::kScaleFloats;
         const float* cols = rows + C::kRowScales + (kMode == kFprop ? half * kNC / 128 : half * kNC);
@@ -747,15 +806,25 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
           for (int g = 0; g < kNC; g += G) {
             uint32_t r[G];
             tmem_ld(tbase + b * BN + g, r);
-            if (g == 0) s = kMode == kSwapped ? rows[0] : rows[32 * q + lane] * cols[0];
+            if (g == 0 && kMode != kMx)
+              s = kMode == kSwapped ? rows[0] : rows[32 * q + lane] * cols[0];
             tmem_wait(r);
             if (g + G == kNC) {  // the block has left TMEM
               tc_fence_before();
               arrive_if(lane == 0, acc_empty0 + 8 * b);
             }
-            fold<G, kColVec>(acc + g, r, s, cols + g);
+            if constexpr (kMode == kMx) {
+#pragma unroll
+              for (int i = 0; i < G; i += 2)
+                unpack2(add2(pack2(acc[g + i], acc[g + i + 1]),
+                             pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]))),
+                        acc[g + i], acc[g + i + 1]);
+            } else {
+              fold<G, kColVec>(acc + g, r, s, cols + g);
+            }
           }
         }
+        if constexpr (kMode == kMx) continue;
         __syncwarp();  // every lane has read the block's scales
         arrive_if(lane == 0 && it % kScaleGroup == kScaleGroup - 1, &scale_empty[sl / kScaleGroup]);
       }
@@ -815,15 +884,15 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     if (leader) {
       for (uint32_t i = consumed; kPair && i < issued; ++i) {
         uint64_t* bar = &full[i % kStages];
-        if (i < i0 && i >= i1) mbar_complete_tx(bar, C::kStageBytes);
-        else if (i >= i0 && i < i1) mbar_arrive_expect_tx(bar, C::kStageBytes);
+        if (i < i0 && i >= i1) mbar_complete_tx(bar, C::kTxBytes);
+        else if (i >= i0 && i < i1) mbar_arrive_expect_tx(bar, C::kTxBytes);
       }
       for (uint32_t i = consumed; i < issued; ++i)
         mbar_wait_timed(&full[i % kStages], (i / kStages) & 1, p.drain_ns);
     }
     for (uint32_t i = consumed > kStages ? consumed - kStages : 0; i < consumed; ++i)
       mbar_wait_timed(&empty[i % kStages], (i / kStages) & 1, p.drain_ns);
-    for (uint32_t i = consumed > 2 ? consumed - 2 : 0; i < consumed; ++i)
+    for (uint32_t i = rec[4] > 2 ? rec[4] - 2 : 0; i < rec[4]; ++i)
       mbar_wait_timed(&ready[i % kScaleRing], (i / kScaleRing) & 1, p.drain_ns);
   }
   __syncthreads();
@@ -857,9 +926,13 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
 // scales are powers of two is known on the device only: this kernel writes the scales in the
 // MMA's 128 x 4 tile layout and, for each CTA, a word that says whether it met another one.
 // The block-scaled kernel then returns at once if any word is set, the folding one if none
-// is. Measured, BF16: 4096 x 24576 x 4096 240 us (3.4 PFLOP/s), 299 folded; weight gradient
-// 6144 x 4096 x 4096 67 and 112. Scales that turn out not to be powers of two pay the two other
-// launches: 311 us there, 54 instead of 46 at 1021 x 12288 x 4096.
+// is. BF16 results come from mxfp8_gemm. The tensor cores' own sum over all of K is 2e-6 off (K =
+// 4096), which a BF16 result's rounding covers; for FP32 results kMx takes only 512 products at
+// a time from them (3e-7 off) and adds those up in FP32 registers.
+// Measured, BF16: 4096 x 24576 x 4096 240 us (3.4 PFLOP/s), 299 folded; weight gradient 6144 x
+// 4096 x 4096 67 and 112; FP32: 80 and 119, 4096 x 12288 x 8192 277 and 440. Scales that turn
+// out not to be powers of two pay the two other launches: 311 us for the first, 54 instead of
+// 46 at 1021 x 12288 x 4096.
 constexpr int kConvertCtas = 608;  // four on each SM
 constexpr int kConvertThreads = 256;
 
@@ -933,8 +1006,9 @@ auto ready_kernel() -> decltype(&blockwise_gemm_kernel<BN, kMode, kPair>) {
 }
 
 template <int BN, int kMode, bool kPair>
-int launch(const CUtensorMap& mr, const CUtensorMap& mc, const CUtensorMap& mo, const Params& p,
-           int64_t grid, int cluster, cudaStream_t stream) {
+int launch(const CUtensorMap& mr, const CUtensorMap& mc, const CUtensorMap& mo,
+           const CUtensorMap& msr, const CUtensorMap& msc, const Params& p, int64_t grid,
+           int cluster, cudaStream_t stream) {
   auto k = ready_kernel<BN, kMode, kPair>();
   if (!k) return MXFP8_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -952,7 +1026,7 @@ int launch(const CUtensorMap& mr, const CUtensorMap& mc, const CUtensorMap& mo, 
     attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
   }
-  return cudaLaunchKernelEx(&cfg, k, mr, mc, mo, p) == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k, mr, mc, mo, msr, msc, p) == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
 }
 
 // 256 x BN tiles on CTA pairs. `a` is the row operand.
@@ -972,7 +1046,12 @@ int launch_pairs(const BlockwiseGemmArgs& a, Params p, cudaStream_t stream) {
   p.band = p.row_tiles < 8 ? p.row_tiles : 8;
   p.split = 1;
   const int64_t pairs = num_sms() / 2;
-  return launch<BN, kMode, true>(mr, mc, mo, p, 2 * (tiles < pairs ? tiles : pairs), 2, stream);
+  CUtensorMap msr = mr, msc = mc;  // unused but for kMx
+  if (kMode == kMx &&
+      (!make_scale_map(&msr, p.sr, (a.M + 127) / 128, p.nkb, 1) ||
+       !make_scale_map(&msc, p.sc, (a.N + 127) / 128, p.nkb, 2)))
+    return MXFP8_ERR_CUDA;
+  return launch<BN, kMode, true>(mr, mc, mo, msr, msc, p, 2 * (tiles < pairs ? tiles : pairs), 2, stream);
 }
 
 // 128 x BN tiles on single CTAs, the reduction split over clusters of `split`.
@@ -995,7 +1074,7 @@ int launch_single(const void* R, int64_t nr, const void* Cop, int64_t nc, int64_
   int64_t grid = tiles * split;
   const int64_t fit = static_cast<int64_t>(num_sms()) * Cfg<BN, kMode, false>::kMinCtas;
   if (split == 1 && grid > fit) grid = fit;  // persistent
-  return launch<BN, kMode, false>(mr, mc, mo, p, grid, split, stream);
+  return launch<BN, kMode, false>(mr, mc, mo, mr, mc, p, grid, split, stream);
 }
 
 // Clusters of `split` single CTAs that the device runs at a time. Fewer than its SMs would hold,
@@ -1078,9 +1157,7 @@ constexpr double kMxMinFlops = 1e11;
 }  // namespace
 
 int64_t blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool out_fp32) {
-  // FP32 results keep the FP32 sum over the blocks: the tensor cores' own accumulation over
-  // all of K measured 2e-6 off (K = 4096), which a BF16 result's rounding (2e-3) covers
-  if (out_fp32 || M <= 128 || N <= 128 || 2.0 * M * N * K < kMxMinFlops) return 0;
+  if (M <= 128 || N <= 128 || 2.0 * M * N * K < kMxMinFlops) return 0;
   const int64_t nkb = (K + BK - 1) / BK;
   return ((M + 127) / 128 + (N + 127) / 128) * nkb * 512 + kConvertCtas * 4;
 }
@@ -1135,12 +1212,22 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = pdl_attr(&attr[0]);
     if (cudaLaunchKernelEx(&cfg, convert_scales_kernel, c) != cudaSuccess) return MXFP8_ERR_CUDA;
-    GemmArgs g{a.A, c.tiles[0], a.B, c.tiles[1], a.C, a.M, a.N, a.K, MXFP8_OP_FPROP,
-               MXFP8_OUT_BF16, nullptr, 0, 0, a.status};
-    g.unless = c.other;
-    g.num_unless = kConvertCtas;
-    const int st = launch_gemm(g, stream);
-    if (st != MXFP8_OK) return st;
+    if (a.out_fp32) {
+      Params x = p;
+      x.sr = reinterpret_cast<const float*>(c.tiles[0]);
+      x.sc = reinterpret_cast<const float*>(c.tiles[1]);
+      x.unless = c.other;
+      x.num_unless = kConvertCtas;
+      const int st = launch_pairs<192, kMx>(a, x, stream);
+      if (st != MXFP8_OK) return st;
+    } else {
+      GemmArgs g{a.A, c.tiles[0], a.B, c.tiles[1], a.C, a.M, a.N, a.K, MXFP8_OP_FPROP,
+                 MXFP8_OUT_BF16, nullptr, 0, 0, a.status};
+      g.unless = c.other;
+      g.num_unless = kConvertCtas;
+      const int st = launch_gemm(g, stream);
+      if (st != MXFP8_OK) return st;
+    }
     p.only_if = c.other;
     p.num_only_if = kConvertCtas;
   }

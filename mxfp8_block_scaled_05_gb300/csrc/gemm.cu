@@ -1881,6 +1881,11 @@ bool make_operand_map(CUtensorMap* map, const void* base, uint64_t inner, uint64
   return make_map(map, base, 2, inner, outer, 1, BK, box_outer);
 }
 
+bool make_scale_map(CUtensorMap* map, const void* base, int64_t row_tiles, int64_t k_tiles,
+                    uint32_t tiles_per_box) {
+  return make_sf_map(map, base, row_tiles, k_tiles, tiles_per_box);
+}
+
 bool make_store_map(CUtensorMap* map, void* base, int64_t rows, int64_t N, bool fp32) {
   return make_out_map(map, base, rows, N, 1, fp32, 2);
 }

@@ -126,6 +126,9 @@ bool make_operand_map(CUtensorMap* map, const void* base, uint64_t inner, uint64
 // Tensor map of a row-major output [rows][N] for stores of 32-row x 64-byte boxes with the
 // 64-byte swizzle.
 bool make_store_map(CUtensorMap* map, void* base, int64_t rows, int64_t N, bool fp32);
+// MXFP8 scale tiles [row tiles][K tiles][512 bytes], in boxes of `tiles_per_box` row tiles.
+bool make_scale_map(CUtensorMap* map, const void* base, int64_t row_tiles, int64_t k_tiles,
+                    uint32_t tiles_per_box);
 
 // Limits of pipeline waits, and of waits for work in flight on the way out of a kernel.
 uint64_t pipeline_wait_ns();

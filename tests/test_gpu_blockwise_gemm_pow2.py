@@ -2,7 +2,9 @@
 every scale is a power of two, and the folding kernel if a single one is not.
 
 The tensor cores then accumulate over all of K, each addition losing at most 2^-23 of the
-running magnitude: |C - C_exact| <= K 2^-23 sum |a b|, and BF16 rounds once more."""
+running magnitude: |C - C_exact| <= K 2^-23 sum |a b|, and BF16 rounds once more. For an FP32
+result they accumulate over 512 at a time, and FP32 registers add those sums up:
+|C - C_exact| <= (512 2^-23 + (K / 512) 2^-24) sum |a b|."""
 import pytest
 import torch
 
@@ -55,7 +57,7 @@ def test_power_of_two_scales(m, size):
     ops = operands(mm, mm, n, k, wgrad)
     op = m.WGRAD if wgrad else m.FPROP
     assert m.blockwise_gemm_workspace_bytes(mm, n, k) > 0
-    assert m.blockwise_gemm_workspace_bytes(mm, n, k, m.OUT_FP32) == 0
+    assert m.blockwise_gemm_workspace_bytes(mm, n, k, m.OUT_FP32) > 0
     c = m.blockwise_gemm(*ops, op)
     ri, ci, ref, ab = sampled(*ops, wgrad, 1)
     err = (c[ri][:, ci].double() - ref).abs()
@@ -63,6 +65,32 @@ def test_power_of_two_scales(m, size):
     assert (err <= bound).all(), (err / bound).max().item()
     for _ in range(2):
         assert torch.equal(m.blockwise_gemm(*ops, op), c)
+
+
+@pytest.mark.parametrize("size", SIZES + [(2056, 6152, 4400, True)])
+def test_power_of_two_scales_fp32(m, size):
+    mm, n, k, wgrad = size
+    ops = operands(mm + 1, mm, n, k, wgrad)
+    op = m.WGRAD if wgrad else m.FPROP
+    out = torch.full((mm + 1, n), 7.0, device=DEV)
+    c = m.blockwise_gemm(*ops, op, m.OUT_FP32, out=out[:mm])
+    assert (out[mm] == 7.0).all()
+    ri, ci, ref, ab = sampled(*ops, wgrad, 3)
+    err = (c[ri][:, ci].double() - ref).abs()
+    bound = ab * (512 * 2.0 ** -23 + k / 512 * 2.0 ** -24)
+    assert (err <= bound).all(), (err / bound).max().item()
+    for _ in range(2):
+        assert torch.equal(m.blockwise_gemm(*ops, op, m.OUT_FP32), c)
+
+
+@pytest.mark.parametrize("which,value", [("a", 3.0), ("b", 0.0)])
+def test_one_other_scale_selects_the_folding_kernel_fp32(m, which, value):
+    mm, n, k, _ = SIZES[2]
+    a, sa, b, sb = operands(n, mm, n, k, True)
+    (sa if which == "a" else sb).view(-1)[0] = value
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    plain = m.blockwise_gemm(a, sa, b, sb, m.WGRAD, m.OUT_FP32, workspace=none)
+    assert torch.equal(m.blockwise_gemm(a, sa, b, sb, m.WGRAD, m.OUT_FP32), plain)
 
 
 @pytest.mark.parametrize("size", SIZES[:1] + SIZES[2:])
@@ -125,3 +153,19 @@ def test_workspace_refusals(m):
     none = m.blockwise_gemm(a, sa, b, sb, workspace=buf)
     sa.view(-1)[0] *= 1.5
     assert not torch.equal(none, m.blockwise_gemm(a, sa, b, sb))
+
+
+def test_wait_limit_is_reported_and_the_next_call_works_fp32(m):
+    mm, n, k, _ = SIZES[2]
+    ops = operands(9, mm, n, k, True)
+    c = m.blockwise_gemm(*ops, m.WGRAD, m.OUT_FP32)
+    assert m.device_status() == m.OK
+    m.set_wait_limit_ns(1)
+    try:
+        m.blockwise_gemm(*ops, m.WGRAD, m.OUT_FP32)
+        torch.cuda.synchronize()
+        assert m.device_status() in (m.ERR_TIMEOUT, m.OK)
+    finally:
+        m.set_wait_limit_ns(0)
+    assert torch.equal(m.blockwise_gemm(*ops, m.WGRAD, m.OUT_FP32), c)
+    assert m.device_status() == m.OK
