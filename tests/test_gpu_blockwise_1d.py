@@ -144,3 +144,18 @@ def test_refusals(m):
         with pytest.raises(m.MXFP8Error) as e:
             call(torch.zeros(shape, dtype=torch.bfloat16, device=DEV))
         assert e.value.status == m.ERR_ALIGNMENT
+
+
+def test_input_past_2_to_the_31_elements(m):
+    rows, cols = 65544, 32784
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    for i in range(0, rows, 8193):
+        x[i:i + 8193] = torch.randn((min(8193, rows - i), cols), generator=g, device=DEV)
+    bits = x.view(torch.int16)
+    ri, ci = [0, 4096, 65535, 65536, rows - 1], [0, 777, 32767, 32768, cols - 1]
+    rb = bits[ri].cpu().numpy().view(np.uint16)
+    cb = bits[:, ci].cpu().numpy().view(np.uint16)
+    rq, rs, cq, cs = m.quantize_blockwise_1d_dual(x, O.BW_SCALE_FP32)
+    same(rq[ri], rs[:, ri], *B.quantize_1d(rb, B.ROW, O.BW_SCALE_FP32))
+    same(cq[ci], cs[:, ci], *B.quantize_1d(np.ascontiguousarray(cb), B.COL, O.BW_SCALE_FP32))

@@ -237,3 +237,21 @@ def test_wait_limit_is_reported_and_the_next_call_works(m, mm, n):
         m.set_wait_limit_ns(0)
     assert torch.equal(m.blockwise_gemm(a, sa, b, sb), want)
     assert m.device_status() == m.OK
+
+
+@pytest.mark.parametrize("wgrad,fp32,pow2", [(False, False, False), (True, True, False),
+                                             (True, True, True)])
+def test_output_past_2_to_the_31_elements(m, wgrad, fp32, pow2):
+    mm, n, k = 65544, 32776, 128
+    a, sa, b, sb = operands(21, mm, n, k, wgrad)
+    if pow2:
+        sa, sb = np.exp2(np.floor(np.log2(sa))), np.exp2(np.floor(np.log2(sb)))
+    c = m.blockwise_gemm(*to(a, sa, b, sb), m.WGRAD if wgrad else m.FPROP,
+                         m.OUT_FP32 if fp32 else m.OUT_BF16)
+    ri = np.array([0, 1, 32767, 65409, 65535, 65536, mm - 1])
+    ci = np.array([0, 7, 16384, 32767, 32768, n - 1])
+    da = B.dequantize_1d(a[ri], sa[:, ri])
+    db = B.dequantize_1d(b[ci], sb[:, ci]) if wgrad else \
+        B.dequantize_1d(b[ci], sb[ci // 128].T)
+    got = c[torch.from_numpy(ri).to(DEV)][:, torch.from_numpy(ci).to(DEV)]
+    check(got, da @ db.T, np.abs(da) @ np.abs(db).T, k, not fp32)
