@@ -218,16 +218,16 @@ struct Shared {
   uint64_t top[kMaxTop];            // the best keys, in order
 };
 
-// The k largest of keys [0, n), in order, into `out` (kNoKey where fewer exist). Keys are
-// distinct but for kNoKey. Called by the whole CTA; `out` is ready after the next barrier.
+// The k largest of keys [0, n), in order, into `out`, which the caller has filled with kNoKey
+// (it stays where fewer exist). Keys are distinct but for kNoKey. Called by the whole CTA;
+// `out` is ready after the next barrier.
 template <int kThreads>
 __device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int k, uint64_t* out,
                                           int tid) {
-  for (int t = tid; t < k; t += kThreads) out[t] = kNoKey;
-  __syncthreads();
   for (int t = tid; t < n; t += kThreads) {
     const uint64_t mine = keys[t];
     int above = 0;
+#pragma unroll 4
     for (int i = 0; i < n; ++i) above += keys[i] > mine;
     if (mine > kNoKey && above < k) out[above] = mine;
   }
@@ -272,6 +272,28 @@ struct Best {
 // thread that reaches the bar took 46% longer at 4096 x 131072: 32-byte pieces 4 KB apart.)
 // What reaches the bar is listed, and ranked by counting; where it is more than the list holds
 // (many equal values), sorted lists kept by the warps take over.
+// A barrier stands between the two halves.
+template <int kThreads>
+__device__ __forceinline__ void set_bars(Shared<kThreads>& sh, int64_t v0, int64_t v1,
+                                         const Best& kept, int k) {
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t full = (v1 - v0) / 32;  // warps with a vector in every lane
+  const int warps = static_cast<int>(full < kWarps ? full : kWarps);
+  if (warps > 0 && 32 * warps >= k) {
+    const int j = (k + warps - 1) / warps;
+    uint32_t v = order_of(kept.top), best = 0;
+    for (int i = 0; i < j; ++i) {
+      best = __reduce_max_sync(0xFFFFFFFFu, v);
+      const int at = __ffs(__ballot_sync(0xFFFFFFFFu, v == best)) - 1;
+      if (lane == at) v = 0;
+    }
+    if (lane == 0) sh.warp_bar[warp] = best;
+  }
+  if (tid == 0) sh.num_chosen = sh.num_reread = sh.num_candidates = 0;
+  if (tid < k) sh.top[tid] = kNoKey;
+}
+
 template <int kThreads, typename T>
 __device__ __forceinline__ void find_top(Shared<kThreads>& sh, const T* row, const RowShape& shape,
                                          int64_t v0, int64_t v1, bool first, bool last,
@@ -282,21 +304,9 @@ __device__ __forceinline__ void find_top(Shared<kThreads>& sh, const T* row, con
   const int64_t tail0 = shape.head + shape.nv * kN;
   constexpr uint32_t kNone = static_cast<uint32_t>(kNoKey >> 32);  // order of -inf
   const uint32_t own = order_of(kept.top);
-  const int64_t full = (v1 - v0) / 32;  // warps with a vector in every lane
+  const int64_t full = (v1 - v0) / 32;
   const int warps = static_cast<int>(full < kWarps ? full : kWarps);
   uint32_t bar_order = kNone + 1;
-  if (warps > 0 && 32 * warps >= k) {
-    const int j = (k + warps - 1) / warps;
-    uint32_t v = own, best = 0;
-    for (int i = 0; i < j; ++i) {
-      best = __reduce_max_sync(0xFFFFFFFFu, v);
-      const int at = __ffs(__ballot_sync(0xFFFFFFFFu, v == best)) - 1;
-      if (lane == at) v = 0;
-    }
-    if (lane == 0) sh.warp_bar[warp] = best;
-  }
-  if (tid == 0) sh.num_chosen = sh.num_reread = sh.num_candidates = 0;
-  __syncthreads();
   if (warps > 0 && 32 * warps >= k) {
     uint32_t least = 0xFFFFFFFFu;
     for (int w = 0; w < warps; ++w) least = min(least, sh.warp_bar[w]);
@@ -325,13 +335,13 @@ __device__ __forceinline__ void find_top(Shared<kThreads>& sh, const T* row, con
   __syncthreads();
   const int steps = static_cast<int>((v1 - v0 + kThreads - 1) / kThreads);
   const int runs = (steps + 31) / 32;  // of 32 vectors, one a lane, for each thread
-  const int all = sh.num_reread * runs;
+  const int all = sh.num_reread * runs;  // the same for every thread
   for (int g = warp; g < all; g += kWarps) {
     const int c = g / runs;
     const int64_t v = v0 + sh.reread[c] + static_cast<int64_t>((g - c * runs) * 32 + lane) * kThreads;
     if (v < v1) list_vector(__ldg(body + v), v);
   }
-  __syncthreads();
+  if (all > 0) __syncthreads();
   int listed = sh.num_candidates;
   if (listed > kMaxCandidates) {
     __syncthreads();
@@ -382,7 +392,7 @@ __device__ __forceinline__ void cluster_wait() {
 // One cluster of `split` CTAs per row; each CTA streams a contiguous part of it once.
 //
 // Bound by memory (2 or 4 bytes a logit): 16-byte loads, four of them in flight a thread, each
-// logit read once. 4096 x 131072 BF16: 159 us (6.7 TB/s), 180 with the 8 likeliest tokens. One
+// logit read once. 4096 x 131072 BF16: 159 us (6.7 TB/s), 179 with the 8 likeliest tokens. One
 // row of 131072 takes 3.5 us, 6.8 with the 5 likeliest.
 // Rows are split over a cluster only when there are too few of them to fill the GPU; each
 // CTA then hands its sums and best keys to the first through distributed shared memory,
@@ -452,6 +462,7 @@ logprob_kernel(const Params p, int split) {
     }
   };
   join_lanes(32);
+  if constexpr (kTop) set_bars(sh, v0, v1, kept, p.top);
   if (lane == 0) {
     sh.part[warp][0] = sm.m;
     sh.part[warp][1] = sm.s;
@@ -495,6 +506,8 @@ logprob_kernel(const Params p, int split) {
       join_lanes(kMaxSplit);
     }
     if constexpr (kTop) {
+      if (tid < p.top) sh.top[tid] = kNoKey;  // its own keys have been read into the lists
+      __syncthreads();
       rank_keys<kThreads>(sh.lists, split * p.top, p.top, sh.top, tid);
       __syncthreads();
     }
