@@ -654,9 +654,10 @@ blockwise_quantize_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_
 // the 8 codes of a column in 8 consecutive bytes. They pass through shared memory (16 KB,
 // 8-byte units XOR-swizzled by the patch column) to leave as 16-byte stores. The scales of
 // the 8 rows a half-warp shares are computed by 8 of its lanes, one division each, instead
-// of 8 divisions in every lane. 4096 x 12288, both copies: 35.6 us (5.6
-// TB/s; 33.2 with one scale a tile); the row-wise copy alone 21.4, the transposed one 22.2
-// (7 TB/s, part of it in L2).
+// of 8 divisions in every lane. 4096 x 12288, both copies: 35.5 us (5.7
+// TB/s; 33.2 with one scale a tile); the row-wise copy alone 22.0, the transposed one 22.6
+// (6.9 and 6.7 TB/s). Four CTAs fit an SM with 64 registers; five, at 48, took 51 us: fewer
+// loads stay in flight.
 template <bool kRow, bool kCol, bool k2D>
 __global__ void __launch_bounds__(kThreads)
 blockwise_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t cols,
@@ -707,7 +708,7 @@ blockwise_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t co
     }
   }
 
-  if constexpr (kCol && !k2D) {  // column maxima over the tile's rows, then their factors
+  if constexpr (kCol && !k2D) {  // column maxima over the tile's rows
     uint32_t m[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -717,22 +718,10 @@ blockwise_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t co
     for (int w = 0; w < 4; ++w) m[w] = max_u16x2(m[w], __shfl_xor_sync(0xFFFFFFFFu, m[w], 16));
     if (lane < 16)
       *reinterpret_cast<uint4*>(&warp_max[t >> 5][4 * v]) = make_uint4(m[0], m[1], m[2], m[3]);
-    __syncthreads();
-    if (t < kTile) {
-      uint32_t a = 0;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w)
-        a = max(a, static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(warp_max[w])[t]));
-      float f, inv;
-      blockwise_scale(a, pow2 != 0, f, inv);
-      factor[t] = f;
-      if (t < cols_valid) col_inv[static_cast<int64_t>(blockIdx.y) * cols + col0 + t] = inv;
-    }
-    __syncthreads();
   }
 
+  float mine = fb;  // lane v < 8 of a half-warp: the factor of row 8 g + v
   if constexpr (kRow) {
-    float mine = fb;  // lane v < 8 of a half-warp: the factor of row 8 g + v
     if constexpr (!k2D) {
       uint32_t m[4];  // rows j and j + 4 in the two halves of a word
 #pragma unroll
@@ -756,6 +745,23 @@ blockwise_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t co
       if (v < 8 && 8 * g + v < rows_valid)
         row_inv[static_cast<int64_t>(blockIdx.x) * rows + row0 + 8 * g + v] = inv;
     }
+  }
+
+  if constexpr (kCol && !k2D) {  // the columns' factors, while the other threads convert rows
+    __syncthreads();
+    if (t < kTile) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w)
+        a = max(a, static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(warp_max[w])[t]));
+      float f, inv;
+      blockwise_scale(a, pow2 != 0, f, inv);
+      factor[t] = f;
+      if (t < cols_valid) col_inv[static_cast<int64_t>(blockIdx.y) * cols + col0 + t] = inv;
+    }
+  }
+
+  if constexpr (kRow) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float f = k2D ? fb : __shfl_sync(0xFFFFFFFFu, mine, (lane & 16) + j);
@@ -774,6 +780,7 @@ blockwise_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t co
   }
 
   if constexpr (kCol) {
+    if constexpr (!k2D) __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // column 8 v + i of the tile, its rows 8 g .. 8 g + 7
       const float f = k2D ? fb : factor[8 * v + i];
