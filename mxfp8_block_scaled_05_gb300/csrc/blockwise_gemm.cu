@@ -37,8 +37,8 @@
 //   kMx       both with power-of-two scales, as E8M0 scales of the block-scaled MMA: FP32 results
 //             of those (see the conversion kernel). TMEM adds up four blocks, the fold warps
 //             those sums. 6144 x 4096 x 4096 80 us, 119 with the scales folded in
-// and by size: pairs of CTAs (cta_group::2, 256 x 256 tiles, 256 x 192 of the weight gradient,
-// each SM stages half of the column operand), or single CTAs (128 x BN tiles) whose reduction
+// and by size: pairs of CTAs (cta_group::2, 256 x 256 tiles, 256 x 192 of the weight gradient and
+// kMx, each SM stages half of the column operand), or single CTAs (128 x BN tiles) whose reduction
 // may be split over a cluster, the parts joined through distributed shared memory in rank
 // order. Which of them, and how many parts, is chosen by estimated time (see Cost).
 //
@@ -94,7 +94,8 @@ struct Cfg {
   static constexpr int kBoxBytes = 32 * 64;
   static constexpr int kBoxes = kMode == kMx ? 1 : 2;  // (kMx needs the room for its stages)
   static constexpr int kOffBox = kOffB + kStages * kBBytes;
-  static constexpr int kOffScale = kOffBox + (kMode == kSwapped ? 0 : kBoxes * kFoldWarps * kBoxBytes);
+  static constexpr int kOffScale =
+      kOffBox + (kMode == kSwapped ? 0 : kBoxes * kFoldWarps * kBoxBytes);
   static constexpr int kRowScales = kMode == kSwapped ? 4 : BM;  // (kSwapped: one)
   static constexpr int kColScales = kMode == kFprop ? 4 : BN;    // (kFprop: one for 128 columns)
   static constexpr int kScaleFloats = kRowScales + kColScales;   // a tile's scales of a block
@@ -125,7 +126,7 @@ constexpr int kOtherRegs = 56;
 
 struct Params {
   const float* sr;      // scales of the row operand: [nkb][ldr], or [row blocks][nkb] (kSwapped)
-  const float* sc;      // scales of the column operand: [nkb][ldc], or [column blocks][nkb] (kFprop)
+  const float* sc;      // of the column operand: [nkb][ldc], or [column blocks][nkb] (kFprop)
   int64_t ldr, ldc;
   void* C;
   int64_t ldo;          // output row pitch in elements
@@ -277,7 +278,8 @@ __device__ __forceinline__ void set_max_regs_dec() {
 
 // acc[0], acc[1] += s (two packed) times v0, v1
 __device__ __forceinline__ void add_scaled(float* acc, uint32_t v0, uint32_t v1, uint64_t s) {
-  const uint64_t a = fma2(pack2(__uint_as_float(v0), __uint_as_float(v1)), s, pack2(acc[0], acc[1]));
+  const uint64_t a =
+      fma2(pack2(__uint_as_float(v0), __uint_as_float(v1)), s, pack2(acc[0], acc[1]));
   unpack2(a, acc[0], acc[1]);
 }
 
@@ -301,10 +303,10 @@ __device__ __forceinline__ void fold(float* acc, const uint32_t (&v)[G], float s
 
 // The weight gradient's fold: a scale for every row and every column. A scale that each lane
 // needs for every column costs one shared-memory cycle a warp and column, 1024 for a 256-wide
-// block (measured 837 cycles a block in the fold alone). So TMEM is read in the 16x256b shape, which gives
-// a lane few columns of several rows: of columns 8 j + 2 (lane % 4) and the next, rows lane / 4
-// (r[4 j], r[4 j + 1]) and lane / 4 + 8 (r[4 j + 2], r[4 j + 3]), of 16 rows and 64 columns a
-// read; column scales are read two at a time and serve four rows.
+// block (measured 837 cycles a block in the fold alone). So TMEM is read in the 16x256b shape,
+// which gives a lane few columns of several rows: of columns 8 j + 2 (lane % 4) and the next,
+// rows lane / 4 (r[4 j], r[4 j + 1]) and lane / 4 + 8 (r[4 j + 2], r[4 j + 3]), of 16 rows and
+// 32 columns a read; column scales are read two at a time and serve four rows.
 __device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32"
@@ -368,7 +370,8 @@ struct BoxStore {
 
 // Sums held one row per lane (acc[i]: column i).
 template <int kNC, int kBoxes>
-__device__ __forceinline__ void store_rows(BoxStore<kBoxes>& out, const Params& p, const float (&acc)[kNC],
+__device__ __forceinline__ void store_rows(BoxStore<kBoxes>& out, const Params& p,
+                                           const float (&acc)[kNC],
                                            int64_t row0, int64_t c0, int lane) {
   if (row0 >= p.nr) return;
 #pragma unroll
@@ -525,7 +528,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
     for (int i = lane; i < C::kNumBars; i += 32) {
       uint64_t* bar = full + i;
       mbar_init(bar, bar < ready         ? 1
-                     : bar < scale_empty ? (kMode == kMx ? 1 : 1 + 32)  // the MMA's commit, the scales' copies
+                     // the MMA's commit, the scales' copies
+                     : bar < scale_empty ? (kMode == kMx ? 1 : 1 + 32)
                      : bar < acc_empty   ? C::kFoldWarps
                      : bar < mma_done    ? (kPair ? 2 : 1) * C::kFoldWarps
                                          : 1);
@@ -570,16 +574,18 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       const int32_t r0 = static_cast<int32_t>(kPair ? (2 * rt + crank) * BM : rt * BM);
       const int32_t c0 = static_cast<int32_t>(ct * BN);
       const int64_t rows_here = p.nr - r0, cols_here = p.nc - c0;
-      const float* srp = kMode == kSwapped ? p.sr + rt * p.nkb + kb0 : p.sr + kb0 * p.ldr + r0 + lane;
-      const float* scp = kMode == kFprop ? p.sc + (c0 / 128 + lane) * static_cast<int64_t>(p.nkb) + kb0
-                                         : p.sc + kb0 * p.ldc + c0 + lane;
+      const float* srp =
+          kMode == kSwapped ? p.sr + rt * p.nkb + kb0 : p.sr + kb0 * p.ldr + r0 + lane;
+      const float* scp = kMode == kFprop
+                             ? p.sc + (c0 / 128 + lane) * static_cast<int64_t>(p.nkb) + kb0
+                             : p.sc + kb0 * p.ldc + c0 + lane;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1;
         const uint32_t sl = it % kScaleRing;
         ok = wait_phase(&empty[s], ph ^ 1, abort_flag, p.wait_ns) &&
              (kMode == kMx || it % kScaleGroup != 0 ||
-              wait_phase(&scale_empty[sl / kScaleGroup],
-                                                  ((it / kScaleRing) & 1) ^ 1, abort_flag, p.wait_ns));
+              wait_phase(&scale_empty[sl / kScaleGroup], ((it / kScaleRing) & 1) ^ 1, abort_flag,
+                         p.wait_ns));
         if (!ok) break;
         if (issuer) {
           uint8_t* as = smem + C::kOffA + s * C::kABytes;
@@ -612,7 +618,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
             if (i + lane < rows_here) cp_async4(slot + i + lane, srp + i);
         }
         if constexpr (kMode == kFprop) {
-          if (lane < BN / 128 && 128 * lane < cols_here) cp_async4(slot + C::kRowScales + lane, scp);
+          if (lane < BN / 128 && 128 * lane < cols_here)
+            cp_async4(slot + C::kRowScales + lane, scp);
         } else {
 #pragma unroll
           for (int i = 0; i < BN; i += 32)
@@ -675,7 +682,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
         const uint32_t s = it % kStages, ph = (it / kStages) & 1;
         const uint32_t b = acc_it & 1, aph = (acc_it >> 1) & 1;
         const bool starts = C::kChunk == 1 || (kb - kb0) % C::kChunk == 0;
-        const bool ends = C::kChunk == 1 || (kb - kb0) % C::kChunk == C::kChunk - 1 || kb == kb1 - 1;
+        const bool ends =
+            C::kChunk == 1 || (kb - kb0) % C::kChunk == C::kChunk - 1 || kb == kb1 - 1;
         ok = wait(&full[s], ph) && (!starts || wait(&acc_empty[b], aph ^ 1));
         if (!ok) break;
         tc_fence_after();
@@ -692,8 +700,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
             tmem_cp_32x128b_x4_2sm(sfb + 4, sd + 1024 / 16);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_mxf8_2sm(d, ad + 2 * k, bd + 2 * k, mxf8_idesc(2 * BM, BN, k, k), sfa, sfb + sfb_shift,
-                           !starts || k > 0);
+              mma_mxf8_2sm(d, ad + 2 * k, bd + 2 * k, mxf8_idesc(2 * BM, BN, k, k), sfa,
+                           sfb + sfb_shift, !starts || k > 0);
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -765,7 +773,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
       for (int kb = kb0; kb < kb1; kb += C::kChunk, ++it) {  // `it` counts accumulators
         const uint32_t b = it & 1;
         const float* rows = ring + (it % kScaleRing) * C::kScaleFloats;
-        const float* cols = rows + C::kRowScales + (kMode == kFprop ? half * kNC / 128 : half * kNC);
+        const float* cols =
+            rows + C::kRowScales + (kMode == kFprop ? half * kNC / 128 : half * kNC);
         float rq[4];
         float2 cq[4];  // the scales of 32 of the columns
         auto load_cq = [&](int u) {
@@ -781,8 +790,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
           // four reads of 16 rows and 32 columns; the next one is under way during the fold
           uint32_t r[2][16];
           auto read = [&](int i) {
-            tmem_ld_quads(tbase + b * BN + (static_cast<uint32_t>(16 * (i & 1)) << 16) + 16 * (i & 2),
-                          r[i & 1]);
+            const uint32_t row = static_cast<uint32_t>(16 * (i & 1)) << 16;
+            tmem_ld_quads(tbase + b * BN + row + 16 * (i & 2), r[i & 1]);
           };
           read(0);
 #pragma unroll
@@ -798,7 +807,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
               tc_fence_before();
               arrive_if(lane == 0, acc_empty0 + 8 * b);
             }
-            fold_quads(&quads[i & 1][2 * (i & 2)], r[i & 1], rq[2 * (i & 1)], rq[2 * (i & 1) + 1], cq);
+            fold_quads(&quads[i & 1][2 * (i & 2)], r[i & 1], rq[2 * (i & 1)],
+                       rq[2 * (i & 1) + 1], cq);
           }
         } else {
           float s = 0.f;
@@ -848,7 +858,8 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
         } else {
 #pragma unroll
           for (int i = 0; i < kNC; i += 4)
-            *reinterpret_cast<float4*>(part_sum + (32 * q + lane) * C::kPartPitch + half * kNC + i) =
+            *reinterpret_cast<float4*>(part_sum + (32 * q + lane) * C::kPartPitch + half * kNC +
+                                       i) =
                 make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
         }
       } else if constexpr (kMode == kSwapped) {
@@ -1026,7 +1037,8 @@ int launch(const CUtensorMap& mr, const CUtensorMap& mc, const CUtensorMap& mo,
     attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
   }
-  return cudaLaunchKernelEx(&cfg, k, mr, mc, mo, msr, msc, p) == cudaSuccess ? MXFP8_OK : MXFP8_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k, mr, mc, mo, msr, msc, p) == cudaSuccess ? MXFP8_OK
+                                                                             : MXFP8_ERR_CUDA;
 }
 
 // 256 x BN tiles on CTA pairs. `a` is the row operand.
@@ -1051,7 +1063,8 @@ int launch_pairs(const BlockwiseGemmArgs& a, Params p, cudaStream_t stream) {
       (!make_scale_map(&msr, p.sr, (a.M + 127) / 128, p.nkb, 1) ||
        !make_scale_map(&msc, p.sc, (a.N + 127) / 128, p.nkb, 2)))
     return MXFP8_ERR_CUDA;
-  return launch<BN, kMode, true>(mr, mc, mo, msr, msc, p, 2 * (tiles < pairs ? tiles : pairs), 2, stream);
+  return launch<BN, kMode, true>(mr, mc, mo, msr, msc, p, 2 * (tiles < pairs ? tiles : pairs), 2,
+                                 stream);
 }
 
 // 128 x BN tiles on single CTAs, the reduction split over clusters of `split`.
