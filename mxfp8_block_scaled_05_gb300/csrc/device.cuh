@@ -220,14 +220,20 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gmem_src, 
 }
 
 // --------------------------------------------------------------------------- tcgen05
+// An .aligned instruction needs all lanes of the warp at the same instruction; neither the end
+// of a divergent branch or loop nor a vote promises that. So the wrappers outside the inner loops
+// (cluster barriers, TMEM allocation) converge the warp themselves; the callers of
+// tcgen05.ld do it with their waits.
 
 __device__ __forceinline__ void tmem_alloc(uint32_t* smem_slot, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                ::"r"(smem_u32(smem_slot)), "r"(ncols) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
                ::"r"(taddr), "r"(ncols) : "memory");
 }
@@ -315,10 +321,19 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
       ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Every thread of every CTA in the cluster; orders shared-memory (and barrier) state.
+// Every thread of every CTA in the cluster; orders shared-memory (and barrier) state. The two
+// halves may be used apart.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -435,12 +450,14 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 
 // Executed by one warp in each CTA of the pair; both receive the same columns.
 __device__ __forceinline__ void tmem_alloc_2sm(uint32_t* smem_slot, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                ::"r"(smem_u32(smem_slot)), "r"(ncols) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_dealloc_2sm(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
                ::"r"(taddr), "r"(ncols) : "memory");
 }

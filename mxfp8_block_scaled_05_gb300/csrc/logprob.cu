@@ -381,14 +381,6 @@ __device__ __forceinline__ void find_top(Shared<kThreads>& sh, const T* row, con
   __syncthreads();
 }
 
-// Halves of a cluster barrier: every thread of every CTA of the cluster does both.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // One cluster of `split` CTAs per row; each CTA streams a contiguous part of it once.
 //
 // Bound by memory (2 or 4 bytes a logit): 16-byte loads, four of them in flight a thread, each
