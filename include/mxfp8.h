@@ -64,7 +64,7 @@ typedef enum mxfp8_status {
                                      32-aligned and ending at total_rows */
   MXFP8_ERR_TIMEOUT = 6,          /* (device) a pipeline wait in a kernel ran out; the
                                      kernel abandoned its work */
-  MXFP8_ERR_BAD_TARGET = 7        /* (device) a target token at or past the vocabulary */
+  MXFP8_ERR_BAD_TARGET = 7        /* (device) a token id at or past the vocabulary */
 } mxfp8_status;
 
 typedef enum mxfp8_axis {
@@ -532,8 +532,9 @@ int mxfp8_token_logprobs(const void* logits_dev, int logits_dtype, int64_t rows,
  *   targets_dev, stats_dev, entropy_dev, top_id_dev   as that call read or wrote them
  *   grad_logprob_dev  g, float [rows] (not read where the target is negative: 0)
  *   grad_entropy_dev  h, float [rows], or NULL for 0
- *   grad_top_dev      gt, float [rows][top]; NULL, as top_id_dev, if top == 0. An id of -1
- *                     is skipped, and its gt is not read.
+ *   grad_top_dev      gt, float [rows][top]; NULL, as top_id_dev, if top == 0. A negative
+ *                     id is skipped, and its gt is not read. One at or past vocab, like such
+ *                     a target, makes the row NaN and latches MXFP8_ERR_BAD_TARGET.
  *   grad_logits_dev   the logits' dtype, [rows][grad_ld], its first `vocab` columns
  *                     written; may be the logits' own buffer (then grad_ld == ld)
  * A row whose logits are all -inf gets zeros. Errors as above.

@@ -139,7 +139,7 @@ const char* mxfp8_status_string(int status) {
     case MXFP8_ERR_UNSUPPORTED_ARCH: return "unsupported device (needs compute capability 10.3, sm_103a)";
     case MXFP8_ERR_CUDA: return "CUDA call failed";
     case MXFP8_ERR_BAD_OFFSETS: return "expert offsets invalid (must be 0-based, non-decreasing, 32-aligned, end at total_rows)";
-    case MXFP8_ERR_BAD_TARGET: return "a target token is at or past the vocabulary";
+    case MXFP8_ERR_BAD_TARGET: return "a target or alternative token is at or past the vocabulary";
     case MXFP8_ERR_TIMEOUT: return "a kernel pipeline wait timed out; its work was abandoned";
     default: return "unknown status";
   }

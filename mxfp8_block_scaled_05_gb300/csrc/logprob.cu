@@ -594,14 +594,18 @@ logprob_grad_kernel(const GradParams p) {
   const int64_t target = p.targets[row_id];
   const bool empty = m == -kInf;
   const float sub = empty ? 0.f : m;
-  const bool bad = target >= p.vocab;
-  if (bad && first && tid == 0) latch_error(p.status, MXFP8_ERR_BAD_TARGET);
-  const float g = target < 0 || empty ? 0.f : bad ? __uint_as_float(0x7FC00000u)
-                                                  : p.g_logprob[row_id];
+  const float nan = __uint_as_float(0x7FC00000u);
+  const float g = target < 0 || empty ? 0.f : target >= p.vocab ? nan : p.g_logprob[row_id];
+  bool bad = target >= p.vocab;
   float mass = g;
   for (int j = 0; j < p.top; ++j) {
     const int64_t id = p.top_id[row_id * p.top + j];
-    if (id >= 0) mass += p.g_top[row_id * p.top + j];
+    if (id >= p.vocab) bad = true;
+    else if (id >= 0) mass += p.g_top[row_id * p.top + j];
+  }
+  if (bad) {  // no column takes such a token's share: the row has no gradient
+    if (!empty) mass = nan;
+    if (first && tid == 0) latch_error(p.status, MXFP8_ERR_BAD_TARGET);
   }
   const float c = p.inv_t * kLog2e, base = log_s * kLog2e;
   // dx = -p (A + B t) / T + the named columns, t = log2 p. p is taken as 2^(t + 24) with
