@@ -537,7 +537,7 @@ int mxfp8_token_logprobs(const void* logits_dev, int logits_dtype, int64_t rows,
  *                     a target, makes the row NaN and latches MXFP8_ERR_BAD_TARGET.
  *   grad_logits_dev   the logits' dtype, [rows][grad_ld], its first `vocab` columns
  *                     written; may be the logits' own buffer (then grad_ld == ld)
- * A row whose logits are all -inf gets zeros. Errors as above.
+ * A row whose logits are all -inf gets zeros, whatever its g, h and gt. Errors as above.
  */
 int mxfp8_token_logprobs_backward(const void* logits_dev, int logits_dtype, int64_t rows,
                                   int64_t vocab, int64_t ld, const int64_t* targets_dev,

@@ -604,14 +604,16 @@ logprob_grad_kernel(const GradParams p) {
     else if (id >= 0) mass += p.g_top[row_id * p.top + j];
   }
   if (bad) {  // no column takes such a token's share: the row has no gradient
-    if (!empty) mass = nan;
+    mass = nan;
     if (first && tid == 0) latch_error(p.status, MXFP8_ERR_BAD_TARGET);
   }
   const float c = p.inv_t * kLog2e, base = log_s * kLog2e;
   // dx = -p (A + B t) / T + the named columns, t = log2 p. p is taken as 2^(t + 24) with
   // 2^-24 in A and B, since ex2 flushes subnormal results: so p is good down to 2^-150.
   constexpr float kLift = 24.f, kDrop = 0x1p-24f;
-  const float A = -(mass + h * ent) * p.inv_t * kDrop, B = -h * kLn2 * p.inv_t * kDrop;
+  // An empty row's gradient is zero even where h or a weight is not finite.
+  const float A = empty ? 0.f : -(mass + h * ent) * p.inv_t * kDrop;
+  const float B = empty ? 0.f : -h * kLn2 * p.inv_t * kDrop;
   auto grad_of = [&](float x) {
     const float t = max_nan((x - sub) * c - base, kLowest);
     return ex2(t + kLift) * fmaf(B, t, A);

@@ -32,3 +32,22 @@ def test_alternative_past_the_vocabulary(m, dtype, vocab):
     assert got[1].isnan().all() and got[2].isnan().all()
     for i in (0, 3, 4):
         assert torch.equal(got[i], want[i])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("weight", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("vocab", [100, 20011])
+def test_empty_row_gets_zeros_whatever_its_weights(m, dtype, weight, vocab):
+    x, t = make(4, 4, vocab, dtype)
+    x[1], x[2] = -float("inf"), -float("inf")
+    t[:] = torch.tensor([3, 4, -1, 6], device=DEV)
+    r = m.token_logprobs(x, t, top=2)
+    g = torch.ones(4, device=DEV)
+    gt = torch.ones(4, 2, device=DEV)
+    want = m.token_logprobs_backward(x, t, r.stats, r.entropy, g, g, r.top_id, gt)
+    bad = g.clone()
+    bad[1:3] = weight
+    gt[1:3] = weight
+    got = m.token_logprobs_backward(x, t, r.stats, r.entropy, bad, bad, r.top_id, gt)
+    assert (got[1:3] == 0).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
