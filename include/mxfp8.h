@@ -376,9 +376,10 @@ size_t mxfp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int op, int o
  *                   tokens, padded as the COL copies are)
  *   C_dev           [M][N], BF16 or FP32, fully overwritten
  * Requires K % 16 == 0 and N % 8 == 0; any M (WGRAD too). Accuracy: |C - C_exact| <=
- * 2^-9 * sum_k |a_k b_k| per element before the output rounding, as long as the products of
- * its blocks' two scales, which are formed in FP32, are normal numbers or zero. A NaN scale or
- * code gives NaN in the elements it reaches. Deterministic.
+ * 2^-9 * sum_k |a_k b_k| per element before the output rounding for K up to 2^22, and
+ * K 2^-31 * sum_k |a_k b_k| beyond (the worst case of an FP32 sum over the blocks), as long as
+ * the products of its blocks' two scales, which are formed in FP32, are normal numbers or zero.
+ * A NaN scale or code gives NaN in the elements it reaches. Deterministic.
  * Empty sizes: M == 0 or N == 0 writes nothing, K == 0 zero-fills C (the operands may then
  * be NULL).
  * Errors: MXFP8_ERR_INVALID_ARG (negative or too large sizes, unknown enums, null
@@ -395,7 +396,9 @@ int mxfp8_blockwise_gemm(const void* A_dev, const float* sA_dev, const void* B_d
  * a block of 128 is then the E8M0 scale of its four blocks of 32. The device finds out: a
  * kernel converts the scales and checks them, then one of the two GEMMs runs and the other
  * returns at once. Both meet the accuracy bound; they are not bit-identical. For an FP32 result
- * the tensor cores sum 512 products at a time, and those sums are added in FP32.
+ * the tensor cores sum 512 products at a time, and those sums are added in FP32. For a BF16
+ * result they sum all of K, which costs up to K 2^-28 * sum_k |a_k b_k|, so that only reductions
+ * of up to 2^17 run that way.
  *   workspace_dev    device memory, 16-byte aligned, or NULL; contents do not matter. One GEMM
  *                    at a time may use it.
  *   workspace_bytes  its size. Below mxfp8_blockwise_gemm_workspace_bytes the call proceeds as
@@ -408,7 +411,8 @@ int mxfp8_blockwise_gemm_ws(const void* A_dev, const float* sA_dev, const void* 
 
 /*
  * Workspace bytes of mxfp8_blockwise_gemm_ws for one problem; 0 where it would not use one: a
- * product too small for the conversion to pay, or invalid arguments.
+ * product too small for the conversion to pay, a BF16 result of a longer reduction, or invalid
+ * arguments.
  */
 size_t mxfp8_blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
 

@@ -1166,11 +1166,17 @@ int launch_swapped(const BlockwiseGemmArgs& a, const Params& p, cudaStream_t str
 // (1021 x 12288 x 4096: 41 us, 46 folded; more for larger products) is about what the
 // conversion and the check cost others (54 us), or more.
 constexpr double kMxMinFlops = 1e11;
+// The longest reduction that a BF16 result leaves to the tensor cores' own sum. They drop what lies
+// below the sum's last bit at each step of 32 products: up to 2^-23 of it, so K 2^-28 in all where
+// the products have one sign (measured, same sign, of sum |a b|: 0.002 at K = 2^20, 0.015 at 2^23;
+// the folding kernel 2e-6). Up to here that is 2^-11, a quarter of BF16's own rounding.
+constexpr int64_t kMxMaxK = int64_t{1} << 17;
 
 }  // namespace
 
 int64_t blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool out_fp32) {
   if (M <= 128 || N <= 128 || 2.0 * M * N * K < kMxMinFlops) return 0;
+  if (!out_fp32 && K > kMxMaxK) return 0;
   const int64_t nkb = (K + BK - 1) / BK;
   return ((M + 127) / 128 + (N + 127) / 128) * nkb * 512 + kConvertCtas * 4;
 }

@@ -1,0 +1,53 @@
+"""Long reductions of the block-wise GEMM whose products all have one sign, where an accumulator
+that drops low bits drifts one way.
+
+For every K up to 2^22: |C - C_exact| <= 2^-9 sum |a b|, and a BF16 result rounds by up to
+2^-9 |C| once more. Here sum |a b| = C_exact. (The 64-bit sums of the reference are exact to
+K 2^-53.)"""
+import pytest
+import torch
+
+from tests.oracle_helpers import gpu_ready
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def m():
+    mod = gpu_ready()
+    yield mod
+    assert mod.device_status() == mod.OK
+
+
+def positive_operands(seed, mm, n, k):
+    """Finite codes of positive sign, scales 1: a weight gradient's operands."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    kb = -(-k // 128)
+    a, b = (torch.randint(1, 0x7F, (r, k), generator=g, device=DEV, dtype=torch.uint8)
+            for r in (mm, n))
+    return a, torch.ones(kb, mm, device=DEV), b, torch.ones(kb, n, device=DEV)
+
+
+def sampled(a, b):
+    """64-bit values of 8 rows and 16 columns, the first and the last among them."""
+    ri = torch.linspace(0, a.shape[0] - 1, 8).long().to(DEV)
+    ci = torch.linspace(0, b.shape[0] - 1, 16).long().to(DEV)
+    ref = torch.zeros(8, 16, dtype=torch.double, device=DEV)
+    for k0 in range(0, a.shape[1], 1 << 20):
+        da, db = (q[i, k0:k0 + (1 << 20)].view(torch.float8_e4m3fn).double()
+                  for q, i in ((a, ri), (b, ci)))
+        ref += da @ db.t()
+    return ri, ci, ref
+
+
+@pytest.mark.parametrize("mm,n,k", [(1536, 2048, 32768 + 16), (2048, 2048, 1 << 18),
+                                    (1024, 1024, 1 << 22)])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_one_sign(m, mm, n, k, fp32):
+    a, sa, b, sb = positive_operands(k, mm, n, k)
+    ri, ci, ref = sampled(a, b)
+    bound = ref * (2.0 ** -9 if fp32 else 2.0 ** -9 + 2.0 ** -9 * (1 + 2.0 ** -9))
+    c = m.blockwise_gemm(a, sa, b, sb, m.WGRAD, m.OUT_FP32 if fp32 else m.OUT_BF16)
+    err = (c[ri][:, ci].double() - ref).abs()
+    assert (err <= bound).all(), (err / ref).max().item()
