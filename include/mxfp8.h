@@ -410,9 +410,11 @@ int mxfp8_blockwise_gemm_ws(const void* A_dev, const float* sA_dev, const void* 
                             void* stream);
 
 /*
- * Workspace bytes of mxfp8_blockwise_gemm_ws for one problem; 0 where it would not use one: a
- * product too small for the conversion to pay, a BF16 result of a longer reduction, or invalid
- * arguments.
+ * Workspace bytes of mxfp8_blockwise_gemm_ws for one problem; 0 where neither a forward (or data
+ * gradient) nor a weight gradient of these sizes would use one: the block-scaled MMA is tried
+ * where it is estimated to save power-of-two scales at least the 7 us that the conversion and the
+ * check cost others. 0 too for a BF16 result of a reduction longer than 2^17, invalid arguments
+ * or no supported device.
  */
 size_t mxfp8_blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
 

@@ -469,6 +469,8 @@ size_t mxfp8_blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int
   if (M <= 0 || N <= 0 || K <= 0 || M > 0x7FFFFF00 || N > 0x7FFFFF00 || K > 0x7FFFFF00)
     return 0;
   if (out_dtype != MXFP8_OUT_BF16 && out_dtype != MXFP8_OUT_FP32) return 0;
+  DeviceState* d = nullptr;
+  if (device_state(&d) != MXFP8_OK) return 0;
   return static_cast<size_t>(
       blockwise_gemm_workspace_bytes(M, N, K, out_dtype == MXFP8_OUT_FP32));
 }

@@ -1194,23 +1194,63 @@ int launch_swapped(const BlockwiseGemmArgs& a, const Params& p, cudaStream_t str
   return launch_single<BN, kSwapped>(a.B, a.N, a.A, a.M, a.K, p, plan.split, stream);
 }
 
-// From this many operations on, the gain of the block-scaled MMA for power-of-two scales
-// (1021 x 12288 x 4096: 41 us, 46 folded; more for larger products) is about what the
-// conversion and the check cost others (54 us), or more.
-constexpr double kMxMinFlops = 1e11;
+// How a product of more than 64 rows (or a weight gradient) is folded, and its estimated time.
+struct FoldPlan {
+  bool pairs;
+  int split;
+  double us;
+};
+
+FoldPlan fold_plan(int64_t M, int64_t N, int64_t nkb, bool wgrad) {
+  const int bn = wgrad ? 192 : 256;  // columns of a pair tile
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+  const Plan single = wgrad ? single_plan<128, kWgrad>(tiles, nkb) : single_plan<128, kFprop>(tiles, nkb);
+  const double pairs = pair_us(((M + 255) / 256) * ((N + bn - 1) / bn), nkb, wgrad);
+  return pairs < single.us ? FoldPlan{true, 1, pairs} : FoldPlan{false, single.split, single.us};
+}
+
+// The block-scaled MMA for power-of-two scales, with the conversion before and the folding
+// kernel's empty launch behind it: estimated microseconds. A block takes a 256-wide pair tile of
+// mxfp8_gemm 0.307 us, a 256 x 192 one of kMx 0.215; neither splits the reduction.
+double block_scaled_us(int64_t M, int64_t N, int64_t nkb, bool out_fp32) {
+  const int64_t pairs = num_sms() / 2, tiles = ((M + 255) / 256) * ((N + 191) / 192);
+  const double k = static_cast<double>(nkb);
+  return out_fp32 ? 9.6 + static_cast<double>((tiles + pairs - 1) / pairs) * (0.215 * k + 1.9)
+                  : 9.1 + dense_gemm_waves(M, N, false) * (0.307 * k + 1.3);
+}
+
+// What the conversion, the check and an empty launch cost a product whose scales turn out not to
+// be powers of two: the block-scaled MMA is tried where it saves others as much. Measured with both
+// kinds of scale at 112 sizes of 8 to 825 GFLOP, a third of them drawn at random, forward and weight
+// gradient, BF16 and FP32 results: the rule decides as the measured times would at 102 of them; what
+// it misses is mostly K of 512 or 1024, where stores count for more than estimated. Saved / paid,
+// us: forward BF16 4096 x 6144 x 4096 21 / 8, 4096^3 9 / 7, 2048 x 6144 x 4096 5 / 7, 512 x 512 x
+// 200000 -282 / 12; weight gradient FP32 6144 x 4096 x 2048 18 / 7, 1024 x 4096 x 4096 3 / 6, 1024
+// x 1024 x 65536 -18 / 9.
+constexpr double kCheckUs = 7;
 // The longest reduction that a BF16 result leaves to the tensor cores' own sum. They drop what lies
 // below the sum's last bit at each step of 32 products: up to 2^-23 of it, so K 2^-28 in all where
 // the products have one sign (measured, same sign, of sum |a b|: 0.002 at K = 2^20, 0.015 at 2^23;
-// the folding kernel 2e-6). Up to here that is 2^-11, a quarter of BF16's own rounding.
+// the folding kernel 2e-6). Up to here that is 2^-11, an eighth of BF16's own rounding.
 constexpr int64_t kMxMaxK = int64_t{1} << 17;
+
+bool block_scaled_pays(int64_t M, int64_t N, int64_t K, bool wgrad, bool out_fp32) {
+  if (M <= 128 || N <= 128 || (!out_fp32 && K > kMxMaxK)) return false;
+  const int64_t nkb = (K + BK - 1) / BK;
+  return fold_plan(M, N, nkb, wgrad).us - block_scaled_us(M, N, nkb, out_fp32) >= kCheckUs;
+}
+
+int64_t workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  const int64_t nkb = (K + BK - 1) / BK;
+  return ((M + 127) / 128 + (N + 127) / 128) * nkb * 512 + kConvertCtas * 4;
+}
 
 }  // namespace
 
 int64_t blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool out_fp32) {
-  if (M <= 128 || N <= 128 || 2.0 * M * N * K < kMxMinFlops) return 0;
-  if (!out_fp32 && K > kMxMaxK) return 0;
-  const int64_t nkb = (K + BK - 1) / BK;
-  return ((M + 127) / 128 + (N + 127) / 128) * nkb * 512 + kConvertCtas * 4;
+  return block_scaled_pays(M, N, K, false, out_fp32) || block_scaled_pays(M, N, K, true, out_fp32)
+             ? workspace_bytes(M, N, K)
+             : 0;
 }
 
 int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
@@ -1243,8 +1283,8 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
   p.ldc = a.N;
   p.nr = a.M;
   p.nc = a.N;
-  const int64_t need = a.workspace ? blockwise_gemm_workspace_bytes(a.M, a.N, a.K, a.out_fp32) : 0;
-  if (need > 0 && a.workspace_bytes >= static_cast<size_t>(need)) {
+  if (a.workspace && a.workspace_bytes >= static_cast<size_t>(workspace_bytes(a.M, a.N, a.K)) &&
+      block_scaled_pays(a.M, a.N, a.K, a.wgrad, a.out_fp32)) {
     const int64_t rta = (a.M + 127) / 128, rtb = (a.N + 127) / 128;
     if ((rta + rtb) * p.nkb > 0x7FFFFFFF) return MXFP8_ERR_INVALID_ARG;  // 32-bit tile index
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -1287,16 +1327,12 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream) {
     p.only_if = c.other;
     p.num_only_if = kConvertCtas;
   }
-  const int bn = a.wgrad ? 192 : 256;  // columns of a pair tile
-  const int64_t tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-  const Plan single =
-      a.wgrad ? single_plan<128, kWgrad>(tiles, p.nkb) : single_plan<128, kFprop>(tiles, p.nkb);
-  if (pair_us(((a.M + 255) / 256) * ((a.N + bn - 1) / bn), p.nkb, a.wgrad) < single.us)
+  const FoldPlan plan = fold_plan(a.M, a.N, p.nkb, a.wgrad);
+  if (plan.pairs)
     return a.wgrad ? launch_pairs<192, kWgrad>(a, p, stream)
                    : launch_pairs<256, kFprop>(a, p, stream);
-  return a.wgrad
-             ? launch_single<128, kWgrad>(a.A, a.M, a.B, a.N, a.K, p, single.split, stream)
-             : launch_single<128, kFprop>(a.A, a.M, a.B, a.N, a.K, p, single.split, stream);
+  return a.wgrad ? launch_single<128, kWgrad>(a.A, a.M, a.B, a.N, a.K, p, plan.split, stream)
+                 : launch_single<128, kFprop>(a.A, a.M, a.B, a.N, a.K, p, plan.split, stream);
 }
 
 }  // namespace mxfp8

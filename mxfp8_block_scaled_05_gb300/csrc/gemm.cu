@@ -1675,6 +1675,18 @@ bool half_tail_enabled() {
 // FLOPs; the 384-wide tile, two MMAs sharing A, is slightly cheaper per FLOP): 192 -> 0.78,
 // 256 -> 1, 384 -> 1.46; a last wave of half tiles costs 0.93 (256) or 0.78 (384, two
 // 192-wide halves). MXFP8_GEMM_BN=192, 256 or 384 forces a width.
+double duo_cost(int64_t M, int64_t N, int bn) {
+  const int64_t clusters = num_sms() / 2;
+  const double full = bn == 192 ? 0.78 : (bn == 256 ? 1.0 : 1.46);
+  const double halfc = bn == 256 ? 0.93 : 0.78;
+  const int64_t tiles = ((M + 255) / 256) * ((N + bn - 1) / bn);
+  const int64_t waves = tiles / clusters, tail = tiles % clusters;
+  double t = static_cast<double>(waves) * full;
+  if (tail > 0)
+    t += (bn != 192 && half_tail_enabled() && 2 * tail <= clusters) ? halfc : full;
+  return t;
+}
+
 int duo_width(int64_t M, int64_t N, bool fp32) {
   static const int forced = [] {
     const char* e = getenv("MXFP8_GEMM_BN");
@@ -1682,23 +1694,12 @@ int duo_width(int64_t M, int64_t N, bool fp32) {
     return (w == 256 || w == 192 || w == 384) ? w : 0;
   }();
   if (forced && !(forced == 384 && fp32)) return forced;
-  const int64_t clusters = num_sms() / 2;
-  auto cost = [&](int bn) {
-    const double full = bn == 192 ? 0.78 : (bn == 256 ? 1.0 : 1.46);
-    const double halfc = bn == 256 ? 0.93 : 0.78;
-    const int64_t tiles = ((M + 255) / 256) * ((N + bn - 1) / bn);
-    const int64_t waves = tiles / clusters, tail = tiles % clusters;
-    double t = static_cast<double>(waves) * full;
-    if (tail > 0)
-      t += (bn != 192 && half_tail_enabled() && 2 * tail <= clusters) ? halfc : full;
-    return t;
-  };
   int best = 256;
-  double best_t = cost(256);
+  double best_t = duo_cost(M, N, 256);
   const int others[2] = {192, 384};
   for (int bn : others) {
     if (bn == 384 && (fp32 || !wide_tiles_enabled())) continue;
-    const double t = cost(bn);
+    const double t = duo_cost(M, N, bn);
     if (t < best_t) best = bn, best_t = t;
   }
   return best;
@@ -1888,6 +1889,10 @@ bool make_scale_map(CUtensorMap* map, const void* base, int64_t row_tiles, int64
 
 bool make_store_map(CUtensorMap* map, void* base, int64_t rows, int64_t N, bool fp32) {
   return make_out_map(map, base, rows, N, 1, fp32, 2);
+}
+
+double dense_gemm_waves(int64_t M, int64_t N, bool fp32) {
+  return duo_cost(M, N, duo_width(M, N, fp32));
 }
 
 uint64_t pipeline_wait_ns() { return wait_limit_ns(); }

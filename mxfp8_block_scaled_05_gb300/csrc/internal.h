@@ -118,6 +118,9 @@ int launch_blockwise_gemm(const BlockwiseGemmArgs& a, cudaStream_t stream);
 // Workspace with which power-of-two scales run on the block-scaled MMA (0: never).
 int64_t blockwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool out_fp32);
 
+// Estimated time of launch_gemm on CTA pairs per K stage, in that of one wave of 256-wide tiles.
+double dense_gemm_waves(int64_t M, int64_t N, bool fp32);
+
 // Tensor map of a row-major byte matrix [outer][inner] in 128-byte x box_outer boxes with
 // the 128-byte swizzle.
 bool make_operand_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
