@@ -23,7 +23,7 @@ def head(hidden, weight, scale_type):
     """logits = hidden . weight^T in block-wise FP8."""
     x, sx = m.quantize_blockwise_1d(hidden, m.ROW, scale_type)
     w, sw = m.quantize_blockwise(weight, scale_type)
-    return m.blockwise_gemm(x, sx, w, sw, m.FPROP)
+    return m.blockwise_gemm(x, sx, w, sw, m.FPROP, scale_type=scale_type)
 
 
 def sample(hidden, weight, temperature, generator):

@@ -508,13 +508,18 @@ def blockwise_gemm_workspace_bytes(m: int, n: int, k: int, out_dtype: int = OUT_
 
 def blockwise_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
                    op: int = FPROP, out_dtype: int = OUT_BF16, out=None, stream=None,
-                   workspace=None) -> torch.Tensor:
+                   workspace=None, scale_type: Optional[int] = None) -> torch.Tensor:
     """C[M, N] = deq(A)[M, K] . deq(B)[N, K]^T of block-wise FP8 operands (both K-major). A
     and sa as quantize_blockwise_1d writes them; B and sb as quantize_blockwise does (128 x
     128 blocks), or for WGRAD as quantize_blockwise_1d does. K % 16 == 0, N % 8 == 0. Large
     products take a workspace of blockwise_gemm_workspace_bytes(...) bytes, in which scales
     are laid out for the block-scaled MMA if all are powers of two; without one given (a uint8
-    CUDA tensor) it is allocated for the call."""
+    CUDA tensor) it is allocated for the call. With one that is too small, an empty one for
+    instance, the scales are folded in without a look at them. So they are with
+    scale_type=BW_FP32, by which a caller whose scales are not powers of two saves the look (7 us
+    or more of a large product); BW_POW2 is what None does: the device looks."""
+    if scale_type not in (None, BW_FP32, BW_POW2):
+        raise ValueError(f"scale_type must be None, BW_FP32 or BW_POW2, got {scale_type}")
     _require(a, torch.uint8, "A")
     _require(b, torch.uint8, "B")
     m, k = a.shape
@@ -530,7 +535,8 @@ def blockwise_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     if m and n and k:  # the scales are read only when there is a reduction to run
         _buffer(sa, torch.float32, kb * m, "sA")
         _buffer(sb, torch.float32, kb * (n if op == WGRAD else (n + 127) // 128), "sB")
-    need = lib().mxfp8_blockwise_gemm_workspace_bytes(m, n, k, out_dtype) if m > 128 else 0
+    look = m > 128 and scale_type != BW_FP32
+    need = lib().mxfp8_blockwise_gemm_workspace_bytes(m, n, k, out_dtype) if look else 0
     if workspace is not None:
         _require(workspace, torch.uint8, "workspace")
     elif need:

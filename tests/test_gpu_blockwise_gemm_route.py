@@ -58,3 +58,22 @@ def test_where_it_pays(m, mm, n, k, wgrad, fp32):
     other[1].view(-1)[3] *= 1.5                 # not a power of two: folded
     c, folded = both(m, other, wgrad, m.OUT_FP32 if fp32 else m.OUT_BF16)
     assert torch.equal(c, folded)
+
+
+@pytest.mark.parametrize("mm,n,k,wgrad,fp32", [(4096, 4096, 4096, False, False),
+                                               (2056, 2048, 8192, True, True)])
+def test_caller_states_the_scale_type(m, mm, n, k, wgrad, fp32):
+    """BW_FP32 folds without a look at the scales (and without a workspace); BW_POW2 is the
+    default's result."""
+    ops = operands(mm, mm, n, k, wgrad)
+    op, dtype = m.WGRAD if wgrad else m.FPROP, m.OUT_FP32 if fp32 else m.OUT_BF16
+    c, folded = both(m, ops, wgrad, dtype)
+    assert not torch.equal(c, folded)
+    out = torch.empty_like(c)
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    m.blockwise_gemm(*ops, op, dtype, out=out, scale_type=m.BW_FP32)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+    assert torch.equal(out, folded)
+    assert torch.equal(m.blockwise_gemm(*ops, op, dtype, scale_type=m.BW_POW2), c)
+    with pytest.raises(ValueError):
+        m.blockwise_gemm(*ops, op, dtype, scale_type=2)
