@@ -96,11 +96,22 @@ def _check(status: int, what: str):
         raise MXFP8Error(status, what)
 
 
+# The current stream's handle and the current device, asked for directly: building the stream's
+# Python object takes 2.9 us on the GB300's host, as long as the launch itself. The direct names
+# are torch's own, and a version without them takes the public way.
+try:
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _device
+except ImportError:
+    _device = torch.cuda.current_device
+
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+
 def _stream(stream=None):
-    """A stream's handle. The current stream is asked for directly: building its Python
-    object takes 2.9 us on the GB300's host, as long as the launch itself."""
+    """A stream's handle."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -112,7 +123,7 @@ def _require(t: torch.Tensor, dtype, name: str):
     """A tensor handed to the library: CUDA, of this dtype, contiguous, and on the current
     device (the library runs every call on the current device)."""
     if (t.is_cuda and t.dtype is dtype and t.is_contiguous()
-            and t.get_device() == torch._C._cuda_getDevice()):
+            and t.get_device() == _device()):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
