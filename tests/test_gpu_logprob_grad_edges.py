@@ -51,3 +51,15 @@ def test_empty_row_gets_zeros_whatever_its_weights(m, dtype, weight, vocab):
     got = m.token_logprobs_backward(x, t, r.stats, r.entropy, bad, bad, r.top_id, gt)
     assert (got[1:3] == 0).all()
     assert torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,vocab,pitch", [(3, 70001, 70016), (1, 131072, 131072)])
+def test_in_place_with_rows_split_over_ctas(m, dtype, rows, vocab, pitch):
+    x, t = make(5, rows, vocab, dtype, pitch)
+    r = m.token_logprobs(x, t, 1.0, 5)
+    g = torch.randn(rows, device=DEV)
+    gt = torch.randn(rows, 5, device=DEV)
+    want = m.token_logprobs_backward(x, t, r.stats, r.entropy, g, g, r.top_id, gt)
+    got = m.token_logprobs_backward(x, t, r.stats, r.entropy, g, g, r.top_id, gt, out=x)
+    assert got.data_ptr() == x.data_ptr() and torch.equal(got, want)
