@@ -520,7 +520,8 @@ int mxfp8_selfcheck_noalloc(const void* w_codes_dev, const void* w_scales_dev,
  * Masks: a logit of -inf has probability 0. A row whose logits are all -inf has log
  * probability -inf (0 if not scored), entropy 0, stats (-inf, 0) and no top tokens. A row
  * holding a NaN or +inf gives NaN (top_id -1).
- * Sums are FP32. Deterministic. rows == 0 is a no-op.
+ * Sums are FP32: log_sum is off by at most (max(256, vocab / 256) + 64) 2^-24 + 2^-20.
+ * Deterministic. rows == 0 is a no-op.
  * Errors: MXFP8_ERR_INVALID_ARG (negative sizes, vocab == 0 or above 2^31 - 1, ld < vocab,
  * a temperature that is not positive or whose reciprocal is not a finite, normal float, top
  * out of range, unknown dtype, null pointers), MXFP8_ERR_ALIGNMENT.
@@ -542,7 +543,10 @@ int mxfp8_token_logprobs(const void* logits_dev, int logits_dtype, int64_t rows,
  *                     id is skipped, and its gt is not read. One at or past vocab, like such
  *                     a target, makes the row NaN and latches MXFP8_ERR_BAD_TARGET.
  *   grad_logits_dev   the logits' dtype, [rows][grad_ld], its first `vocab` columns
- *                     written; may be the logits' own buffer (then grad_ld == ld)
+ *                     written; may be the logits' own buffer (then grad_ld == ld), else
+ *                     the two may not overlap. Where its rows start at another place within
+ *                     16 bytes than the logits' (another alignment, or pitches that differ by
+ *                     no multiple of 16 bytes), values go one at a time: 2 to 3 times slower
  * A row whose logits are all -inf gets zeros, whatever its g, h and gt. Errors as above.
  */
 int mxfp8_token_logprobs_backward(const void* logits_dev, int logits_dtype, int64_t rows,

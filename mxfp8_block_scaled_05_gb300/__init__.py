@@ -635,7 +635,8 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: 
     token_logprobs' logprob, entropy and top_logprob are given (float32; the last two
     optional). `stats`, `entropy` and `top_id` are that call's, `temperature` its
     temperature. The result has the logits' type, shape and row pitch; `out` may be any such
-    tensor of contiguous rows, the logits themselves included."""
+    tensor of contiguous rows, the logits themselves included (another place within 16 bytes
+    than the logits' makes the call 2 to 3 times slower)."""
     dt, rows, vocab, pitch = _logits(logits, "logits")
     _buffer(targets, torch.int64, rows, "targets")
     _buffer(stats, torch.float32, 2 * rows, "stats")

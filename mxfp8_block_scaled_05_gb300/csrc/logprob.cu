@@ -8,9 +8,11 @@
 // With m = max x, d = (x - m) / T and S = sum e^d:
 //   log p_v = d_v - log S,   H = -sum p log p = log S - sum(e^d d) / S.
 // Everything is taken relative to the row's maximum, so no large log-sum-exp is subtracted
-// from a large logit. Sums, maxima and statistics are FP32 (per thread over a few hundred
-// values, then joined pairwise); powers are taken in base 2 (one multiplication by
-// log2(e) / T, then ex2).
+// from a large logit. Sums, maxima and statistics are FP32. A thread adds up at most max(256,
+// vocab / 256) values in order (an eighth of that where 8 CTAs share a row), then threads and
+// CTAs are joined pairwise, so log S is off by at most (that number + 64) 2^-24 + 2^-20. Powers are
+// taken in base 2: one multiplication by log2(e) / T, then ex2.approx, which is 2^-22 off at most
+// and takes one instruction: a choice for speed, well inside that bound.
 //
 // Masks: a logit of -inf (or one so far below the maximum that e^d vanishes, such as the
 // type's lowest value) has probability 0 and adds nothing to the entropy. t = d log2(e) is
@@ -385,7 +387,7 @@ __device__ __forceinline__ void find_top(Shared<kThreads>& sh, const T* row, con
 //
 // Bound by memory (2 or 4 bytes a logit): 16-byte loads, four of them in flight a thread, each
 // logit read once. 4096 x 131072 BF16: 159 us (6.7 TB/s), 179 with the 8 likeliest tokens. One
-// row of 131072 takes 3.5 us, 6.8 with the 5 likeliest.
+// row of 131072 takes 4.1 us, 7.2 with the 5 likeliest, 8.7 with 20.
 // Rows are split over a cluster only when there are too few of them to fill the GPU; each
 // CTA then hands its sums and best keys to the first through distributed shared memory,
 // without a workspace.
@@ -443,7 +445,6 @@ logprob_kernel(const Params p, int split) {
                         has_tail ? Vec<T>::load(row + tail0 + tid) : -kInf};
     sm.add(x, c);
   }
-  const float own_max = sm.m;
   // join the CTA's threads
   auto join_lanes = [&](int lanes) {
     for (int o = lanes / 2; o > 0; o >>= 1) {
@@ -564,8 +565,11 @@ struct GradParams {
 // gradient written once. The few columns that a token or an alternative names are written
 // a second time, complete, by the CTA that owns them; their logits are read before
 // anything is written, so `out` may be the logits' own buffer.
+// p_v comes from log S in FP32, so a row's p share a factor that is off by half an ulp of log S
+// (5e-7 near 10); the three numbers that the forward call saves a row hold no more.
 // kVector: logits and gradient rows share their place within 16 bytes and go in 16-byte
-// pieces; otherwise one value at a time.
+// pieces; otherwise one value at a time, in 3.3 times the time for BF16 (4096 x 32000: 265 us, 81
+// in pieces) and 2.2 for FP32 (509 x 32003 in rows of 32064, result packed: 42 us, 19).
 template <typename T, bool kVector>
 __global__ void __launch_bounds__(kThreads)
 logprob_grad_kernel(const GradParams p) {
@@ -715,7 +719,7 @@ cudaError_t launch_forward(const Params& p, int split, cudaStream_t stream) {
            : threads == 128 ? logprob_kernel<T, kTop, 128>
                             : logprob_kernel<T, kTop, 64>;
   // Up to two CTAs an SM may take their places while the kernel before still runs, which saves
-  // 0.6 us (1 x 131072: 3.8 us, 4.4 without). Of more, some SMs would get two fewer than others
+  // 0.6 us (of 1 x 131072). Of more, some SMs would get two fewer than others
   // that way: 500 x 131072 BF16, top 5: 34 us, 38 with early places; 400 x 32000: 12.4 and 15.4.
   const bool early = grid <= 2u * static_cast<unsigned>(num_sms());
   return launch(k, grid, threads, split, early, stream, p, split);
@@ -728,8 +732,8 @@ cudaError_t launch_logprob(const LogprobArgs& a, cudaStream_t stream) {
   Params p{a.logits, a.rows, a.vocab, a.ld, a.targets, a.inv_t, a.logprob, a.entropy,
            a.stats, a.top, a.top_logprob, a.top_id, a.status};
   // CTAs per row: one for each SM while a part keeps 2048 values, two while it keeps 4096
-  // 16-byte vectors, 16 a thread (top 5: 253 x 50021 FP32 16.5 us in halves, 18.6 whole; 128 x
-  // 32000 BF16 10.3 in halves, 11.5 in quarters)
+  // 16-byte vectors, 16 a thread (top 5: 253 x 50021 FP32 takes 11% less in halves than whole;
+  // 128 x 32000 BF16 12% more in quarters than in halves)
   const int64_t per_vector = a.fp32 ? 4 : 8;
   int split = 1;
   while (split < kMaxSplit && a.vocab >= 4096 * split &&
