@@ -20,10 +20,12 @@
 // leave the chain does: the producer copies the scales (with each fold warp fetching its own:
 // 4096 x 24576 x 4096 317 us, 299 now; weight gradient 6144 x 4096 x 4096 132 and 112), and
 // one barrier a block says that both its product and its scales are there.
-// Measured on GB300, BF16 results: 4096 x 24576 x 4096 299 us (2.76 PFLOP/s), 4096^3 58 us
-// (2.38); weight gradient 6144 x 4096 x 4096 112 us (1.83), with FP32 results and K = 4016
-// 122 us. Few rows are bound by the weights' bytes: 1 x 24576 x 4096 13 us (7.8 TB/s, part of
-// it from L2), 37 rows 21 us; 1 x 4096 x 4096 takes 5.8 us, mostly launch and latency.
+// Measured on GB300, BF16 results, kernels back to back: 4096 x 24576 x 4096 300 us (2.75
+// PFLOP/s; up to 325 once the GPU is at its power limit), 4096^3 58 us (2.37); weight gradient
+// 6144 x 4096 x 4096 115 us (1.79), 119 with FP32 results, 121 at K = 4016. One row is bound by the
+// weights' bytes: 1 x 24576 x 4096 13 us (7.8 TB/s, part of it from L2); 1 x 4096 x 4096 takes 6.1
+// us, mostly launch and latency. 37 x 24576 x 4096 takes 21 us, bound by 192 tiles on 152 SMs, 40
+// of which run two (152 tiles take 14.3).
 //
 // Roles: warp 0 TMA producer and scales, warp 1 MMA issuer (and TMEM allocation), the last 8 or
 // 12 warps fold and store: one per TMEM lane quarter and group of columns.
@@ -36,7 +38,7 @@
 //             tiles of A (128 x 4096 x 4096: 10.4 swapped, 8.8 in those)
 //   kMx       both with power-of-two scales, as E8M0 scales of the block-scaled MMA: FP32 results
 //             of those (see the conversion kernel). TMEM adds up four blocks, the fold warps
-//             those sums. 6144 x 4096 x 4096 80 us, 119 with the scales folded in
+//             those sums. 6144 x 4096 x 4096 78 us, 119 with the scales folded in
 // and by size: pairs of CTAs (cta_group::2, 256 x 256 tiles, 256 x 192 of the weight gradient and
 // kMx, each SM stages half of the column operand), or single CTAs (128 x BN tiles) whose reduction
 // may be split over a cluster, the parts joined through distributed shared memory in rank
@@ -969,13 +971,13 @@ blockwise_gemm_kernel(const __grid_constant__ CUtensorMap map_r,
 // scales are powers of two is known on the device only: this kernel writes the scales in the
 // MMA's 128 x 4 tile layout and, for each CTA, a word that says whether it met another one.
 // The block-scaled kernel then returns at once if any word is set, the folding one if none
-// is. BF16 results come from mxfp8_gemm. The tensor cores' own sum over all of K is 2e-6 off (K =
-// 4096), which a BF16 result's rounding covers; for FP32 results kMx takes only 512 products at
-// a time from them (3e-7 off) and adds those up in FP32 registers.
-// Measured, BF16: 4096 x 24576 x 4096 240 us (3.4 PFLOP/s), 299 folded; weight gradient 6144 x
-// 4096 x 4096 67 and 112; FP32: 80 and 119, 4096 x 12288 x 8192 277 and 440. Scales that turn
-// out not to be powers of two pay the two other launches: 311 us for the first, 54 instead of
-// 46 at 1021 x 12288 x 4096.
+// is. BF16 results come from mxfp8_gemm, where the tensor cores sum over all of K (see kMxMaxK); for
+// FP32 results kMx takes only 512 products at a time from them and adds those up in FP32
+// registers (products of one sign, K = 4096 to 32768: 1.2e-6 off, 7e-7 folded; of both, 1e-7 and
+// 6e-8). Measured back to back, BF16: 4096 x 24576 x 4096 228 to 246 us (3.6 to 3.4 PFLOP/s, by
+// power; a single call with cold caches 256), 300 to 325 folded; weight gradient 6144 x 4096 x 4096
+// 66 and 115; FP32: 78 and 119, 4096 x 12288 x 8192 274 and 438. Scales that turn out not to be
+// powers of two pay the two other launches: 65 us instead of 58 at 4096^3.
 constexpr int kConvertCtas = 608;  // four on each SM
 constexpr int kConvertThreads = 256;
 
@@ -1204,7 +1206,8 @@ struct FoldPlan {
 FoldPlan fold_plan(int64_t M, int64_t N, int64_t nkb, bool wgrad) {
   const int bn = wgrad ? 192 : 256;  // columns of a pair tile
   const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-  const Plan single = wgrad ? single_plan<128, kWgrad>(tiles, nkb) : single_plan<128, kFprop>(tiles, nkb);
+  const Plan single =
+      wgrad ? single_plan<128, kWgrad>(tiles, nkb) : single_plan<128, kFprop>(tiles, nkb);
   const double pairs = pair_us(((M + 255) / 256) * ((N + bn - 1) / bn), nkb, wgrad);
   return pairs < single.us ? FoldPlan{true, 1, pairs} : FoldPlan{false, single.split, single.us};
 }
