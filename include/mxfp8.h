@@ -61,10 +61,12 @@ typedef enum mxfp8_status {
   MXFP8_ERR_UNSUPPORTED_ARCH = 3, /* current device is not compute capability 10.3 */
   MXFP8_ERR_CUDA = 4,             /* a CUDA runtime/driver call failed */
   MXFP8_ERR_BAD_OFFSETS = 5,      /* (device) expert offsets not 0-based, non-decreasing,
-                                     32-aligned and ending at total_rows */
+                                     32-aligned and ending at total_rows; a routing plan of
+                                     more rows than total_rows */
   MXFP8_ERR_TIMEOUT = 6,          /* (device) a pipeline wait in a kernel ran out; the
                                      kernel abandoned its work */
-  MXFP8_ERR_BAD_TARGET = 7        /* (device) a token id at or past the vocabulary */
+  MXFP8_ERR_BAD_TARGET = 7,       /* (device) a token id at or past the vocabulary */
+  MXFP8_ERR_BAD_EXPERT = 8        /* (device) an expert id at or past the number of experts */
 } mxfp8_status;
 
 typedef enum mxfp8_axis {
@@ -558,6 +560,133 @@ int mxfp8_token_logprobs_backward(const void* logits_dev, int logits_dtype, int6
                                   void* grad_logits_dev, int64_t grad_ld, void* stream);
 
 /*
+ * Routing of tokens to experts: what makes the token segments that the grouped calls read, and
+ * takes their results back. Entry i = t * top_k + j is token t's j-th choice of an expert. A
+ * plan is three int32 arrays that mxfp8_route writes:
+ *   offsets   [num_experts + 1], the segments as mxfp8_quantize_grouped and mxfp8_grouped_gemm
+ *             take them: starts at 0, multiples of 32, ends at total_rows
+ *   row_of    [tokens * top_k], the segment row of each entry, -1 for an entry of no expert
+ *   entry_of  [total_rows], the entry of each row, -1 for a padding row
+ * The pages pad token segments to multiples of 32 (section "The pipeline", learner paragraph) and
+ * train a mixture of experts (section "A held-out workload, and end to end", Table 4); how tokens
+ * get to their experts is this library's.
+ */
+
+/*
+ * A number of rows that the segments of any choice fit in: tokens * top_k, plus 31 rows of
+ * padding for each expert that can be in use, rounded down to a multiple of 32. 0 for no entries and
+ * for invalid arguments (negative tokens, top_k < 1, num_experts outside 1 .. 1024, or a result
+ * above 2^31 - 256).
+ */
+int64_t mxfp8_route_rows(int64_t tokens, int top_k, int num_experts);
+
+/*
+ * Sorts the entries by expert. Entries of an expert keep their order, so the plan does not
+ * depend on timing.
+ *   ids_dev      int64 [tokens][top_k], 8-byte aligned. A negative id is an entry of no expert
+ *                (a dropped token, a padding token). One at or past num_experts is treated so
+ *                too, and latches MXFP8_ERR_BAD_EXPERT. A token may name an expert twice.
+ *   total_rows   a multiple of 32: mxfp8_route_rows, or fewer where the caller knows the counts.
+ *                The last expert's segment takes the rows that are left over, as padding. If the
+ *                segments need more, the plan is one of no entries (offsets 0 .. 0, total_rows;
+ *                all else -1) and MXFP8_ERR_BAD_OFFSETS is latched.
+ *   offsets_dev, row_of_dev, entry_of_dev   the plan, written in full
+ * tokens * top_k up to 2^31 - 256, num_experts 1 .. 1024. No entries: ids_dev and row_of_dev may
+ * be NULL; total_rows == 0: entry_of_dev too.
+ */
+int mxfp8_route(const int64_t* ids_dev, int64_t tokens, int top_k, int num_experts,
+                int64_t total_rows, int32_t* offsets_dev, int32_t* row_of_dev,
+                int32_t* entry_of_dev, void* stream);
+
+/*
+ * Copies the tokens' rows into the segments: out[row_of[i]] = w_i x[i / top_k]; padding rows
+ * become zero. The gradient of x is mxfp8_combine without weights; that of the weights is the
+ * inner products mxfp8_combine_backward gives.
+ *   x_dev        [tokens][cols], BF16 or FP32 (dtype: MXFP8_OUT_BF16 / MXFP8_OUT_FP32)
+ *   weights_dev  float [tokens][top_k], or NULL for 1 (the values then move unchanged). Products
+ *                are FP32, rounded once.
+ *   out_dev      [total_rows][cols], of x's type, written in full; may not overlap x
+ * Any cols; the fast path needs rows of a multiple of 16 bytes. x and out start on 16 bytes.
+ * A plan whose rows do not fit total_rows is not followed there: MXFP8_ERR_BAD_OFFSETS is latched
+ * and the row skipped.
+ */
+int mxfp8_dispatch(const void* x_dev, int dtype, int64_t tokens, int64_t cols, int top_k,
+                   const float* weights_dev, const int32_t* row_of_dev,
+                   const int32_t* entry_of_dev, int64_t total_rows, void* out_dev, void* stream);
+
+/*
+ * mxfp8_dispatch of BF16 rows straight into the grouped GEMMs' MXFP8 operands: the bytes are
+ * those of mxfp8_quantize_grouped on the dispatched rows, which are never written.
+ *   row_out_dev, row_scales_dev   the ROW copy, E4M3 [total_rows][cols]; cols % 32 == 0
+ *   col_out_dev, col_scales_dev   the COL copy, E4M3 [cols][total_rows]; cols % 8 == 0
+ * Either copy may be left out (both its pointers NULL), not both. Scale buffers hold
+ * mxfp8_grouped_scale_bytes(total_rows, cols, num_experts, axis) bytes and are written in full:
+ * zeros follow the last block. Invalid offsets latch MXFP8_ERR_BAD_OFFSETS and write nothing.
+ * total_rows == 0 or cols == 0 is a no-op.
+ */
+int mxfp8_quantize_dispatch(const void* x_dev, int64_t tokens, int64_t cols, int top_k,
+                            const float* weights_dev, const int32_t* entry_of_dev,
+                            int64_t total_rows, const int32_t* offsets_dev, int num_experts,
+                            void* row_out_dev, void* row_scales_dev, void* col_out_dev,
+                            void* col_scales_dev, void* stream);
+
+/*
+ * Sums the segments' rows back to their tokens: out[t] = sum_j w_i y[row_of[i]], i = t top_k + j,
+ * over the entries that have a row (none: zeros; their weights are not read). FP32 sums in the order
+ * of j, rounded once. Without weights this is the gradient of mxfp8_dispatch without weights.
+ *   y_dev        [total_rows][cols], BF16 or FP32
+ *   weights_dev  float [tokens][top_k], or NULL for 1
+ *   out_dev      [tokens][cols], of y's type; may not overlap y
+ * Sizes, alignment and errors as for mxfp8_dispatch.
+ */
+int mxfp8_combine(const void* y_dev, int dtype, int64_t total_rows, int64_t cols, int64_t tokens,
+                  int top_k, const float* weights_dev, const int32_t* row_of_dev, void* out_dev,
+                  void* stream);
+
+/*
+ * Gradients of mxfp8_combine: grad_y[row_of[i]] = w_i grad_out[t] (zeros in padding rows), and
+ * grad_weights[i] = <grad_out[t], y[row_of[i]]> (0 for an entry without a row), FP32 sums.
+ *   grad_out_dev      [tokens][cols], of y's type
+ *   grad_y_dev        [total_rows][cols], of y's type, written in full, or NULL where only the
+ *                     weights' gradient is wanted (entry_of_dev may then be NULL): the rows'
+ *                     gradient also comes from mxfp8_quantize_dispatch(grad_out, weights), on the
+ *                     MXFP8 grid. May be y itself, else the two may not overlap.
+ *   grad_weights_dev  float [tokens][top_k]
+ */
+int mxfp8_combine_backward(const void* grad_out_dev, const void* y_dev, int dtype,
+                           int64_t tokens, int64_t cols, int top_k, const float* weights_dev,
+                           const int32_t* row_of_dev, const int32_t* entry_of_dev,
+                           int64_t total_rows, void* grad_y_dev, float* grad_weights_dev,
+                           void* stream);
+
+/*
+ * The gated activation h = silu(g) * u, silu(g) = g / (1 + e^-g), of x = [g | u], with x kept in 8
+ * bits for the backward pass (2.0625 bytes for each value of h, 4 as BF16).
+ *   x_dev       BF16 [rows][2 * width], width % 32 == 0
+ *   h_dev       BF16 [rows][width], from x itself, rounded once
+ *   codes_dev   E4M3 [rows][2 * width], scales_dev [rows][2 * width / 32]: the bytes of
+ *               mxfp8_quantize_rule(x, ROW, LINEAR, scale_rule); both NULL: not kept.
+ *               MXFP8_RULE_CEIL saturates nothing: every value of a block is then within 2^-4 of
+ *               itself or within 2^-17 of the block's largest.
+ * A gate of -inf gives NaN; sigmoids below 2^-126 are 0.
+ * All buffers start on 16 bytes (scales_dev anywhere). rows == 0 or width == 0 is a no-op.
+ */
+int mxfp8_swiglu(const void* x_dev, int64_t rows, int64_t width, void* h_dev, void* codes_dev,
+                 void* scales_dev, int scale_rule, void* stream);
+
+/*
+ * Gradient of mxfp8_swiglu from what it kept: with g, u the kept values, s = 1 / (1 + e^-g),
+ *   grad_x = [grad_h u s (1 + g (1 - s)) | grad_h g s], and h = g s u again,
+ * FP32, each rounded to BF16 once. A block kept with a NaN scale gives NaN.
+ *   grad_h_dev  BF16 [rows][width]
+ *   grad_x_dev  BF16 [rows][2 * width]; may not overlap the inputs
+ *   h_dev       BF16 [rows][width], or NULL: not wanted. May be grad_h itself.
+ */
+int mxfp8_swiglu_backward(const void* grad_h_dev, const void* codes_dev, const void* scales_dev,
+                          int64_t rows, int64_t width, void* grad_x_dev, void* h_dev,
+                          void* stream);
+
+/*
  * Sets how long a GEMM kernel's pipeline waits (a stage's copies, the tensor cores, the
  * accumulator hand-over) may take before the kernel gives up, for every GEMM launched
  * after the call, in any host thread: `ns` nanoseconds, or the default for ns == 0
@@ -574,8 +703,8 @@ int mxfp8_set_wait_limit_ns(uint64_t ns);
 /*
  * Synchronizes `stream`, then returns and clears the current device's status word:
  * MXFP8_OK, or the first device-side error latched since the last call
- * (MXFP8_ERR_BAD_OFFSETS, MXFP8_ERR_TIMEOUT, MXFP8_ERR_BAD_TARGET), or MXFP8_ERR_CUDA if
- * the synchronization itself failed. The word is read and cleared in one atomic exchange, enqueued on
+ * (MXFP8_ERR_BAD_OFFSETS, MXFP8_ERR_TIMEOUT, MXFP8_ERR_BAD_TARGET, MXFP8_ERR_BAD_EXPERT), or
+ * MXFP8_ERR_CUDA if the synchronization itself failed. The word is read and cleared in one atomic exchange, enqueued on
  * `stream` after its earlier work. An error that a kernel on another stream latches
  * concurrently is reported by this call or by the next one; it is never cleared unread.
  */

@@ -23,7 +23,7 @@ RULE_FLOOR, RULE_CEIL = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
 
 OK, ERR_INVALID_ARG, ERR_ALIGNMENT, ERR_UNSUPPORTED_ARCH, ERR_CUDA, ERR_BAD_OFFSETS, \
-    ERR_TIMEOUT, ERR_BAD_TARGET = range(8)
+    ERR_TIMEOUT, ERR_BAD_TARGET, ERR_BAD_EXPERT = range(9)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxfp8.so")
 
@@ -57,6 +57,15 @@ SIGNATURES = {
     "mxfp8_token_logprobs": (_I, [_P, _I, _I64, _I64, _I64, _P, _D, _P, _P, _P, _I, _P, _P, _P]),
     "mxfp8_token_logprobs_backward": (_I, [_P, _I, _I64, _I64, _I64, _P, _D, _P, _P, _P, _P, _I,
                                            _P, _P, _P, _I64, _P]),
+    "mxfp8_route_rows": (_I64, [_I64, _I, _I]),
+    "mxfp8_route": (_I, [_P, _I64, _I, _I, _I64, _P, _P, _P, _P]),
+    "mxfp8_dispatch": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _P, _I64, _P, _P]),
+    "mxfp8_quantize_dispatch": (_I, [_P, _I64, _I64, _I, _P, _P, _I64, _P, _I, _P, _P, _P, _P,
+                                     _P]),
+    "mxfp8_combine": (_I, [_P, _I, _I64, _I64, _I64, _I, _P, _P, _P, _P]),
+    "mxfp8_combine_backward": (_I, [_P, _P, _I, _I64, _I64, _I, _P, _P, _P, _I64, _P, _P, _P]),
+    "mxfp8_swiglu": (_I, [_P, _I64, _I64, _P, _P, _P, _I, _P]),
+    "mxfp8_swiglu_backward": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _P]),
     "mxfp8_selfcheck_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "mxfp8_selfcheck": (_I, [_P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _SZ, _P, _P]),
     "mxfp8_selfcheck_noalloc": (_I, [_P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _P]),
@@ -677,6 +686,276 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: 
         top, _ptr(top_id) if top else None, _ptr(grad_top) if top else None, _ptr(out),
         out_pitch, _stream(stream)), "mxfp8_token_logprobs_backward")
     return out
+
+
+# ------------------------------------------------------------- routing tokens to experts
+
+class RoutePlan(NamedTuple):
+    """Entries (token, choice) sorted by expert into segments padded to 32 rows (route). All
+    int32, on the device."""
+    offsets: torch.Tensor   # [num_experts + 1], as quantize_grouped and grouped_gemm take them
+    row_of: torch.Tensor    # [tokens, top_k], the row of each entry; -1: of no expert
+    entry_of: torch.Tensor  # [rows], the entry (token * top_k + choice) of each row; -1: padding
+
+
+def route_rows(tokens: int, top_k: int, num_experts: int) -> int:
+    """Rows that the segments of any choice of experts fit in."""
+    rows = int(lib().mxfp8_route_rows(tokens, top_k, num_experts))
+    if rows == 0 and tokens != 0:
+        raise ValueError(f"no segments for tokens={tokens} top_k={top_k} "
+                         f"num_experts={num_experts}")
+    return rows
+
+
+def route(ids: torch.Tensor, num_experts: int, rows: Optional[int] = None,
+          stream=None) -> RoutePlan:
+    """Sorts the entries of ids (int64 [tokens, top_k], negative: of no expert) by expert, each
+    expert's in their order. `rows` (default: route_rows, which any choice fits) may be fewer
+    where the caller knows the experts' counts; the last segment takes what is left over."""
+    _require(ids, torch.int64, "ids")
+    if ids.dim() != 2 or ids.shape[1] < 1:
+        raise ValueError(f"ids must be [tokens, top_k], got {tuple(ids.shape)}")
+    tokens, top_k = ids.shape
+    if rows is None:
+        rows = route_rows(tokens, top_k, num_experts)
+    elif rows < 0:
+        raise ValueError(f"rows must not be negative, got {rows}")
+    dev = ids.device
+    offsets = _new((max(num_experts, 0) + 1,), torch.int32, dev, stream)
+    row_of = _new((tokens, top_k), torch.int32, dev, stream)
+    entry_of = _new((rows,), torch.int32, dev, stream)
+    _check(lib().mxfp8_route(_ptr(ids), tokens, top_k, num_experts, rows, _ptr(offsets),
+                             _ptr(row_of), _ptr(entry_of), _stream(stream)), "mxfp8_route")
+    return RoutePlan(offsets, row_of, entry_of)
+
+
+def _plan(plan: RoutePlan, weights, tokens: Optional[int] = None):
+    """A plan's tensors, and the weights beside them, checked. Returns (tokens, top_k, rows)."""
+    _require(plan.row_of, torch.int32, "plan.row_of")
+    _require(plan.entry_of, torch.int32, "plan.entry_of")
+    if plan.row_of.dim() != 2 or plan.row_of.shape[1] < 1:
+        raise ValueError(f"plan.row_of must be [tokens, top_k], got {tuple(plan.row_of.shape)}")
+    n, top_k = plan.row_of.shape
+    if tokens is not None and tokens != n:
+        raise ValueError(f"{tokens} rows of tokens; the plan is of {n}")
+    if weights is not None:
+        _require(weights, torch.float32, "weights")
+        if weights.shape != plan.row_of.shape:
+            raise ValueError(f"weights are {tuple(weights.shape)}; the plan is of "
+                             f"{tuple(plan.row_of.shape)}")
+    return n, top_k, plan.entry_of.numel()
+
+
+def _rows(t: torch.Tensor, name: str):
+    """Rows of a token or a segment: 2-D, BF16 or FP32. Returns the dtype code."""
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    _require(t, t.dtype, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    return OUT_BF16 if t.dtype == torch.bfloat16 else OUT_FP32
+
+
+def _optional(t):
+    return None if t is None else t.data_ptr()
+
+
+def dispatch(x: torch.Tensor, plan: RoutePlan, weights: Optional[torch.Tensor] = None, out=None,
+             stream=None) -> torch.Tensor:
+    """The tokens' rows x (BF16 or FP32 [tokens, cols]) in the plan's segments, [rows, cols]: row
+    r holds its entry's token, times that entry's weight (float32 [tokens, top_k]) if given;
+    padding rows are zero. The gradient of x without weights is combine(grad, plan)."""
+    dt = _rows(x, "x")
+    tokens, top_k, rows = _plan(plan, weights, x.shape[0])
+    cols = x.shape[1]
+    if out is None:
+        out = _new((rows, cols), x.dtype, x.device, stream)
+    else:
+        _buffer(out, x.dtype, rows * cols, "out")
+    _check(lib().mxfp8_dispatch(_ptr(x), dt, tokens, cols, top_k, _optional(weights),
+                                _ptr(plan.row_of), _ptr(plan.entry_of), rows, _ptr(out),
+                                _stream(stream)), "mxfp8_dispatch")
+    return out
+
+
+def _quantize_dispatch(x, plan, weights, row, col, stream):
+    """Both copies' buffers; `row` and `col` are (codes, scales) with None to be allocated, or
+    None for a copy that is not made."""
+    _require(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must have two dimensions, got {x.dim()}")
+    tokens, top_k, rows = _plan(plan, weights, x.shape[0])
+    _require(plan.offsets, torch.int32, "plan.offsets")
+    cols, e = x.shape[1], plan.offsets.numel() - 1
+    got = []
+    for axis, pair, name in ((ROW, row, "row"), (COL, col, "col")):
+        if pair is None:
+            got += [None, None]
+            continue
+        codes, scales = pair
+        need = grouped_scale_bytes(rows, cols, e, axis)
+        if codes is None:
+            codes = _new((rows, cols) if axis == ROW else (cols, rows), torch.uint8, x.device,
+                         stream)
+        else:
+            _buffer(codes, torch.uint8, rows * cols, f"{name} codes")
+        if scales is None:
+            scales = _new((need,), torch.uint8, x.device, stream)
+        else:
+            _buffer(scales, torch.uint8, need, f"{name} scales")
+        got += [codes, scales]
+    if rows and cols:
+        _check(lib().mxfp8_quantize_dispatch(_ptr(x), tokens, cols, top_k, _optional(weights),
+                                             _ptr(plan.entry_of), rows, _ptr(plan.offsets), e,
+                                             *(_optional(t) for t in got), _stream(stream)),
+               "mxfp8_quantize_dispatch")
+    return got
+
+
+def quantize_dispatch(x: torch.Tensor, plan: RoutePlan, axis: int = ROW,
+                      weights: Optional[torch.Tensor] = None, out=None, scales=None, stream=None):
+    """quantize_grouped(dispatch(x, plan, weights), plan.offsets, axis) in one pass, byte for
+    byte (x BF16 [tokens, cols]). Returns (codes, scales); scale bytes past the last segment's
+    are zero."""
+    if axis not in (ROW, COL):
+        raise ValueError(f"axis must be ROW or COL, got {axis}")
+    got = _quantize_dispatch(x, plan, weights, (out, scales) if axis == ROW else None,
+                             (out, scales) if axis == COL else None, stream)
+    return tuple(got[:2] if axis == ROW else got[2:])
+
+
+def quantize_dispatch_dual(x: torch.Tensor, plan: RoutePlan,
+                           weights: Optional[torch.Tensor] = None, row_out=None, row_scales=None,
+                           col_out=None, col_scales=None, stream=None):
+    """quantize_dispatch ROW and COL from one read. Returns (row_codes, row_scales, col_codes,
+    col_scales): an expert layer's forward and weight-gradient operands; with x the gradient of
+    combine's result and its weights, the operands of the layer before it."""
+    return tuple(_quantize_dispatch(x, plan, weights, (row_out, row_scales),
+                                    (col_out, col_scales), stream))
+
+
+def combine(y: torch.Tensor, plan: RoutePlan, weights: Optional[torch.Tensor] = None, out=None,
+            stream=None) -> torch.Tensor:
+    """The sum of each token's segment rows y (BF16 or FP32 [rows, cols]), weighted (float32
+    [tokens, top_k]) if weights are given, [tokens, cols] of y's type: FP32 sums in the order of
+    the choices, rounded once. A token without rows gets zeros."""
+    dt = _rows(y, "y")
+    tokens, top_k, rows = _plan(plan, weights)
+    if y.shape[0] != rows:
+        raise ValueError(f"y has {y.shape[0]} rows; the plan has {rows}")
+    cols = y.shape[1]
+    if out is None:
+        out = _new((tokens, cols), y.dtype, y.device, stream)
+    else:
+        _buffer(out, y.dtype, tokens * cols, "out")
+    _check(lib().mxfp8_combine(_ptr(y), dt, rows, cols, tokens, top_k, _optional(weights),
+                               _ptr(plan.row_of), _ptr(out), _stream(stream)), "mxfp8_combine")
+    return out
+
+
+def combine_backward(grad_out: torch.Tensor, y: torch.Tensor, plan: RoutePlan,
+                     weights: torch.Tensor, grad_rows: bool = True, out=None, out_weights=None,
+                     stream=None):
+    """Gradients of combine(y, plan, weights): (grad_y [rows, cols] of y's type, padding rows
+    zero; grad_weights float32 [tokens, top_k]). grad_rows=False leaves the first out (None):
+    quantize_dispatch_dual(grad_out, plan, weights) gives it as the grouped GEMMs read it."""
+    dt = _rows(y, "y")
+    _require(grad_out, y.dtype, "grad_out")
+    if weights is None:
+        raise ValueError("weights are needed; without them grad_y is dispatch(grad_out, plan)")
+    tokens, top_k, rows = _plan(plan, weights)
+    cols = y.shape[1]
+    if y.shape[0] != rows:
+        raise ValueError(f"y has {y.shape[0]} rows; the plan has {rows}")
+    if tuple(grad_out.shape) != (tokens, cols):
+        raise ValueError(f"grad_out must be {(tokens, cols)}, got {tuple(grad_out.shape)}")
+    if not grad_rows:
+        if out is not None:
+            raise ValueError("out is given, but grad_rows is False")
+    elif out is None:
+        out = _new((rows, cols), y.dtype, y.device, stream)
+    else:
+        _buffer(out, y.dtype, rows * cols, "out")
+    if out_weights is None:
+        out_weights = _new((tokens, top_k), torch.float32, y.device, stream)
+    else:
+        _buffer(out_weights, torch.float32, tokens * top_k, "out_weights")
+    _check(lib().mxfp8_combine_backward(_ptr(grad_out), _ptr(y), dt, tokens, cols, top_k,
+                                        _ptr(weights), _ptr(plan.row_of), _ptr(plan.entry_of),
+                                        rows, _optional(out), _ptr(out_weights),
+                                        _stream(stream)), "mxfp8_combine_backward")
+    return out, out_weights
+
+
+# ------------------------------------------------------- gated activation, 8-bit checkpoint
+
+class Swiglu(NamedTuple):
+    """Result of swiglu."""
+    h: torch.Tensor                 # BF16 [rows, width]
+    codes: Optional[torch.Tensor]   # E4M3 as uint8 [rows, 2 * width], or None
+    scales: Optional[torch.Tensor]  # E8M0 bytes [rows, 2 * width / 32], or None
+
+
+def swiglu(gate_up: torch.Tensor, checkpoint: bool = True, rule: int = RULE_CEIL, out=None,
+           codes=None, scales=None, stream=None) -> Swiglu:
+    """h = silu(gate) * up of a BF16 [rows, 2 * width] tensor [gate | up] (width % 32 == 0), with
+    gate_up kept in MXFP8 for swiglu_backward: quantize(gate_up, ROW, LINEAR, rule=rule) byte for
+    byte, from the same read. checkpoint=False keeps nothing."""
+    _require(gate_up, torch.bfloat16, "gate_up")
+    if gate_up.dim() != 2 or gate_up.shape[1] % 64:
+        raise ValueError(f"gate_up must be [rows, 2 * width], width a multiple of 32, got "
+                         f"{tuple(gate_up.shape)}")
+    rows, width = gate_up.shape[0], gate_up.shape[1] // 2
+    dev = gate_up.device
+    if out is None:
+        out = _new((rows, width), torch.bfloat16, dev, stream)
+    else:
+        _buffer(out, torch.bfloat16, rows * width, "out")
+    if checkpoint:
+        if codes is None:
+            codes = _new((rows, 2 * width), torch.uint8, dev, stream)
+        else:
+            _buffer(codes, torch.uint8, 2 * rows * width, "codes")
+        if scales is None:
+            scales = _new((rows, width // 16), torch.uint8, dev, stream)
+        else:
+            _buffer(scales, torch.uint8, rows * (width // 16), "scales")
+    elif codes is not None or scales is not None:
+        raise ValueError("codes or scales are given, but checkpoint is False")
+    if rows and width:
+        _check(lib().mxfp8_swiglu(_ptr(gate_up), rows, width, _ptr(out), _optional(codes),
+                                  _optional(scales), rule, _stream(stream)), "mxfp8_swiglu")
+    return Swiglu(out, codes, scales)
+
+
+def swiglu_backward(grad_h: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                    recompute: bool = False, out=None, out_h=None, stream=None):
+    """Gradient of swiglu with respect to gate_up, from the gradient of h (BF16 [rows, width])
+    and what swiglu kept. Returns (BF16 [rows, 2 * width], h or None): with recompute=True h of
+    the kept values comes too, BF16 [rows, width], for the next layer's weight gradient (out_h
+    may be grad_h itself)."""
+    _require(grad_h, torch.bfloat16, "grad_h")
+    if grad_h.dim() != 2 or grad_h.shape[1] % 32:
+        raise ValueError(f"grad_h must be [rows, width], width a multiple of 32, got "
+                         f"{tuple(grad_h.shape)}")
+    rows, width = grad_h.shape
+    _buffer(codes, torch.uint8, 2 * rows * width, "codes")
+    _buffer(scales, torch.uint8, rows * (width // 16), "scales")
+    if out is None:
+        out = _new((rows, 2 * width), torch.bfloat16, grad_h.device, stream)
+    else:
+        _buffer(out, torch.bfloat16, 2 * rows * width, "out")
+    if not recompute:
+        if out_h is not None:
+            raise ValueError("out_h is given, but recompute is False")
+    elif out_h is None:
+        out_h = _new((rows, width), torch.bfloat16, grad_h.device, stream)
+    else:
+        _buffer(out_h, torch.bfloat16, rows * width, "out_h")
+    _check(lib().mxfp8_swiglu_backward(_ptr(grad_h), _ptr(codes), _ptr(scales), rows, width,
+                                       _ptr(out), _optional(out_h), _stream(stream)),
+           "mxfp8_swiglu_backward")
+    return out, out_h
 
 
 SELF_CHECK_TOLERANCE = 0.25  # section "Correctness: how it fails": the self-check's tolerance

@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp8.so")
 SOURCES = ("api.cu", "quantize.cu", "gemm.cu", "blockwise_gemm.cu",
-           "logprob.cu", "selfcheck.cu")
+           "logprob.cu", "routing.cu", "swiglu.cu", "selfcheck.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -140,6 +140,7 @@ const char* mxfp8_status_string(int status) {
     case MXFP8_ERR_CUDA: return "CUDA call failed";
     case MXFP8_ERR_BAD_OFFSETS: return "expert offsets invalid (must be 0-based, non-decreasing, 32-aligned, end at total_rows)";
     case MXFP8_ERR_BAD_TARGET: return "a target or alternative token is at or past the vocabulary";
+    case MXFP8_ERR_BAD_EXPERT: return "an expert id is at or past the number of experts";
     case MXFP8_ERR_TIMEOUT: return "a kernel pipeline wait timed out; its work was abandoned";
     default: return "unknown status";
   }
@@ -665,6 +666,247 @@ int mxfp8_token_logprobs_backward(const void* logits_dev, int logits_dtype, int6
   const cudaError_t e = launch_logprob_grad(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXFP8_OK
                           : e == cudaErrorInvalidValue ? MXFP8_ERR_INVALID_ARG : MXFP8_ERR_CUDA;
+}
+
+constexpr int64_t kMaxRouted = 0x7FFFFF00;  // entries, and rows of all segments together
+
+int64_t mxfp8_route_rows(int64_t tokens, int top_k, int num_experts) {
+  int64_t n = 0;
+  if (tokens < 0 || top_k < 1 || num_experts < 1 || num_experts > 1024) return 0;
+  if (!mul3(tokens, top_k, 1, &n) || n > kMaxRouted) return 0;
+  const int64_t rows = (n + 31 * (n < num_experts ? n : num_experts)) / 32 * 32;
+  return rows <= kMaxRouted ? rows : 0;
+}
+
+// Checks that the calls on a plan share; *entries gets tokens * top_k.
+static int plan_checks(int64_t tokens, int top_k, int64_t rows, int64_t* entries) {
+  if (tokens < 0 || top_k < 1 || rows < 0 || rows > kMaxRouted) return MXFP8_ERR_INVALID_ARG;
+  if (!mul3(tokens, top_k, 1, entries) || *entries > kMaxRouted) return MXFP8_ERR_INVALID_ARG;
+  return rows % 32 ? MXFP8_ERR_ALIGNMENT : MXFP8_OK;
+}
+
+int mxfp8_route(const int64_t* ids_dev, int64_t tokens, int top_k, int num_experts,
+                int64_t total_rows, int32_t* offsets_dev, int32_t* row_of_dev,
+                int32_t* entry_of_dev, void* stream) {
+  int64_t n = 0;
+  int st = plan_checks(tokens, top_k, total_rows, &n);
+  if (st != MXFP8_OK) return st;
+  if (num_experts < 1 || num_experts > 1024) return MXFP8_ERR_INVALID_ARG;
+  if (!offsets_dev || (n && (!ids_dev || !row_of_dev)) || (total_rows && !entry_of_dev))
+    return MXFP8_ERR_INVALID_ARG;
+  if (!aligned8(ids_dev) || !aligned4(offsets_dev) || !aligned4(row_of_dev) ||
+      !aligned4(entry_of_dev))
+    return MXFP8_ERR_ALIGNMENT;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  const RouteArgs a{ids_dev, n, num_experts, total_rows, offsets_dev, row_of_dev, entry_of_dev,
+                    d->status};
+  return launch_route(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MXFP8_OK
+                                                                           : MXFP8_ERR_CUDA;
+}
+
+// Checks of the calls that move rows: sizes in FP32 bytes must fit in int64.
+static int rows_checks(int dtype, int64_t tokens, int64_t cols, int top_k, int64_t rows) {
+  int64_t n = 0, bytes = 0;
+  if (dtype != MXFP8_OUT_BF16 && dtype != MXFP8_OUT_FP32) return MXFP8_ERR_INVALID_ARG;
+  // 65535 pieces of 32 columns, the smallest that a launch takes
+  if (cols < 0 || cols > int64_t{65535} * 32) return MXFP8_ERR_INVALID_ARG;
+  const int st = plan_checks(tokens, top_k, rows, &n);
+  if (st != MXFP8_OK) return st;
+  if (!mul3(tokens, cols, 4, &bytes) || !mul3(rows, cols, 4, &bytes)) return MXFP8_ERR_INVALID_ARG;
+  return MXFP8_OK;
+}
+
+int mxfp8_dispatch(const void* x_dev, int dtype, int64_t tokens, int64_t cols, int top_k,
+                   const float* weights_dev, const int32_t* row_of_dev,
+                   const int32_t* entry_of_dev, int64_t total_rows, void* out_dev,
+                   void* stream) {
+  int st = rows_checks(dtype, tokens, cols, top_k, total_rows);
+  if (st != MXFP8_OK) return st;
+  if (total_rows == 0 || cols == 0) return MXFP8_OK;
+  if (!entry_of_dev || !out_dev || (tokens && (!x_dev || !row_of_dev)))
+    return MXFP8_ERR_INVALID_ARG;
+  if (!aligned16(x_dev) || !aligned16(out_dev) || !aligned4(weights_dev) ||
+      !aligned4(row_of_dev) || !aligned4(entry_of_dev))
+    return MXFP8_ERR_ALIGNMENT;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  RowsArgs a{};
+  a.src = x_dev;
+  a.weights = weights_dev;
+  a.row_of = row_of_dev;
+  a.entry_of = entry_of_dev;
+  a.tokens = tokens;
+  a.cols = cols;
+  a.rows = total_rows;
+  a.k = top_k;
+  a.fp32 = dtype == MXFP8_OUT_FP32;
+  a.out = out_dev;
+  a.status = d->status;
+  return launch_dispatch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MXFP8_OK
+                                                                              : MXFP8_ERR_CUDA;
+}
+
+int mxfp8_quantize_dispatch(const void* x_dev, int64_t tokens, int64_t cols, int top_k,
+                            const float* weights_dev, const int32_t* entry_of_dev,
+                            int64_t total_rows, const int32_t* offsets_dev, int num_experts,
+                            void* row_out_dev, void* row_scales_dev, void* col_out_dev,
+                            void* col_scales_dev, void* stream) {
+  const bool row = row_out_dev || row_scales_dev, col = col_out_dev || col_scales_dev;
+  int64_t n = 0, elems = 0;
+  int st = plan_checks(tokens, top_k, total_rows, &n);
+  if (st != MXFP8_OK) return st;
+  if (num_experts < 1 || num_experts > 1024 || cols < 0) return MXFP8_ERR_INVALID_ARG;
+  if (cols % (row ? 32 : 8)) return MXFP8_ERR_ALIGNMENT;
+  if (total_rows == 0 || cols == 0) return MXFP8_OK;
+  if (!mul3(tokens, cols, 4, &elems) || !mul3(total_rows, cols, 4, &elems))
+    return MXFP8_ERR_INVALID_ARG;
+  if ((!row && !col) || (row && (!row_out_dev || !row_scales_dev)) ||
+      (col && (!col_out_dev || !col_scales_dev)) || !entry_of_dev || !offsets_dev ||
+      (tokens && !x_dev))
+    return MXFP8_ERR_INVALID_ARG;
+  if (!aligned16(x_dev) || !aligned16(row_out_dev) || !aligned16(row_scales_dev) ||
+      !aligned16(col_out_dev) || !aligned16(col_scales_dev) || !aligned4(weights_dev) ||
+      !aligned4(entry_of_dev) || !aligned4(offsets_dev))
+    return MXFP8_ERR_ALIGNMENT;
+  if (cdiv(total_rows, 128) + num_experts > kMaxTokenTiles || cdiv(cols, 128) > 0x7FFFFFFF)
+    return MXFP8_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  const QuantizeDispatchArgs a{x_dev, tokens, top_k, weights_dev, entry_of_dev, offsets_dev,
+                               num_experts, total_rows, cols, row_out_dev, row_scales_dev,
+                               col_out_dev, col_scales_dev, d->status};
+  return launch_quantize_dispatch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MXFP8_OK
+             : MXFP8_ERR_CUDA;
+}
+
+int mxfp8_combine(const void* y_dev, int dtype, int64_t total_rows, int64_t cols, int64_t tokens,
+                  int top_k, const float* weights_dev, const int32_t* row_of_dev, void* out_dev,
+                  void* stream) {
+  int st = rows_checks(dtype, tokens, cols, top_k, total_rows);
+  if (st != MXFP8_OK) return st;
+  if (tokens == 0 || cols == 0) return MXFP8_OK;
+  if (!row_of_dev || !out_dev || (total_rows && !y_dev)) return MXFP8_ERR_INVALID_ARG;
+  if (!aligned16(y_dev) || !aligned16(out_dev) || !aligned4(weights_dev) || !aligned4(row_of_dev))
+    return MXFP8_ERR_ALIGNMENT;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  RowsArgs a{};
+  a.src = y_dev;
+  a.weights = weights_dev;
+  a.row_of = row_of_dev;
+  a.tokens = tokens;
+  a.cols = cols;
+  a.rows = total_rows;
+  a.k = top_k;
+  a.fp32 = dtype == MXFP8_OUT_FP32;
+  a.out = out_dev;
+  a.status = d->status;
+  return launch_combine(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MXFP8_OK
+                                                                             : MXFP8_ERR_CUDA;
+}
+
+int mxfp8_combine_backward(const void* grad_out_dev, const void* y_dev, int dtype,
+                           int64_t tokens, int64_t cols, int top_k, const float* weights_dev,
+                           const int32_t* row_of_dev, const int32_t* entry_of_dev,
+                           int64_t total_rows, void* grad_y_dev, float* grad_weights_dev,
+                           void* stream) {
+  int st = rows_checks(dtype, tokens, cols, top_k, total_rows);
+  if (st != MXFP8_OK) return st;
+  const bool rows_out = grad_y_dev && total_rows && cols;   // something to write there
+  if (tokens == 0 && !rows_out) return MXFP8_OK;
+  if (tokens && (!weights_dev || !row_of_dev || !grad_weights_dev ||
+                 (cols && (!grad_out_dev || (total_rows && !y_dev)))))
+    return MXFP8_ERR_INVALID_ARG;
+  if (rows_out && !entry_of_dev) return MXFP8_ERR_INVALID_ARG;
+  if (!aligned16(grad_out_dev) || !aligned16(y_dev) || !aligned16(grad_y_dev) ||
+      !aligned4(weights_dev) || !aligned4(row_of_dev) || !aligned4(entry_of_dev) ||
+      !aligned4(grad_weights_dev))
+    return MXFP8_ERR_ALIGNMENT;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  RowsArgs a{};
+  a.src = grad_out_dev;
+  a.y = y_dev;
+  a.weights = weights_dev;
+  a.row_of = row_of_dev;
+  a.entry_of = entry_of_dev;
+  a.tokens = tokens;
+  a.cols = cols;
+  a.rows = total_rows;
+  a.k = top_k;
+  a.fp32 = dtype == MXFP8_OUT_FP32;
+  a.out = rows_out ? grad_y_dev : nullptr;
+  a.grad_w = grad_weights_dev;
+  a.status = d->status;
+  return launch_combine_grad(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MXFP8_OK
+             : MXFP8_ERR_CUDA;
+}
+
+// Sizes of the gated activation: bytes of [rows][2 width] BF16 fit in int64.
+static int swiglu_checks(int64_t rows, int64_t width) {
+  int64_t bytes = 0;
+  if (rows < 0 || width < 0 || width > kMaxRouted / 2) return MXFP8_ERR_INVALID_ARG;
+  if (!mul3(rows, width, 4, &bytes)) return MXFP8_ERR_INVALID_ARG;
+  if (width % 32) return MXFP8_ERR_ALIGNMENT;
+  // 2^31 - 1 CTAs of 256 threads, 16 values each
+  return rows * (width / 16) > int64_t{0x7FFFFFFF} * 256 ? MXFP8_ERR_INVALID_ARG : MXFP8_OK;
+}
+
+int mxfp8_swiglu(const void* x_dev, int64_t rows, int64_t width, void* h_dev, void* codes_dev,
+                 void* scales_dev, int scale_rule, void* stream) {
+  int st = swiglu_checks(rows, width);
+  if (st != MXFP8_OK) return st;
+  if (scale_rule != MXFP8_RULE_FLOOR && scale_rule != MXFP8_RULE_CEIL)
+    return MXFP8_ERR_INVALID_ARG;
+  if (rows == 0 || width == 0) return MXFP8_OK;
+  if (!x_dev || !h_dev || !codes_dev != !scales_dev) return MXFP8_ERR_INVALID_ARG;
+  if (!aligned16(x_dev) || !aligned16(h_dev) || !aligned16(codes_dev)) return MXFP8_ERR_ALIGNMENT;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  SwigluArgs a{};
+  a.x = x_dev;
+  a.rows = rows;
+  a.width = width;
+  a.rule = scale_rule;
+  a.codes = codes_dev;
+  a.scales = scales_dev;
+  a.h = h_dev;
+  return launch_swiglu(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MXFP8_OK
+                                                                            : MXFP8_ERR_CUDA;
+}
+
+int mxfp8_swiglu_backward(const void* grad_h_dev, const void* codes_dev, const void* scales_dev,
+                          int64_t rows, int64_t width, void* grad_x_dev, void* h_dev,
+                          void* stream) {
+  int st = swiglu_checks(rows, width);
+  if (st != MXFP8_OK) return st;
+  if (rows == 0 || width == 0) return MXFP8_OK;
+  if (!grad_h_dev || !codes_dev || !scales_dev || !grad_x_dev) return MXFP8_ERR_INVALID_ARG;
+  if (!aligned16(grad_h_dev) || !aligned16(codes_dev) || !aligned16(grad_x_dev) ||
+      !aligned16(h_dev))
+    return MXFP8_ERR_ALIGNMENT;
+  DeviceState* d = nullptr;
+  st = device_state(&d);
+  if (st != MXFP8_OK) return st;
+  SwigluArgs a{};
+  a.grad = grad_h_dev;
+  a.rows = rows;
+  a.width = width;
+  a.codes = const_cast<void*>(codes_dev);
+  a.scales = const_cast<void*>(scales_dev);
+  a.h = h_dev;
+  a.grad_x = grad_x_dev;
+  return launch_swiglu_grad(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MXFP8_OK
+                                                                                 : MXFP8_ERR_CUDA;
 }
 
 int mxfp8_set_wait_limit_ns(uint64_t ns) {

@@ -194,6 +194,74 @@ struct LogprobGradArgs {
 cudaError_t launch_logprob(const LogprobArgs& a, cudaStream_t stream);
 cudaError_t launch_logprob_grad(const LogprobGradArgs& a, cudaStream_t stream);
 
+// Entries (token, choice) sorted by expert.
+struct RouteArgs {
+  const int64_t* ids;     // [entries]
+  int64_t entries;        // tokens * top_k
+  int num_experts;
+  int64_t rows;           // of all segments together
+  int32_t* offsets;       // [num_experts + 1]
+  int32_t* row_of;        // [entries]
+  int32_t* entry_of;      // [rows]
+  int* status;
+};
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
+
+// Rows of tokens to and from the experts' segments (BF16, or FP32 with fp32 set).
+struct RowsArgs {
+  const void* src;          // dispatch: x [tokens][cols]; combine: y [rows][cols]; gradient: dout
+  const void* y;            // gradient: y [rows][cols]
+  const float* weights;     // [tokens][k], or nullptr for 1
+  const int32_t* row_of;    // [tokens][k]
+  const int32_t* entry_of;  // [rows]
+  int64_t tokens, cols, rows;
+  int k;
+  bool fp32;
+  void* out;                // [rows][cols], combine: [tokens][cols]; gradient: may be nullptr
+  float* grad_w;            // gradient: [tokens][k]
+  int* status;
+};
+
+cudaError_t launch_dispatch(const RowsArgs& a, cudaStream_t stream);
+cudaError_t launch_combine(const RowsArgs& a, cudaStream_t stream);
+cudaError_t launch_combine_grad(const RowsArgs& a, cudaStream_t stream);
+
+// Grouped MXFP8 operands from the tokens' rows; a null row_out / col_out leaves that copy out.
+struct QuantizeDispatchArgs {
+  const void* src;          // BF16 [tokens][cols]
+  int64_t tokens;
+  int top_k;
+  const float* weights;     // [tokens][top_k], or nullptr
+  const int32_t* entry_of;  // [rows]
+  const int32_t* offsets;   // [num_experts + 1]
+  int num_experts;
+  int64_t rows, cols;
+  void* row_out;
+  void* row_scales;
+  void* col_out;
+  void* col_scales;
+  int* status;
+};
+
+cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t stream);
+
+// h = silu(gate) * up of gate_up [rows][2 width], with gate_up kept as row-wise MXFP8 (codes
+// null: not kept), and the gradient from that copy.
+struct SwigluArgs {
+  const void* x;         // forward: BF16 [rows][2 width]
+  const void* grad;      // backward: BF16 [rows][width]
+  int64_t rows, width;
+  int rule;
+  void* codes;           // E4M3 [rows][2 width]
+  void* scales;          // [rows][2 width / 32]
+  void* h;               // BF16 [rows][width]; backward: may be nullptr
+  void* grad_x;          // backward: BF16 [rows][2 width]
+};
+
+cudaError_t launch_swiglu(const SwigluArgs& a, cudaStream_t stream);
+cudaError_t launch_swiglu_grad(const SwigluArgs& a, cudaStream_t stream);
+
 int num_sms();  // of the current device (cached)
 
 // Pipeline wait limit of the GEMM kernels for later launches (0: the default).

@@ -31,6 +31,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "convert.cuh"
 #include "device.cuh"
 #include "internal.h"
 #include "mxfp8.h"
@@ -113,26 +114,6 @@ __device__ int find_expert(const Segments& s, int E, int t) {
   return lo;
 }
 
-constexpr uint32_t kAbs2 = 0x7FFF7FFFu;  // clears both BF16 sign bits of a word
-
-// Per-half maximum of |a| and |b| for two BF16 pairs, NaN winning over every number; the
-// sign bits of the result are meaningless (cleared by kAbs2 once per block). Compared with
-// clearing both signs and taking an unsigned 16-bit maximum this is one instruction instead
-// of three. A BF16 subnormal amax gives scale byte 0 whether or not it is flushed here.
-__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// Per-half unsigned 16-bit maximum of two words: on sign-cleared BF16 bits, the exact
-// maximum magnitude, subnormals included (the block-wise FP32 scale depends on it).
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // 16 bytes global -> shared, bypassing L1; `valid` false writes 16 zero bytes instead.
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -141,90 +122,6 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool vali
 
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-
-
-// Scale byte from the largest |BF16| bits of a block; 0xFF for a NaN/Inf block.
-// Floor rule (OCP): floor(log2 amax) - 8 = biased exponent - 135, byte = E - 8.
-// Round-up rule: one more when the mantissa of amax exceeds 1.75 (amax > 448 * 2^e), so
-// that nothing saturates. Both clamp at byte 0 (e = -127).
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits, int rule) {
-  if (amax_bits >= 0x7F80u) return 0xFFu;
-  int e = static_cast<int>(amax_bits >> 7) - 8;
-  if (rule == MXFP8_RULE_CEIL) e += (amax_bits & 0x7Fu) > 0x60u;
-  return e > 0 ? static_cast<uint32_t>(e) : 0u;
-}
-
-// 2^-e for scale byte s = e + 127, as an FP32 (a normal number for s <= 253; the 0xFF of a
-// NaN/Inf block gives -Inf, whose products are discarded).
-__device__ __forceinline__ float inv_scale(uint32_t s) {
-  return __uint_as_float((254u - s) << 23);
-}
-
-// Two elements given as FP32 bit patterns (lo first in memory order) -> 2 bytes: each
-// scaled by an IEEE single-precision product rounded to nearest (exact for a power-of-two
-// scale), then one RNE-saturating E4M3 conversion of the pair. Two scalar products measured
-// slightly faster than one packed mul.rn.f32x2 (whose operands must sit in a register pair).
-__device__ __forceinline__ uint32_t e4m3x2_f32bits(uint32_t lo, uint32_t hi, float mul) {
-  const float a = __fmul_rn(__uint_as_float(lo), mul);
-  const float b = __fmul_rn(__uint_as_float(hi), mul);
-  uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(b), "f"(a));
-  return c;
-}
-
-// Two BF16 pairs (4 elements, memory order lo(w0), hi(w0), lo(w1), hi(w1)) -> 4 bytes.
-// A BF16 value's FP32 bit pattern is its 16 bits shifted to the top half.
-__device__ __forceinline__ uint32_t e4m3x4(uint32_t w0, uint32_t w1, float mul) {
-  return e4m3x2_f32bits(w0 << 16, w0 & 0xFFFF0000u, mul) |
-         (e4m3x2_f32bits(w1 << 16, w1 & 0xFFFF0000u, mul) << 16);
-}
-
-// The MXFP8 kernels scale by an exact power of two, so they can scale two BF16 values with
-// one packed BF16 product (exact: the results lie in [2^-133, 2^9) or are far below E4M3's
-// smallest subnormal, and BF16 keeps subnormals) before widening them for the conversion.
-// The block-wise kernel's FP32 scale is not a power of two: it keeps the FP32 products.
-
-// BF16 bits of 2^-e for scale byte s = e + 127 (a normal number for s <= 253; the 0xFF of a
-// NaN/Inf block gives +Inf, whose products are discarded).
-__device__ __forceinline__ uint32_t inv_scale_bf16(uint32_t s) { return ((254u - s) & 0xFFu) << 7; }
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// Two values given as FP32 bit patterns (lo first in memory order) -> 2 bytes, one
-// RNE-saturating E4M3 conversion of the pair.
-__device__ __forceinline__ uint32_t e4m3x2_of(uint32_t lo, uint32_t hi) {
-  uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-      : "=h"(c) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
-  return c;
-}
-
-// Two BF16 pairs (4 elements, memory order lo(w0), hi(w0), lo(w1), hi(w1)) scaled by the
-// BF16 pair mul2 (2^-e in both halves) -> 4 bytes.
-__device__ __forceinline__ uint32_t e4m3x4_pow2(uint32_t w0, uint32_t w1, uint32_t mul2) {
-  const uint32_t v0 = mul_bf16x2(w0, mul2), v1 = mul_bf16x2(w1, mul2);
-  return e4m3x2_of(v0 << 16, v0 & 0xFFFF0000u) | (e4m3x2_of(v1 << 16, v1 & 0xFFFF0000u) << 16);
-}
-
-// 32 bytes global store in one instruction (the address must be 32-byte aligned).
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&o)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-               ::"l"(p), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]),
-                 "r"(o[6]), "r"(o[7]) : "memory");
-}
-
-// The same 4 elements of a NaN/Inf block: 0x7F with each element's own sign. Blocks like
-// this take a separate branch after the normal conversion, which stays free of selects.
-__device__ __forceinline__ uint32_t nan4(uint32_t w0, uint32_t w1) {
-  const uint32_t s0 = (w0 >> 8) & 0x80u, s1 = (w0 >> 24) & 0x80u;
-  const uint32_t s2 = (w1 >> 8) & 0x80u, s3 = (w1 >> 24) & 0x80u;
-  return (0x7Fu | s0) | ((0x7Fu | s1) << 8) | ((0x7Fu | s2) << 16) | ((0x7Fu | s3) << 24);
 }
 
 // One CTA = one 128 x 128 BF16 tile (128 token rows x 128 columns). kRow: write the
@@ -549,6 +446,114 @@ quantize_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t col
   }
 }
 
+// The MXFP8 operands of the experts' GEMMs straight from the tokens' rows: segment row r holds
+// token entry_of[r] / top_k's row, times that entry's weight if there are weights (an FP32 product,
+// rounded to BF16), or zeros where there is no entry. The bytes are those of the grouped
+// quantizer on the dispatched BF16 rows, which are never written: per element that saves a
+// write and a read of 2 bytes, and a token's row comes out of L2 for all but its first expert.
+// Scale tiles past the last segment's are zero, so that the whole buffers are defined.
+struct DispatchParams {
+  const uint16_t* src;      // [tokens][cols]
+  const float* weights;     // [tokens][top_k], or nullptr
+  const int32_t* entry_of;  // [rows]
+  int64_t entries;          // tokens * top_k
+  uint32_t top_k;
+  int64_t rows, cols;
+  const int32_t* offsets;
+  int E;
+  int* status;
+};
+
+template <bool kRow, bool kCol, bool kWeighted>
+__global__ void __launch_bounds__(kThreads, 6)
+quantize_dispatch_kernel(const DispatchParams p, QOut ro, QOut co) {
+  __shared__ __align__(16) uint16_t tile[kTile][kTilePitch];
+  __shared__ __align__(16) uint8_t stile_r[512];
+  __shared__ __align__(16) uint8_t stile_c[512];
+  __shared__ int32_t token[kTile];   // of each row of the tile, -1 for none
+  __shared__ float weight[kWeighted ? kTile : 1];
+  extern __shared__ __align__(16) uint8_t dyn[];
+  Segments& seg = *reinterpret_cast<Segments*>(dyn);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  load_segments(seg, p.offsets, p.E, p.rows, p.status);
+  if (!seg.ok) return;
+  const int t = threadIdx.x;
+  const int64_t bx = blockIdx.x;
+  const int tile_row = static_cast<int>(blockIdx.y);
+  const int64_t n_col_tiles = (p.cols + kTile - 1) / kTile;
+  if (tile_row >= seg.tile_base[p.E]) {   // no segment's: the tail of the scale buffers
+    const int64_t at = (tile_row * n_col_tiles + bx) * 512;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    if (kRow && t < 32) reinterpret_cast<uint4*>(ro.scales + at)[t] = none;
+    if (kCol && t >= 32 && t < 64) reinterpret_cast<uint4*>(co.scales + at)[t - 32] = none;
+    return;
+  }
+  const int e = find_expert(seg, p.E, tile_row);
+  const int64_t i = tile_row - seg.tile_base[e];
+  const int64_t cnt = seg.off[e + 1] - seg.off[e];
+  const int64_t row0 = seg.off[e] + i * kTile;
+  const int64_t left = cnt - i * kTile;
+  const int rows_valid = static_cast<int>(left < kTile ? left : kTile);
+  const int64_t row_scale_tile = tile_row * n_col_tiles + bx;
+  const int64_t col_scale_tile =
+      n_col_tiles * seg.tile_base[e] + bx * ((cnt + kTile - 1) / kTile) + i;
+  if (t < kTile) {
+    int32_t entry = t < rows_valid ? p.entry_of[row0 + t] : -1;
+    if (entry >= p.entries) {   // a plan of other sizes
+      latch_error(p.status, MXFP8_ERR_BAD_OFFSETS);
+      entry = -1;
+    }
+    token[t] = entry < 0 ? -1 : static_cast<int32_t>(static_cast<uint32_t>(entry) / p.top_k);
+    if (kWeighted) weight[t] = entry < 0 ? 0.f : p.weights[entry];
+  }
+  __syncthreads();
+
+  const int v = t & 15, rsub = t >> 4;
+  const int64_t col0 = bx * kTile;
+  const int64_t cols_left = p.cols - col0;
+  const int cols_valid = static_cast<int>(cols_left < kTile ? cols_left : kTile);
+  const bool col_ok = 8 * v < cols_valid;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = rsub + 16 * j;
+    const int32_t from = token[r];
+    const bool ok = col_ok && from >= 0;
+    cp_async16(&tile[r][8 * v], ok ? p.src + from * p.cols + col0 + 8 * v : p.src, ok);
+  }
+  cp_async_wait_all();
+  if constexpr (kWeighted) {   // each thread on the vectors that it copied itself
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = rsub + 16 * j;
+      uint4* at = reinterpret_cast<uint4*>(&tile[r][8 * v]);
+      const uint4 x = *at;
+      const float w = weight[r];
+      const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        o[q] = cvt_bf16x2(__fmul_rn(__uint_as_float(in[q] & 0xFFFF0000u), w),
+                          __fmul_rn(__uint_as_float(in[q] << 16), w));
+      *at = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  __syncthreads();
+  if constexpr (kRow)
+    row_pass_smem<true>(tile, stile_r, ro, p.cols, row0, rows_valid, col0, cols_valid,
+                        MXFP8_RULE_FLOOR);
+  if constexpr (kCol)
+    col_pass_smem<true>(tile, stile_c, co, p.rows, row0, rows_valid, col0, cols_valid,
+                        MXFP8_RULE_FLOOR);
+  __syncthreads();
+  if (kRow && t < 32)
+    reinterpret_cast<uint4*>(ro.scales + row_scale_tile * 512)[t] =
+        reinterpret_cast<const uint4*>(stile_r)[t];
+  if (kCol && t >= 32 && t < 64)
+    reinterpret_cast<uint4*>(co.scales + col_scale_tile * 512)[t - 32] =
+        reinterpret_cast<const uint4*>(stile_c)[t - 32];
+}
+
 // Factor s of a block-wise block from its largest |BF16| bits, and 1 / s. The factor is
 // 448 / amax in IEEE single precision (clamped to the largest float on overflow) or the
 // power of two 2^-ceil(log2(amax / 448)); 1 for a zero block; 0 marks a block holding a NaN
@@ -862,6 +867,25 @@ cudaError_t launch_axes(const QuantizeArgs& a, cudaStream_t stream) {
   return launch_tiles<kRow, kCol, false, false>(a, stream);
 }
 
+template <bool kRow, bool kCol>
+cudaError_t launch_dispatch_axes(const QuantizeDispatchArgs& a, cudaStream_t stream) {
+  const int64_t col_tiles = (a.cols + kTile - 1) / kTile;
+  const int64_t row_tiles = (a.rows + kTile - 1) / kTile + a.num_experts;
+  if (row_tiles > 65535 || col_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const DispatchParams p{static_cast<const uint16_t*>(a.src), a.weights, a.entry_of,
+                         a.tokens * a.top_k, static_cast<uint32_t>(a.top_k), a.rows, a.cols,
+                         a.offsets, a.num_experts, a.status};
+  const QOut ro{static_cast<uint8_t*>(a.row_out), static_cast<uint8_t*>(a.row_scales), 0};
+  const QOut co{static_cast<uint8_t*>(a.col_out), static_cast<uint8_t*>(a.col_scales), 0};
+  auto k = a.weights ? quantize_dispatch_kernel<kRow, kCol, true>
+                     : quantize_dispatch_kernel<kRow, kCol, false>;
+  const dim3 grid(static_cast<unsigned>(col_tiles), static_cast<unsigned>(row_tiles));
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(sizeof(Segments)));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, grid, sizeof(Segments), stream, p, ro, co);
+}
+
 }  // namespace
 
 int64_t scale_bytes_host(int64_t rows, int64_t cols, int axis, int layout);
@@ -922,6 +946,13 @@ cudaError_t launch_blockwise_tiles(const BlockwiseArgs& a, cudaStream_t stream) 
   return launch_pdl(k, grid, 0, stream, static_cast<const uint16_t*>(a.src), a.rows, a.cols,
                     static_cast<uint8_t*>(a.row_out), a.row_inv,
                     static_cast<uint8_t*>(a.col_out), a.col_inv, a.pow2 ? 1 : 0);
+}
+
+cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t stream) {
+  if (a.rows == 0 || a.cols == 0) return cudaSuccess;
+  if (a.row_out && a.col_out) return launch_dispatch_axes<true, true>(a, stream);
+  return a.row_out ? launch_dispatch_axes<true, false>(a, stream)
+                   : launch_dispatch_axes<false, true>(a, stream);
 }
 
 cudaError_t launch_quantize(const QuantizeArgs& a, cudaStream_t stream) {
