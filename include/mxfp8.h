@@ -622,11 +622,13 @@ int mxfp8_dispatch(const void* x_dev, int dtype, int64_t tokens, int64_t cols, i
  * Either copy may be left out (both its pointers NULL), not both. Scale buffers hold
  * mxfp8_grouped_scale_bytes(total_rows, cols, num_experts, axis) bytes and are written in full:
  * zeros follow the last block. Invalid offsets latch MXFP8_ERR_BAD_OFFSETS and write nothing.
- * total_rows == 0 or cols == 0 is a no-op.
+ * total_rows == 0 or cols == 0 is a no-op. tokens * cols below 2^35, at most 65535 - num_experts
+ * tiles of 128 rows.
  */
 int mxfp8_quantize_dispatch(const void* x_dev, int64_t tokens, int64_t cols, int top_k,
-                            const float* weights_dev, const int32_t* entry_of_dev,
-                            int64_t total_rows, const int32_t* offsets_dev, int num_experts,
+                            const float* weights_dev, const int32_t* row_of_dev,
+                            const int32_t* entry_of_dev, int64_t total_rows,
+                            const int32_t* offsets_dev, int num_experts,
                             void* row_out_dev, void* row_scales_dev, void* col_out_dev,
                             void* col_scales_dev, void* stream);
 

@@ -60,8 +60,8 @@ SIGNATURES = {
     "mxfp8_route_rows": (_I64, [_I64, _I, _I]),
     "mxfp8_route": (_I, [_P, _I64, _I, _I, _I64, _P, _P, _P, _P]),
     "mxfp8_dispatch": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _P, _I64, _P, _P]),
-    "mxfp8_quantize_dispatch": (_I, [_P, _I64, _I64, _I, _P, _P, _I64, _P, _I, _P, _P, _P, _P,
-                                     _P]),
+    "mxfp8_quantize_dispatch": (_I, [_P, _I64, _I64, _I, _P, _P, _P, _I64, _P, _I, _P, _P, _P,
+                                     _P, _P]),
     "mxfp8_combine": (_I, [_P, _I, _I64, _I64, _I64, _I, _P, _P, _P, _P]),
     "mxfp8_combine_backward": (_I, [_P, _P, _I, _I64, _I64, _I, _P, _P, _P, _I64, _P, _P, _P]),
     "mxfp8_swiglu": (_I, [_P, _I64, _I64, _P, _P, _P, _I, _P]),
@@ -806,7 +806,8 @@ def _quantize_dispatch(x, plan, weights, row, col, stream):
         got += [codes, scales]
     if rows and cols:
         _check(lib().mxfp8_quantize_dispatch(_ptr(x), tokens, cols, top_k, _optional(weights),
-                                             _ptr(plan.entry_of), rows, _ptr(plan.offsets), e,
+                                             _ptr(plan.row_of), _ptr(plan.entry_of), rows,
+                                             _ptr(plan.offsets), e,
                                              *(_optional(t) for t in got), _stream(stream)),
                "mxfp8_quantize_dispatch")
     return got

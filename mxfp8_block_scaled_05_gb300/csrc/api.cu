@@ -750,8 +750,9 @@ int mxfp8_dispatch(const void* x_dev, int dtype, int64_t tokens, int64_t cols, i
 }
 
 int mxfp8_quantize_dispatch(const void* x_dev, int64_t tokens, int64_t cols, int top_k,
-                            const float* weights_dev, const int32_t* entry_of_dev,
-                            int64_t total_rows, const int32_t* offsets_dev, int num_experts,
+                            const float* weights_dev, const int32_t* row_of_dev,
+                            const int32_t* entry_of_dev, int64_t total_rows,
+                            const int32_t* offsets_dev, int num_experts,
                             void* row_out_dev, void* row_scales_dev, void* col_out_dev,
                             void* col_scales_dev, void* stream) {
   const bool row = row_out_dev || row_scales_dev, col = col_out_dev || col_scales_dev;
@@ -761,24 +762,25 @@ int mxfp8_quantize_dispatch(const void* x_dev, int64_t tokens, int64_t cols, int
   if (num_experts < 1 || num_experts > 1024 || cols < 0) return MXFP8_ERR_INVALID_ARG;
   if (cols % (row ? 32 : 8)) return MXFP8_ERR_ALIGNMENT;
   if (total_rows == 0 || cols == 0) return MXFP8_OK;
-  if (!mul3(tokens, cols, 4, &elems) || !mul3(total_rows, cols, 4, &elems))
+  if (!mul3(total_rows, cols, 4, &elems) || !mul3(tokens, cols, 1, &elems))
     return MXFP8_ERR_INVALID_ARG;
+  if (elems >= int64_t{1} << 35) return MXFP8_ERR_INVALID_ARG;   // rows' places in 32 bits
   if ((!row && !col) || (row && (!row_out_dev || !row_scales_dev)) ||
       (col && (!col_out_dev || !col_scales_dev)) || !entry_of_dev || !offsets_dev ||
-      (tokens && !x_dev))
+      (tokens && (!x_dev || !row_of_dev)))
     return MXFP8_ERR_INVALID_ARG;
   if (!aligned16(x_dev) || !aligned16(row_out_dev) || !aligned16(row_scales_dev) ||
       !aligned16(col_out_dev) || !aligned16(col_scales_dev) || !aligned4(weights_dev) ||
-      !aligned4(entry_of_dev) || !aligned4(offsets_dev))
+      !aligned4(row_of_dev) || !aligned4(entry_of_dev) || !aligned4(offsets_dev))
     return MXFP8_ERR_ALIGNMENT;
   if (cdiv(total_rows, 128) + num_experts > kMaxTokenTiles || cdiv(cols, 128) > 0x7FFFFFFF)
     return MXFP8_ERR_INVALID_ARG;
   DeviceState* d = nullptr;
   st = device_state(&d);
   if (st != MXFP8_OK) return st;
-  const QuantizeDispatchArgs a{x_dev, tokens, top_k, weights_dev, entry_of_dev, offsets_dev,
-                               num_experts, total_rows, cols, row_out_dev, row_scales_dev,
-                               col_out_dev, col_scales_dev, d->status};
+  const QuantizeDispatchArgs a{x_dev, tokens, top_k, weights_dev, row_of_dev, entry_of_dev,
+                               offsets_dev, num_experts, total_rows, cols, row_out_dev,
+                               row_scales_dev, col_out_dev, col_scales_dev, d->status};
   return launch_quantize_dispatch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MXFP8_OK
              : MXFP8_ERR_CUDA;

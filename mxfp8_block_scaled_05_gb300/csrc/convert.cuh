@@ -95,6 +95,26 @@ __device__ __forceinline__ uint32_t e4m3x4_pow2(uint32_t w0, uint32_t w1, uint32
   return e4m3x2_of(v0 << 16, v0 & 0xFFFF0000u) | (e4m3x2_of(v1 << 16, v1 & 0xFFFF0000u) << 16);
 }
 
+// A BF16 pair times a pair of powers of two, widened to FP32: one mixed-precision fused
+// multiply-add each, on the FMA pipe, where a packed product and two unpackings take the ALU pipe,
+// which the conversions load already. Exact; -0 is added, so that -0 stays -0.
+__device__ __forceinline__ void scale_bf16x2(uint32_t w, uint32_t mul2, float& lo, float& hi) {
+  asm("{\n\t.reg .b16 a, b, m, n;\n\t"
+      "mov.b32 {a, b}, %2;\n\tmov.b32 {m, n}, %3;\n\t"
+      "fma.rn.f32.bf16 %0, a, m, %4;\n\tfma.rn.f32.bf16 %1, b, n, %4;\n\t}"
+      : "=f"(lo), "=f"(hi) : "r"(w), "r"(mul2), "f"(-0.0f));
+}
+
+// Four FP32 values to 4 E4M3 codes, the first lowest.
+__device__ __forceinline__ uint32_t e4m3x4_f32(float a, float b, float c, float d) {
+  uint32_t o;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(o) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return o;
+}
+
 // 32 bytes global store in one instruction (the address must be 32-byte aligned).
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&o)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"

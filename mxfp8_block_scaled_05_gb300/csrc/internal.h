@@ -233,6 +233,7 @@ struct QuantizeDispatchArgs {
   int64_t tokens;
   int top_k;
   const float* weights;     // [tokens][top_k], or nullptr
+  const int32_t* row_of;    // [tokens][top_k]
   const int32_t* entry_of;  // [rows]
   const int32_t* offsets;   // [num_experts + 1]
   int num_experts;

@@ -35,106 +35,11 @@
 #include "device.cuh"
 #include "internal.h"
 #include "mxfp8.h"
+#include "segments.cuh"
+#include "tile_passes.cuh"
 
 namespace mxfp8 {
 namespace {
-
-constexpr int kTile = 128;        // rows and columns of a CTA tile
-constexpr int kThreads = 256;
-constexpr int kTilePitch = kTile + 8;  // BF16 row pitch of the shared tile: 272 bytes
-constexpr int kMaxExperts = 1024; // grouped calls: experts scanned in shared memory
-
-// Expert segmentation of the token rows for grouped calls. Every CTA re-derives the
-// prefix sums of ceil(count / 128) from the offsets, so that no table has to be kept in
-// global memory; invalid offsets make every CTA return without writing anything.
-struct Segments {
-  int32_t off[kMaxExperts + 1];
-  int32_t tile_base[kMaxExperts + 1];  // prefix sum of ceil(count_e / 128)
-  int32_t warp_sum[kThreads / 32];     // scratch of the block-wide scan
-  int ok;
-};
-
-// The prefix sums come from a block-wide scan: each thread sums the tile counts of
-// kMaxExperts / kThreads consecutive experts, a warp shuffle scan and the warps' totals
-// place each thread's run, and the thread writes its experts' bases. A grouped launch runs
-// this in every CTA, so a serial loop over the experts by one thread would cost each CTA
-// microseconds.
-__device__ void load_segments(Segments& s, const int32_t* __restrict__ offsets, int E,
-                              int64_t total_rows, int* status) {
-  constexpr int kPer = kMaxExperts / kThreads;  // experts per thread
-  static_assert(kPer * kThreads == kMaxExperts, "experts must split evenly over the CTA");
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t == 0) s.ok = 1;
-  __syncthreads();
-  for (int i = t; i <= E; i += kThreads) s.off[i] = offsets[i];
-  __syncthreads();
-  int32_t tiles[kPer];
-  int32_t mine = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = t * kPer + j;
-    int32_t n = 0;
-    if (e < E) {
-      const int32_t lo = s.off[e], hi = s.off[e + 1];
-      if (hi < lo || (lo & 31) || (hi & 31)) s.ok = 0;
-      n = hi > lo ? (hi - lo + 127) / 128 : 0;
-    }
-    tiles[j] = n;
-    mine += n;
-  }
-  if (t == 0 && (s.off[0] != 0 || static_cast<int64_t>(s.off[E]) != total_rows)) s.ok = 0;
-  int32_t incl = mine;  // inclusive scan within the warp
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  if (lane == 31) s.warp_sum[warp] = incl;
-  __syncthreads();
-  int32_t base = incl - mine;
-  for (int w = 0; w < warp; ++w) base += s.warp_sum[w];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = t * kPer + j;
-    if (e < E) s.tile_base[e] = base;
-    base += tiles[j];
-  }
-  if (t == kThreads - 1) s.tile_base[E] = base;  // the total: threads past E add nothing
-  __syncthreads();
-  if (t == 0 && !s.ok) latch_error(status, MXFP8_ERR_BAD_OFFSETS);
-}
-
-// Finds the expert owning global tile-row `t` (tile_base[e] <= t < tile_base[e+1]).
-__device__ int find_expert(const Segments& s, int E, int t) {
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s.tile_base[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
-// 16 bytes global -> shared, bypassing L1; `valid` false writes 16 zero bytes instead.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-               ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16u : 0u) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-// One CTA = one 128 x 128 BF16 tile (128 token rows x 128 columns). kRow: write the
-// row-wise copy (blocks along the columns); kCol: write the column-wise copy (blocks
-// along the rows, emitted transposed). With both, the input is read once, into a shared
-// tile whose rows are padded to 272 bytes: the row-wise pass (one thread per 32-block,
-// eight consecutive rows per eight lanes) and the column-wise pass (one word per row and
-// lane) then read it without bank conflicts.
-struct QOut {
-  uint8_t* codes;
-  uint8_t* scales;
-  int64_t scale_item_bytes;  // bytes of one batch item's scale block
-};
 
 // Jobs of a multi-tensor launch: job j owns the grid's tiles [tile_base[j], tile_base[j+1]).
 struct QJobs {
@@ -148,150 +53,12 @@ struct QJobs {
   int64_t tile_base[kMaxQuantizeJobs + 1];
 };
 
-// Row-wise copy of a 128 x 128 tile staged in shared memory: one thread per 32-block (8
-// consecutive rows per 8 lanes, conflict-free with the padded pitch), 32 code bytes per
-// thread; the scale bytes go to the 512-byte tile stile_r (swizzled) or straight out.
-template <bool kSwizzled>
-__device__ __forceinline__ void row_pass_smem(const uint16_t (*tile)[kTilePitch],
-                                              uint8_t* stile_r, const QOut& ro, int64_t cols,
-                                              int64_t row0, int rows_valid, int64_t col0,
-                                              int cols_valid, int rule) {
-  const int t = threadIdx.x;
-  const int64_t s_cols = cols / 32;
-  const int w = t >> 5, l = t & 31;
-  const int b = l >> 3;
-  const bool block_ok = 32 * b < cols_valid;
-  const bool wide = (reinterpret_cast<uintptr_t>(ro.codes) & 31) == 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = 8 * w + (l & 7) + 64 * i;
-    const uint4* rp = reinterpret_cast<const uint4*>(&tile[r][32 * b]);
-    const uint4 x0 = rp[0], x1 = rp[1], x2 = rp[2], x3 = rp[3];
-    uint32_t m2 = max_abs_bf16x2(
-        max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(x0.x, x0.y), max_abs_bf16x2(x0.z, x0.w)),
-                       max_abs_bf16x2(max_abs_bf16x2(x1.x, x1.y), max_abs_bf16x2(x1.z, x1.w))),
-        max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(x2.x, x2.y), max_abs_bf16x2(x2.z, x2.w)),
-                       max_abs_bf16x2(max_abs_bf16x2(x3.x, x3.y), max_abs_bf16x2(x3.z, x3.w))));
-    m2 &= kAbs2;
-    const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-    const bool valid = block_ok && r < rows_valid;
-    const uint32_t s = scale_byte(m, rule);
-    if (valid) {
-      uint32_t o[8];
-      if (__builtin_expect(s != 0xFFu, 1)) {
-        const uint32_t mul2 = inv_scale_bf16(s) * 0x10001u;
-        o[0] = e4m3x4_pow2(x0.x, x0.y, mul2); o[1] = e4m3x4_pow2(x0.z, x0.w, mul2);
-        o[2] = e4m3x4_pow2(x1.x, x1.y, mul2); o[3] = e4m3x4_pow2(x1.z, x1.w, mul2);
-        o[4] = e4m3x4_pow2(x2.x, x2.y, mul2); o[5] = e4m3x4_pow2(x2.z, x2.w, mul2);
-        o[6] = e4m3x4_pow2(x3.x, x3.y, mul2); o[7] = e4m3x4_pow2(x3.z, x3.w, mul2);
-      } else {
-        o[0] = nan4(x0.x, x0.y); o[1] = nan4(x0.z, x0.w);
-        o[2] = nan4(x1.x, x1.y); o[3] = nan4(x1.z, x1.w);
-        o[4] = nan4(x2.x, x2.y); o[5] = nan4(x2.z, x2.w);
-        o[6] = nan4(x3.x, x3.y); o[7] = nan4(x3.z, x3.w);
-      }
-      uint8_t* dst = ro.codes + (row0 + r) * cols + col0 + 32 * b;
-      if (wide) {
-        st_global_v8(dst, o);
-      } else {
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-    }
-    if (kSwizzled)
-      stile_r[(r & 31) * 16 + (r >> 5) * 4 + b] = valid ? static_cast<uint8_t>(s) : 0;
-    else if (valid)
-      ro.scales[(row0 + r) * s_cols + col0 / 32 + b] = static_cast<uint8_t>(s);
-  }
-}
-
-// Column-wise copy (transpose) of a 128 x 128 tile staged in shared memory; the tile
-// buffer is reused to stage the transposed codes, so it is dead once this returns.
-template <bool kSwizzled>
-__device__ __forceinline__ void col_pass_smem(uint16_t (*tile)[kTilePitch], uint8_t* stile_c,
-                                              const QOut& co, int64_t rows, int64_t row0,
-                                              int rows_valid, int64_t col0, int cols_valid,
-                                              int rule) {
-  const int t = threadIdx.x;
-  // thread = column pair (2cp, 2cp+1) x token block j (32 rows); each word read holds
-  // both columns of one row (column c in the low half)
-  const int w = t >> 5, lane = t & 31;
-  const int cp = (w & 1) * 32 + lane;
-  const int j = w >> 1;
-  const int c = 2 * cp;
-  const bool valid = c < cols_valid && 32 * j < rows_valid;
-  const uint32_t* colw = reinterpret_cast<const uint32_t*>(&tile[32 * j][c]);
-  constexpr int kRowWords = kTilePitch / 2;
-  uint32_t m01 = 0;  // both columns' block maxima, one per half
-#pragma unroll
-  for (int i = 0; i < 32; ++i) m01 = max_abs_bf16x2(m01, colw[i * kRowWords]);
-  m01 &= kAbs2;
-  const uint32_t s0 = scale_byte(m01 & 0xFFFFu, rule), s1 = scale_byte(m01 >> 16, rule);
-  uint4 stage_o0[2], stage_o1[2];
-  if (valid) {
-    uint32_t o0[8], o1[8];
-    if (__builtin_expect(s0 != 0xFFu && s1 != 0xFFu, 1)) {
-      // each row word holds column c (low half) and c + 1 (high half): one packed product
-      // scales both by their own block's 2^-e
-      const uint32_t mulp = inv_scale_bf16(s0) | (inv_scale_bf16(s1) << 16);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const uint32_t b0 = mul_bf16x2(colw[(4 * q) * kRowWords], mulp);
-        const uint32_t b1 = mul_bf16x2(colw[(4 * q + 1) * kRowWords], mulp);
-        const uint32_t b2 = mul_bf16x2(colw[(4 * q + 2) * kRowWords], mulp);
-        const uint32_t b3 = mul_bf16x2(colw[(4 * q + 3) * kRowWords], mulp);
-        o0[q] = e4m3x2_of(b0 << 16, b1 << 16) | (e4m3x2_of(b2 << 16, b3 << 16) << 16);
-        o1[q] = e4m3x2_of(b0 & 0xFFFF0000u, b1 & 0xFFFF0000u) |
-                (e4m3x2_of(b2 & 0xFFFF0000u, b3 & 0xFFFF0000u) << 16);
-      }
-    } else {  // a NaN/Inf block in either column (rare)
-      const float mul0 = inv_scale(s0), mul1 = inv_scale(s1);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const uint32_t a0 = colw[(4 * q) * kRowWords], a1 = colw[(4 * q + 1) * kRowWords];
-        const uint32_t a2 = colw[(4 * q + 2) * kRowWords], a3 = colw[(4 * q + 3) * kRowWords];
-        const uint32_t c0a = __byte_perm(a0, a1, 0x5410), c0b = __byte_perm(a2, a3, 0x5410);
-        const uint32_t c1a = __byte_perm(a0, a1, 0x7632), c1b = __byte_perm(a2, a3, 0x7632);
-        o0[q] = s0 == 0xFFu ? nan4(c0a, c0b) : e4m3x4(c0a, c0b, mul0);
-        o1[q] = s1 == 0xFFu ? nan4(c1a, c1b) : e4m3x4(c1a, c1b, mul1);
-      }
-    }
-    stage_o0[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-    stage_o0[1] = make_uint4(o0[4], o0[5], o0[6], o0[7]);
-    stage_o1[0] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-    stage_o1[1] = make_uint4(o1[4], o1[5], o1[6], o1[7]);
-  }
-  if (kSwizzled) {
-    stile_c[(c & 31) * 16 + (c >> 5) * 4 + j] = valid ? static_cast<uint8_t>(s0) : 0;
-    stile_c[((c + 1) & 31) * 16 + ((c + 1) >> 5) * 4 + j] = valid ? static_cast<uint8_t>(s1) : 0;
-  } else if (valid) {
-    const int64_t s_cols = rows / 32;
-    co.scales[(col0 + c) * s_cols + row0 / 32 + j] = static_cast<uint8_t>(s0);
-    co.scales[(col0 + c + 1) * s_cols + row0 / 32 + j] = static_cast<uint8_t>(s1);
-  }
-  // The transposed codes go through shared memory so that each output row's 128 bytes
-  // leave in one coalesced piece: stage[row][chunk] holds 16-byte chunks, chunk index
-  // XOR (row & 7) against bank conflicts; the BF16 tile buffer is reused once every
-  // thread has read what it needs of it.
-  __syncthreads();
-  uint4* stage = reinterpret_cast<uint4*>(&tile[0][0]);
-  if (valid) {
-    stage[c * 8 + ((2 * j) ^ (c & 7))] = stage_o0[0];
-    stage[c * 8 + ((2 * j + 1) ^ (c & 7))] = stage_o0[1];
-    stage[(c + 1) * 8 + ((2 * j) ^ ((c + 1) & 7))] = stage_o1[0];
-    stage[(c + 1) * 8 + ((2 * j + 1) ^ ((c + 1) & 7))] = stage_o1[1];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (t >> 3) + 32 * i;  // output row = tile column
-    const int ch = t & 7;             // 16 tokens per chunk
-    if (r < cols_valid && 16 * ch < rows_valid)
-      *reinterpret_cast<uint4*>(co.codes + (col0 + r) * rows + row0 + 16 * ch) =
-          stage[r * 8 + (ch ^ (r & 7))];
-  }
-}
-
+// One CTA = one 128 x 128 BF16 tile (128 token rows x 128 columns). kRow: write the
+// row-wise copy (blocks along the columns); kCol: write the column-wise copy (blocks
+// along the rows, emitted transposed). With both, the input is read once, into a shared
+// tile whose rows are padded to 272 bytes: the row-wise pass (one thread per 32-block,
+// eight consecutive rows per eight lanes) and the column-wise pass (one word per row and
+// lane) then read it without bank conflicts.
 template <bool kRow, bool kCol, bool kSwizzled, bool kGrouped, bool kMulti>
 __global__ void __launch_bounds__(kThreads, kCol ? 6 : 1)
 quantize_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t cols, QOut ro,
@@ -304,7 +71,7 @@ quantize_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t col
   Segments* seg = reinterpret_cast<Segments*>(dyn);
   grid_dependency_wait();
   grid_launch_dependents();
-  if (kGrouped) load_segments(*seg, offsets, E, rows, status);
+  if (kGrouped) load_segments<kThreads>(*seg, offsets, E, rows, status);
 
   // ---- which tile, and where its two 512-byte scale tiles go
   int64_t bx = blockIdx.x, by = blockIdx.y, item = blockIdx.z;
@@ -444,114 +211,6 @@ quantize_tile_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t col
       reinterpret_cast<uint4*>(co.scales + col_scale_tile * 512)[t - 32] =
           reinterpret_cast<const uint4*>(stile_c)[t - 32];
   }
-}
-
-// The MXFP8 operands of the experts' GEMMs straight from the tokens' rows: segment row r holds
-// token entry_of[r] / top_k's row, times that entry's weight if there are weights (an FP32 product,
-// rounded to BF16), or zeros where there is no entry. The bytes are those of the grouped
-// quantizer on the dispatched BF16 rows, which are never written: per element that saves a
-// write and a read of 2 bytes, and a token's row comes out of L2 for all but its first expert.
-// Scale tiles past the last segment's are zero, so that the whole buffers are defined.
-struct DispatchParams {
-  const uint16_t* src;      // [tokens][cols]
-  const float* weights;     // [tokens][top_k], or nullptr
-  const int32_t* entry_of;  // [rows]
-  int64_t entries;          // tokens * top_k
-  uint32_t top_k;
-  int64_t rows, cols;
-  const int32_t* offsets;
-  int E;
-  int* status;
-};
-
-template <bool kRow, bool kCol, bool kWeighted>
-__global__ void __launch_bounds__(kThreads, 6)
-quantize_dispatch_kernel(const DispatchParams p, QOut ro, QOut co) {
-  __shared__ __align__(16) uint16_t tile[kTile][kTilePitch];
-  __shared__ __align__(16) uint8_t stile_r[512];
-  __shared__ __align__(16) uint8_t stile_c[512];
-  __shared__ int32_t token[kTile];   // of each row of the tile, -1 for none
-  __shared__ float weight[kWeighted ? kTile : 1];
-  extern __shared__ __align__(16) uint8_t dyn[];
-  Segments& seg = *reinterpret_cast<Segments*>(dyn);
-  grid_dependency_wait();
-  grid_launch_dependents();
-  load_segments(seg, p.offsets, p.E, p.rows, p.status);
-  if (!seg.ok) return;
-  const int t = threadIdx.x;
-  const int64_t bx = blockIdx.x;
-  const int tile_row = static_cast<int>(blockIdx.y);
-  const int64_t n_col_tiles = (p.cols + kTile - 1) / kTile;
-  if (tile_row >= seg.tile_base[p.E]) {   // no segment's: the tail of the scale buffers
-    const int64_t at = (tile_row * n_col_tiles + bx) * 512;
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    if (kRow && t < 32) reinterpret_cast<uint4*>(ro.scales + at)[t] = none;
-    if (kCol && t >= 32 && t < 64) reinterpret_cast<uint4*>(co.scales + at)[t - 32] = none;
-    return;
-  }
-  const int e = find_expert(seg, p.E, tile_row);
-  const int64_t i = tile_row - seg.tile_base[e];
-  const int64_t cnt = seg.off[e + 1] - seg.off[e];
-  const int64_t row0 = seg.off[e] + i * kTile;
-  const int64_t left = cnt - i * kTile;
-  const int rows_valid = static_cast<int>(left < kTile ? left : kTile);
-  const int64_t row_scale_tile = tile_row * n_col_tiles + bx;
-  const int64_t col_scale_tile =
-      n_col_tiles * seg.tile_base[e] + bx * ((cnt + kTile - 1) / kTile) + i;
-  if (t < kTile) {
-    int32_t entry = t < rows_valid ? p.entry_of[row0 + t] : -1;
-    if (entry >= p.entries) {   // a plan of other sizes
-      latch_error(p.status, MXFP8_ERR_BAD_OFFSETS);
-      entry = -1;
-    }
-    token[t] = entry < 0 ? -1 : static_cast<int32_t>(static_cast<uint32_t>(entry) / p.top_k);
-    if (kWeighted) weight[t] = entry < 0 ? 0.f : p.weights[entry];
-  }
-  __syncthreads();
-
-  const int v = t & 15, rsub = t >> 4;
-  const int64_t col0 = bx * kTile;
-  const int64_t cols_left = p.cols - col0;
-  const int cols_valid = static_cast<int>(cols_left < kTile ? cols_left : kTile);
-  const bool col_ok = 8 * v < cols_valid;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = rsub + 16 * j;
-    const int32_t from = token[r];
-    const bool ok = col_ok && from >= 0;
-    cp_async16(&tile[r][8 * v], ok ? p.src + from * p.cols + col0 + 8 * v : p.src, ok);
-  }
-  cp_async_wait_all();
-  if constexpr (kWeighted) {   // each thread on the vectors that it copied itself
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = rsub + 16 * j;
-      uint4* at = reinterpret_cast<uint4*>(&tile[r][8 * v]);
-      const uint4 x = *at;
-      const float w = weight[r];
-      const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        o[q] = cvt_bf16x2(__fmul_rn(__uint_as_float(in[q] & 0xFFFF0000u), w),
-                          __fmul_rn(__uint_as_float(in[q] << 16), w));
-      *at = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  }
-  __syncthreads();
-  if constexpr (kRow)
-    row_pass_smem<true>(tile, stile_r, ro, p.cols, row0, rows_valid, col0, cols_valid,
-                        MXFP8_RULE_FLOOR);
-  if constexpr (kCol)
-    col_pass_smem<true>(tile, stile_c, co, p.rows, row0, rows_valid, col0, cols_valid,
-                        MXFP8_RULE_FLOOR);
-  __syncthreads();
-  if (kRow && t < 32)
-    reinterpret_cast<uint4*>(ro.scales + row_scale_tile * 512)[t] =
-        reinterpret_cast<const uint4*>(stile_r)[t];
-  if (kCol && t >= 32 && t < 64)
-    reinterpret_cast<uint4*>(co.scales + col_scale_tile * 512)[t - 32] =
-        reinterpret_cast<const uint4*>(stile_c)[t - 32];
 }
 
 // Factor s of a block-wise block from its largest |BF16| bits, and 1 / s. The factor is
@@ -867,25 +526,6 @@ cudaError_t launch_axes(const QuantizeArgs& a, cudaStream_t stream) {
   return launch_tiles<kRow, kCol, false, false>(a, stream);
 }
 
-template <bool kRow, bool kCol>
-cudaError_t launch_dispatch_axes(const QuantizeDispatchArgs& a, cudaStream_t stream) {
-  const int64_t col_tiles = (a.cols + kTile - 1) / kTile;
-  const int64_t row_tiles = (a.rows + kTile - 1) / kTile + a.num_experts;
-  if (row_tiles > 65535 || col_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const DispatchParams p{static_cast<const uint16_t*>(a.src), a.weights, a.entry_of,
-                         a.tokens * a.top_k, static_cast<uint32_t>(a.top_k), a.rows, a.cols,
-                         a.offsets, a.num_experts, a.status};
-  const QOut ro{static_cast<uint8_t*>(a.row_out), static_cast<uint8_t*>(a.row_scales), 0};
-  const QOut co{static_cast<uint8_t*>(a.col_out), static_cast<uint8_t*>(a.col_scales), 0};
-  auto k = a.weights ? quantize_dispatch_kernel<kRow, kCol, true>
-                     : quantize_dispatch_kernel<kRow, kCol, false>;
-  const dim3 grid(static_cast<unsigned>(col_tiles), static_cast<unsigned>(row_tiles));
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(sizeof(Segments)));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k, grid, sizeof(Segments), stream, p, ro, co);
-}
-
 }  // namespace
 
 int64_t scale_bytes_host(int64_t rows, int64_t cols, int axis, int layout);
@@ -946,13 +586,6 @@ cudaError_t launch_blockwise_tiles(const BlockwiseArgs& a, cudaStream_t stream) 
   return launch_pdl(k, grid, 0, stream, static_cast<const uint16_t*>(a.src), a.rows, a.cols,
                     static_cast<uint8_t*>(a.row_out), a.row_inv,
                     static_cast<uint8_t*>(a.col_out), a.col_inv, a.pow2 ? 1 : 0);
-}
-
-cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t stream) {
-  if (a.rows == 0 || a.cols == 0) return cudaSuccess;
-  if (a.row_out && a.col_out) return launch_dispatch_axes<true, true>(a, stream);
-  return a.row_out ? launch_dispatch_axes<true, false>(a, stream)
-                   : launch_dispatch_axes<false, true>(a, stream);
 }
 
 cudaError_t launch_quantize(const QuantizeArgs& a, cudaStream_t stream) {

@@ -1,0 +1,651 @@
+// quantize_dispatch.cu - the MXFP8 operands of the experts' GEMMs straight from the tokens' rows.
+//
+// Segment row r holds token entry_of[r] / top_k's row, times that entry's weight if there are
+// weights (an FP32 product, rounded to BF16), or zeros where there is no entry. Its row-wise copy
+// (blocks of 32 along the columns) and its column-wise copy (blocks of 32 along the rows,
+// transposed) are the bytes of the grouped quantizer on the dispatched BF16 rows, which are never
+// written: that saves a write of 2 bytes and a read of 2 for each element. Format and layouts as
+// in quantize.cu.
+//
+// The row copy alone goes by tokens, because what a token's row becomes row-wise does not depend
+// on the expert: a warp reads a part of a row, converts it once and sends the codes to all of the
+// token's rows. The column copy's blocks mix the tokens of a segment, so it goes by 128 x 128 tiles
+// of the segments, whose rows come out of L2 for all but a token's first expert. Both copies
+// together go by tiles as in the grouped quantizer, or, where that is faster, one after the other.
+// Each kernel is persistent, so that a CTA derives the segments from the offsets once.
+//
+// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 36 us, column copy 60,
+// both 100. What bounds them: the row copy the rate at which an SM sends bulk copies away (22 bytes
+// a clock) and the scattered scale words (6 us); the column copy 268 MB read from L2 (27 us of
+// it), the ALU pipe and the L1 path, each busy half of the time, and two barriers a tile.
+// Loads in flight need the L1 cache: tables sized by the experts, one stage buffer and four CTAs
+// an SM took 60 us where two buffers of 52 KB a CTA took 87, and both copies in five CTAs 116,
+// in six 148.
+
+#include <algorithm>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "convert.cuh"
+#include "device.cuh"
+#include "internal.h"
+#include "mxfp8.h"
+#include "segments.cuh"
+#include "tile_passes.cuh"
+
+namespace mxfp8 {
+namespace {
+
+constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 4;
+constexpr int kPiece = 512;   // columns a warp converts at once, 16 a lane
+constexpr int kZeros = 512;   // bytes of zeros that padding rows are copied from
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+struct Params {
+  const uint16_t* src;       // [tokens][cols]
+  const float* weights;      // [tokens][k], or nullptr
+  const int32_t* row_of;     // [tokens][k]
+  const int32_t* entry_of;   // [rows]
+  const int32_t* offsets;
+  int64_t tokens, entries, rows, cols;
+  uint32_t k;
+  int E;
+  uint8_t* row_codes;
+  uint8_t* row_scales;
+  uint8_t* col_codes;
+  uint8_t* col_scales;
+  int64_t col_tiles, row_tiles;     // 128 x 128 tiles; row_tiles: the most that segments have
+  uint32_t parts, part_cols;        // of a token's row: how many, and their columns
+  uint32_t token_units;             // tokens * parts
+  uint32_t run;                     // column tiles of a tile item
+  uint32_t tile_items;
+  int* status;
+};
+
+struct RowStage {   // of a warp
+  __align__(16) uint8_t codes[4 * kPiece];
+  uint32_t words[4 * kPiece / kTile];
+};
+
+struct RowShared {
+  RowStage row[kWarps];
+  __align__(16) uint8_t zeros[kZeros];
+};
+
+struct TileShared {
+  __align__(16) uint8_t stage[kTile * kTile];   // transposed codes of a tile
+  __align__(16) uint8_t scales[512];            // and its scale tile
+};
+
+__device__ __forceinline__ uint32_t block_max(const uint32_t (&w)[8]) {
+  return max_abs_bf16x2(
+      max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3])),
+      max_abs_bf16x2(max_abs_bf16x2(w[4], w[5]), max_abs_bf16x2(w[6], w[7])));
+}
+
+// Two BF16 values times a weight, each product rounded to FP32 and then to BF16.
+__device__ __forceinline__ uint32_t weigh(uint32_t x, float w) {
+  return cvt_bf16x2(__fmul_rn(__uint_as_float(x & 0xFFFF0000u), w),
+                    __fmul_rn(__uint_as_float(x << 16), w));
+}
+
+// 16 columns a lane: the lane's codes, and the scale bytes of the four blocks of its eight lanes
+// in one word (zero past the columns).
+__device__ __forceinline__ uint4 convert_piece(const uint32_t (&w)[8], bool valid,
+                                               uint32_t& scale_word) {
+  uint32_t m2 = block_max(w);
+  m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 1)) & kAbs2;
+  const uint32_t s = scale_byte(max(m2 & 0xFFFFu, m2 >> 16), MXFP8_RULE_FLOOR);
+  uint32_t word = valid ? s << (8 * ((threadIdx.x >> 1) & 3)) : 0u;
+  word |= __shfl_xor_sync(kFull, word, 2);
+  word |= __shfl_xor_sync(kFull, word, 4);
+  scale_word = word;
+  if (__builtin_expect(s != 0xFFu, 1)) {
+    const uint32_t mul2 = inv_scale_bf16(s) * 0x10001u;
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) scale_bf16x2(w[i], mul2, f[2 * i], f[2 * i + 1]);
+    return make_uint4(e4m3x4_f32(f[0], f[1], f[2], f[3]), e4m3x4_f32(f[4], f[5], f[6], f[7]),
+                      e4m3x4_f32(f[8], f[9], f[10], f[11]),
+                      e4m3x4_f32(f[12], f[13], f[14], f[15]));
+  }
+  return make_uint4(nan4(w[0], w[1]), nan4(w[2], w[3]), nan4(w[4], w[5]), nan4(w[6], w[7]));
+}
+
+// Row copy. A warp takes a part of a token's row: it converts it once (once for each weight, with
+// weights) into shared memory, from where one bulk copy a segment row takes the codes away; the
+// lane that has the row issues it and writes the row's scale words. Without weights a part is
+// up to 2048 columns, in one buffer; with them up to 1024, in two buffers in turn.
+template <bool kWeighted>
+__device__ __forceinline__ void token_unit(const Params& p, const SegmentView& seg, RowStage& st,
+                                           uint32_t u, int& buf) {
+  constexpr int kPieces = kWeighted ? 2 : 4;
+  constexpr int kPart = kPieces * kPiece;
+  const int lane = threadIdx.x & 31;
+  const uint32_t t = u / p.parts;
+  const int64_t c0 = static_cast<int64_t>(u - t * p.parts) * p.part_cols;
+  const int cols = static_cast<int>(p.cols - c0 < p.part_cols ? p.cols - c0 : p.part_cols);
+  const uint16_t* x = p.src + t * p.cols + c0 + 16 * lane;
+  uint32_t v[kPieces][8];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    if (kPiece * i + 16 * lane < cols) {   // cols % 32 == 0
+      const uint4 a = ld_nc_v4(x + kPiece * i), b = ld_nc_v4(x + kPiece * i + 8);
+      v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+      v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 8; ++h) v[i][h] = 0;
+    }
+  }
+  const auto convert = [&](float w) {
+    if (kWeighted) {
+      buf ^= 1;
+      bulk_wait_read_but_one();
+    } else {
+      bulk_wait_read_all();
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      if (kPiece * i >= cols) break;
+      const int c = kPiece * i + 16 * lane;
+      uint32_t wv[8], word;
+#pragma unroll
+      for (int h = 0; h < 8; ++h) wv[h] = kWeighted ? weigh(v[i][h], w) : v[i][h];
+      const uint4 o = convert_piece(wv, c < cols, word);
+      if (c < cols) *reinterpret_cast<uint4*>(st.codes + buf * kPart + c) = o;
+      if ((lane & 7) == 0) st.words[buf * (kPart / kTile) + c / kTile] = word;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+  const auto store = [&](int32_t row, int64_t scales_at) {
+    bulk_store(p.row_codes + row * p.cols + c0, st.codes + buf * kPart,
+               static_cast<uint32_t>(cols));
+    uint32_t* to = reinterpret_cast<uint32_t*>(p.row_scales) + scales_at + c0;
+    for (int c = 0; c < cols; c += kTile)   // 128 words a tile of 128 columns
+      to[c] = st.words[buf * (kPart / kTile) + c / kTile];
+  };
+  if (!kWeighted) convert(1.f);
+  for (uint32_t j0 = 0; j0 < p.k; j0 += 32) {
+    int32_t row = -1;
+    float w = 1.f;
+    int64_t scales = 0;   // the row's first scale word
+    if (lane < p.k - j0) {
+      const int64_t entry = static_cast<int64_t>(t) * p.k + j0 + lane;
+      row = p.row_of[entry];
+      if (row >= p.rows) {   // a plan of other sizes
+        latch_error(p.status, MXFP8_ERR_BAD_OFFSETS);
+        row = -1;
+      }
+      if (row >= 0) {
+        if (kWeighted) w = p.weights[entry];
+        int lo = 0, hi = p.E - 1;   // the last expert that starts at or before the row
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (seg.off[mid] <= row) lo = mid; else hi = mid - 1;
+        }
+        const int local = row - seg.off[lo];
+        scales = (seg.tile_base[lo] + (local >> 7)) * p.col_tiles * kTile + (local & 31) * 4 +
+                 ((local & 127) >> 5);
+      }
+    }
+    if constexpr (kWeighted) {
+      for (unsigned live = __ballot_sync(kFull, row >= 0); live; live &= live - 1) {
+        const int j = __ffs(live) - 1;
+        convert(__shfl_sync(kFull, w, j));
+        if (lane == j) store(row, scales);
+        bulk_commit_group();
+      }
+    } else {
+      if (row >= 0) store(row, scales);
+    }
+  }
+  if (!kWeighted) bulk_commit_group();
+}
+
+// The place of global tile row `tile_row` in the segments.
+struct TileRow {
+  int64_t row0;        // its first row
+  int rows;            // of the segment in it
+  int64_t index, seg_tiles, seg_base;
+};
+
+__device__ __forceinline__ TileRow tile_row_of(const SegmentView& seg, int E, int tile_row) {
+  const int e = find_expert(seg, E, tile_row);
+  TileRow q;
+  q.seg_base = seg.tile_base[e];
+  q.index = tile_row - q.seg_base;
+  const int64_t count = seg.off[e + 1] - seg.off[e];
+  q.row0 = seg.off[e] + q.index * kTile;
+  const int64_t left = count - q.index * kTile;
+  q.rows = static_cast<int>(left < kTile ? left : kTile);
+  q.seg_tiles = (count + kTile - 1) / kTile;
+  return q;
+}
+
+// Row copy of rows without an entry: zero codes, and zero bytes in the scale tiles, past the
+// segments' ends too. A warp takes 32 rows of a tile row; the lane of a row issues its copies
+// from a block of zeros.
+__device__ __forceinline__ void pad_units(const Params& p, const SegmentView& seg, const uint8_t* zeros) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // Neighbouring units go to different SMs: the padding that the last segment takes is one run,
+  // and an SM sends copies away at 22 bytes a clock at most.
+  const uint32_t units = static_cast<uint32_t>(p.row_tiles) * 4, step = gridDim.x * kWarps;
+  for (uint32_t u = warp * gridDim.x + blockIdx.x; u < units; u += step) {
+    const int tile_row = static_cast<int>(u >> 2), r = 32 * (u & 3) + lane;
+    bool none = true;
+    int64_t row = -1;
+    if (tile_row < seg.tile_base[p.E]) {
+      const TileRow q = tile_row_of(seg, p.E, tile_row);
+      if (r < q.rows) {
+        row = q.row0 + r;
+        none = p.entry_of[row] < 0;
+      }
+    }
+    if (!none) continue;
+    uint32_t* scales = reinterpret_cast<uint32_t*>(p.row_scales) +
+                       tile_row * p.col_tiles * kTile + (r & 31) * 4 + (r >> 5);
+    for (int64_t i = 0; i < p.col_tiles; ++i) scales[i * kTile] = 0;
+    if (row < 0) continue;
+    for (int64_t c = 0; c < p.cols; c += kZeros)
+      bulk_store(p.row_codes + row * p.cols + c, zeros,
+                 static_cast<uint32_t>(p.cols - c < kZeros ? p.cols - c : kZeros));
+  }
+  bulk_commit_group();
+}
+
+// Column copy of a run of 128 x 128 tiles beside one another. A thread holds 8 consecutive rows
+// of 8 columns; the four lanes that hold a block's 32 rows share its maximum. The conversion takes
+// two values at once, here from two rows, which leaves a column's 8 codes in 8 consecutive bytes.
+// They pass through shared memory (8-byte units, their index XORed with twice the column's
+// eighth, so that both the writes and the reads of 16 bytes are free of bank conflicts) and leave
+// as rows of 128 bytes; the next tile's loads are in flight meanwhile.
+struct Patch {
+  uint32_t x[8][4];
+};
+
+// A thread's rows: their places in x in units of 8 values (tokens * cols is below 2^35), and
+// which of them there are.
+struct PatchRows {
+  uint32_t at[8];
+  uint32_t there;
+  bool all;      // of the warp's rows
+};
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+
+__device__ __forceinline__ void load_patch(const Params& p, const PatchRows& rows, int64_t col,
+                                           Patch& t) {
+  const uint16_t* x = p.src + col;
+  if (rows.all && col < p.cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = ld_nc_v4(x + static_cast<uint64_t>(rows.at[i]) * 8);
+      t.x[i][0] = v.x;
+      t.x[i][1] = v.y;
+      t.x[i][2] = v.z;
+      t.x[i][3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = (rows.there >> i & 1) && col < p.cols
+                          ? ld_nc_v4(x + static_cast<uint64_t>(rows.at[i]) * 8)
+                          : make_uint4(0, 0, 0, 0);
+      t.x[i][0] = v.x;
+      t.x[i][1] = v.y;
+      t.x[i][2] = v.z;
+      t.x[i][3] = v.w;
+    }
+  }
+}
+
+// Eight codes of each of two columns (low and high halves) of eight rows, scaled by mul's halves.
+__device__ __forceinline__ void convert_pair(const uint32_t (&x)[8], uint32_t mul, uint2& o0,
+                                             uint2& o1) {
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = mul_bf16x2(x[i], mul);
+  const auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+  const auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
+  o0.x = e4m3x4_f32(lo(b[0]), lo(b[1]), lo(b[2]), lo(b[3]));
+  o0.y = e4m3x4_f32(lo(b[4]), lo(b[5]), lo(b[6]), lo(b[7]));
+  o1.x = e4m3x4_f32(hi(b[0]), hi(b[1]), hi(b[2]), hi(b[3]));
+  o1.y = e4m3x4_f32(hi(b[4]), hi(b[5]), hi(b[6]), hi(b[7]));
+}
+
+// The same where a block of the two columns holds a NaN or an infinity (scale byte 0xFF).
+__device__ __forceinline__ void convert_pair_nan(const uint32_t (&x)[8], uint32_t s0, uint32_t s1,
+                                                 uint2& o0, uint2& o1) {
+  const float mul0 = inv_scale(s0), mul1 = inv_scale(s1);
+  uint32_t lo[4], hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = __byte_perm(x[2 * i], x[2 * i + 1], 0x5410);
+    hi[i] = __byte_perm(x[2 * i], x[2 * i + 1], 0x7632);
+  }
+  o0.x = s0 == 0xFFu ? nan4(lo[0], lo[1]) : e4m3x4(lo[0], lo[1], mul0);
+  o0.y = s0 == 0xFFu ? nan4(lo[2], lo[3]) : e4m3x4(lo[2], lo[3], mul0);
+  o1.x = s1 == 0xFFu ? nan4(hi[0], hi[1]) : e4m3x4(hi[0], hi[1], mul1);
+  o1.y = s1 == 0xFFu ? nan4(hi[2], hi[3]) : e4m3x4(hi[2], hi[3], mul1);
+}
+
+template <bool kWeighted>
+__device__ __forceinline__ void tile_item(const Params& p, const SegmentView& seg, TileShared& sh,
+                                          uint32_t item) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int block = warp >> 1, sub = lane >> 3, vec = lane & 7;
+  const int c = 64 * (warp & 1) + 8 * vec;   // the thread's first column of a tile
+  const uint32_t row_tiles = static_cast<uint32_t>(p.row_tiles);
+  const uint32_t part = item / row_tiles;
+  const int tile_row = static_cast<int>(item - part * row_tiles);
+  const int64_t bx0 = static_cast<int64_t>(part) * p.run;
+  const int64_t bx1 = bx0 + p.run < p.col_tiles ? bx0 + p.run : p.col_tiles;
+  if (tile_row >= seg.tile_base[p.E]) {   // no segment's: the tail of the scales
+    uint4* tail = reinterpret_cast<uint4*>(p.col_scales + (tile_row * p.col_tiles + bx0) * 512);
+    for (int i = tid; i < static_cast<int>(bx1 - bx0) * 32; i += kThreads)
+      tail[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const TileRow q = tile_row_of(seg, p.E, tile_row);
+  const bool rows_ok = 32 * block < q.rows;  // segments are multiples of 32 rows
+  uint32_t token = 0;
+  float weight = 0.f;
+  int32_t entry = rows_ok ? p.entry_of[q.row0 + 32 * block + lane] : -1;
+  if (entry >= p.entries) {   // a plan of other sizes
+    latch_error(p.status, MXFP8_ERR_BAD_OFFSETS);
+    entry = -1;
+  }
+  if (entry >= 0) {
+    token = static_cast<uint32_t>(entry) / p.k;
+    if (kWeighted) weight = p.weights[entry];
+  }
+  PatchRows rows;
+  const uint32_t row_units = static_cast<uint32_t>(p.cols / 8);
+  const unsigned there = __ballot_sync(kFull, entry >= 0);
+  rows.all = there == kFull;
+  rows.there = (there >> (8 * sub)) & 0xFFu;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rows.at[i] = __shfl_sync(kFull, token, 8 * sub + i) * row_units;
+
+  Patch t;
+  if (rows_ok) load_patch(p, rows, bx0 * kTile + c, t);
+  const int out_row = tid >> 3, chunk = tid & 7;   // a column of the tile, 16 rows of it
+  uint8_t* out = p.col_codes + (bx0 * kTile + out_row) * p.rows + q.row0 + 16 * chunk;
+  const int64_t tile0 = p.col_tiles * q.seg_base + q.index;
+  for (int64_t bx = bx0; bx < bx1; ++bx) {
+    const int64_t col0 = bx * kTile;
+    const int cols = static_cast<int>(p.cols - col0 < kTile ? p.cols - col0 : kTile);
+    if (kWeighted && rows_ok) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = __shfl_sync(kFull, weight, 8 * sub + i);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) t.x[i][h] = weigh(t.x[i][h], w);
+      }
+    }
+    uint32_t exps[4], worst = 0;
+    if (rows_ok) {
+      // Of two columns at once: the exponent fields of the block maxima, and from them the scale
+      // bytes max(E - 8, 0) and the BF16 factors 2^(127 - byte), in place at bit 7 of each half.
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t m2 = max_abs_bf16x2(
+            max_abs_bf16x2(max_abs_bf16x2(t.x[0][h], t.x[1][h]),
+                           max_abs_bf16x2(t.x[2][h], t.x[3][h])),
+            max_abs_bf16x2(max_abs_bf16x2(t.x[4][h], t.x[5][h]),
+                           max_abs_bf16x2(t.x[6][h], t.x[7][h])));
+        m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 8));
+        m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 16));
+        exps[h] = max_u16x2(m2 & 0x7F807F80u, 0x04000400u);
+        worst = max_u16x2(worst, exps[h]);
+      }
+    }
+    __syncthreads();   // the tile before has left the stage
+    const int a = c + 2 * sub;   // each of the four lanes writes the scale bytes of a column pair
+    uint8_t* scale_to = sh.scales + (a & 31) * 16 + (a >> 5) * 4 + block;
+    if (rows_ok) {
+      const bool finite = worst < 0x7F800000u && (worst & 0xFFFFu) < 0x7F80u;
+      uint8_t* stage = sh.stage + c * kTile + 8 * ((4 * block + sub) ^ (2 * vec));
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {   // columns c + 2h (low halves) and c + 2h + 1
+        uint32_t x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = t.x[i][h];
+        uint2 o0, o1;
+        if (__builtin_expect(finite, 1)) {
+          convert_pair(x, 0x83008300u - exps[h], o0, o1);
+        } else {
+          const uint32_t e0 = (exps[h] >> 7) & 0xFFu, e1 = exps[h] >> 23;
+          convert_pair_nan(x, e0 == 0xFFu ? 0xFFu : e0 - 8, e1 == 0xFFu ? 0xFFu : e1 - 8, o0, o1);
+        }
+        *reinterpret_cast<uint2*>(stage + 2 * h * kTile) = o0;
+        *reinterpret_cast<uint2*>(stage + (2 * h + 1) * kTile) = o1;
+      }
+      const uint32_t e = sub == 0 ? exps[0] : sub == 1 ? exps[1] : sub == 2 ? exps[2] : exps[3];
+      const uint32_t e0 = (e >> 7) & 0xFFu, e1 = e >> 23;
+      const bool valid = a < cols;    // cols % 8 == 0
+      scale_to[0] = static_cast<uint8_t>(!valid ? 0u : e0 == 0xFFu ? 0xFFu : e0 - 8);
+      scale_to[16] = static_cast<uint8_t>(!valid ? 0u : e1 == 0xFFu ? 0xFFu : e1 - 8);
+    } else {
+      scale_to[0] = scale_to[16] = 0;
+    }
+    if (rows_ok && bx + 1 < bx1) load_patch(p, rows, col0 + kTile + c, t);
+    __syncthreads();
+    if (16 * chunk < q.rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (out_row + 32 * i < cols)
+          *reinterpret_cast<uint4*>(out + 32 * i * p.rows) = *reinterpret_cast<const uint4*>(
+              sh.stage + (out_row + 32 * i) * kTile +
+              16 * (chunk ^ (((out_row + 32 * i) >> 3) & 7)));
+    }
+    out += kTile * p.rows;
+    if (tid < 32)
+      reinterpret_cast<uint4*>(p.col_scales + (tile0 + bx * q.seg_tiles) * 512)[tid] =
+          reinterpret_cast<const uint4*>(sh.scales)[tid];
+  }
+}
+
+template <bool kWeighted>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_row_kernel(const Params p) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  RowShared& sh = *reinterpret_cast<RowShared*>(dyn);
+  SegmentView seg(reinterpret_cast<int32_t*>(dyn + sizeof(RowShared)), p.E);
+  static_assert(kZeros == 2 * kThreads, "one store a thread");
+  reinterpret_cast<uint16_t*>(sh.zeros)[threadIdx.x] = 0;
+  fence_proxy_async_smem();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  load_segments<kThreads>(seg, p.offsets, p.E, p.rows, p.status);   // ends in a barrier
+  if (!seg.ok) return;
+  pad_units(p, seg, sh.zeros);
+  const int warp = threadIdx.x >> 5;
+  int buf = 0;
+  for (uint32_t u = blockIdx.x * kWarps + warp; u < p.token_units; u += gridDim.x * kWarps)
+    token_unit<kWeighted>(p, seg, sh.row[warp], u, buf);
+  bulk_wait_read_all();
+}
+
+template <bool kWeighted>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_col_kernel(const Params p) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  TileShared& sh = *reinterpret_cast<TileShared*>(dyn);
+  SegmentView seg(reinterpret_cast<int32_t*>(dyn + sizeof(TileShared)), p.E);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  load_segments<kThreads>(seg, p.offsets, p.E, p.rows, p.status);
+  if (!seg.ok) return;
+  for (uint32_t item = blockIdx.x; item < p.tile_items; item += gridDim.x)
+    tile_item<kWeighted>(p, seg, sh, item);
+}
+
+// Both copies by tiles from one read of a tile, as the grouped quantizer makes them.
+struct DualShared {
+  __align__(16) uint16_t tile[kTile][kTilePitch];
+  __align__(16) uint8_t scales_r[512];
+  __align__(16) uint8_t scales_c[512];
+  uint32_t at[kTile];   // of each row of the tile: its place in x in units of 8 values
+  float weight[kTile];
+};
+
+template <bool kWeighted>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_dual_kernel(const Params p) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  DualShared& sh = *reinterpret_cast<DualShared*>(dyn);
+  SegmentView seg(reinterpret_cast<int32_t*>(dyn + sizeof(DualShared)), p.E);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  load_segments<kThreads>(seg, p.offsets, p.E, p.rows, p.status);
+  if (!seg.ok) return;
+  const int t = threadIdx.x, v = t & 15, rsub = t >> 4;
+  const uint32_t row_tiles = static_cast<uint32_t>(p.row_tiles);
+  const QOut ro{p.row_codes, p.row_scales, 0}, co{p.col_codes, p.col_scales, 0};
+  for (uint32_t item = blockIdx.x; item < p.tile_items; item += gridDim.x) {
+    const uint32_t bx = item / row_tiles;
+    const int tile_row = static_cast<int>(item - bx * row_tiles);
+    if (tile_row >= seg.tile_base[p.E]) {   // no segment's: the tail of the scales
+      const int64_t at = (tile_row * p.col_tiles + bx) * 512;
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      if (t < 32) reinterpret_cast<uint4*>(p.row_scales + at)[t] = none;
+      if (t >= 32 && t < 64) reinterpret_cast<uint4*>(p.col_scales + at)[t - 32] = none;
+      continue;
+    }
+    const TileRow q = tile_row_of(seg, p.E, tile_row);
+    const int64_t col0 = static_cast<int64_t>(bx) * kTile;
+    const int cols = static_cast<int>(p.cols - col0 < kTile ? p.cols - col0 : kTile);
+    if (t < kTile) {
+      int32_t entry = t < q.rows ? p.entry_of[q.row0 + t] : -1;
+      if (entry >= p.entries) {   // a plan of other sizes
+        latch_error(p.status, MXFP8_ERR_BAD_OFFSETS);
+        entry = -1;
+      }
+      sh.at[t] = entry < 0 ? kNoRow
+                           : static_cast<uint32_t>(entry) / p.k * static_cast<uint32_t>(p.cols / 8);
+      if (kWeighted) sh.weight[t] = entry < 0 ? 0.f : p.weights[entry];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = rsub + 16 * j;
+      const uint32_t at = sh.at[r];
+      const bool ok = 8 * v < cols && at != kNoRow;
+      cp_async16(&sh.tile[r][8 * v],
+                 ok ? p.src + static_cast<uint64_t>(at) * 8 + col0 + 8 * v : p.src, ok);
+    }
+    cp_async_wait_all();
+    if constexpr (kWeighted) {   // each thread on the vectors that it copied itself
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = rsub + 16 * j;
+        uint4* at = reinterpret_cast<uint4*>(&sh.tile[r][8 * v]);
+        const uint4 x = *at;
+        const float w = sh.weight[r];
+        *at = make_uint4(weigh(x.x, w), weigh(x.y, w), weigh(x.z, w), weigh(x.w, w));
+      }
+    }
+    __syncthreads();
+    row_pass_smem<true>(sh.tile, sh.scales_r, ro, p.cols, q.row0, q.rows, col0, cols,
+                        MXFP8_RULE_FLOOR);
+    col_pass_smem<true>(sh.tile, sh.scales_c, co, p.rows, q.row0, q.rows, col0, cols,
+                        MXFP8_RULE_FLOOR);
+    __syncthreads();
+    if (t < 32)
+      reinterpret_cast<uint4*>(p.row_scales + (tile_row * p.col_tiles + bx) * 512)[t] =
+          reinterpret_cast<const uint4*>(sh.scales_r)[t];
+    if (t >= 32 && t < 64)
+      reinterpret_cast<uint4*>(p.col_scales +
+                               (p.col_tiles * q.seg_base + bx * q.seg_tiles + q.index) *
+                                   512)[t - 32] =
+          reinterpret_cast<const uint4*>(sh.scales_c)[t - 32];
+  }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+cudaError_t launch(void (*k)(const Params), int64_t wanted, size_t dyn, const Params& p,
+                   cudaStream_t stream) {
+  if (dyn > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(dyn));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(wanted), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = dyn;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_attr(&attr[0]);
+  return cudaLaunchKernelEx(&cfg, k, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t stream) {
+  if (a.rows == 0 || a.cols == 0) return cudaSuccess;
+  Params p{};
+  p.src = static_cast<const uint16_t*>(a.src);
+  p.weights = a.weights;
+  p.row_of = a.row_of;
+  p.entry_of = a.entry_of;
+  p.offsets = a.offsets;
+  p.tokens = a.tokens;
+  p.entries = a.tokens * a.top_k;
+  p.rows = a.rows;
+  p.cols = a.cols;
+  p.k = static_cast<uint32_t>(a.top_k);
+  p.E = a.num_experts;
+  p.row_codes = static_cast<uint8_t*>(a.row_out);
+  p.row_scales = static_cast<uint8_t*>(a.row_scales);
+  p.col_codes = static_cast<uint8_t*>(a.col_out);
+  p.col_scales = static_cast<uint8_t*>(a.col_scales);
+  p.col_tiles = cdiv(a.cols, kTile);
+  p.row_tiles = cdiv(a.rows, kTile) + a.num_experts;
+  p.status = a.status;
+  const int64_t most = int64_t{kCtasPerSm} * num_sms();   // CTAs
+  const size_t table = sizeof(int32_t) * SegmentView::words(p.E);
+#ifndef TWO
+#define TWO 0
+#endif
+  // Both copies from one read of the tiles, or one after the other. Apart, each is made the way that
+  // suits it, which pays for large copies of tokens with several experts, unweighted: 8192 tokens of
+  // 2048 columns, 8 experts each, 100 us and 110 in one; 16384, 4 experts, 107 and 111; but 4096
+  // tokens, 8 experts, 65 and 65; 8192, 4 experts, 71 and 66; 16384 of 4096, 2 experts, 116 and 101;
+  // 256, 8 experts, 29 and 26.
+  const bool apart = a.top_k >= 4 && !a.weights && p.entries * a.cols >= int64_t{1} << 27;
+  if (a.row_out && a.col_out && !apart) {
+    const int64_t items = p.row_tiles * p.col_tiles;
+    if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    p.tile_items = static_cast<uint32_t>(items);
+    return launch(a.weights ? dispatch_dual_kernel<true> : dispatch_dual_kernel<false>,
+                  std::min(most, items), sizeof(DualShared) + table, p, stream);
+  }
+  if (a.row_out) {
+    // parts of a row as long as the buffers take, while each warp keeps a unit
+    p.part_cols = (a.weights ? 2 : 4) * kPiece;
+    while (p.part_cols > kPiece && a.tokens * cdiv(a.cols, p.part_cols) < most * kWarps)
+      p.part_cols /= 2;
+    const int64_t parts = cdiv(a.cols, p.part_cols), units = a.tokens * parts;
+    if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    p.parts = static_cast<uint32_t>(parts);
+    p.token_units = static_cast<uint32_t>(units);
+    const int64_t work = units > 4 * p.row_tiles ? units : 4 * p.row_tiles;
+    const cudaError_t e = launch(a.weights ? dispatch_row_kernel<true> : dispatch_row_kernel<false>,
+                                 std::min(most, cdiv(work, kWarps)), sizeof(RowShared) + table, p, stream);
+    if (e != cudaSuccess || !a.col_out) return e;
+  }
+  // neighbouring tiles are joined into items while each CTA keeps four
+  const int64_t run = p.row_tiles * p.col_tiles / (4 * most);
+  p.run = static_cast<uint32_t>(run < 1 ? 1 : run > 8 ? 8 : run);
+  const int64_t items = p.row_tiles * cdiv(p.col_tiles, p.run);
+  if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  p.tile_items = static_cast<uint32_t>(items);
+  return launch(a.weights ? dispatch_col_kernel<true> : dispatch_col_kernel<false>, std::min(most, items),
+                sizeof(TileShared) + table, p, stream);
+}
+
+}  // namespace mxfp8

@@ -242,12 +242,31 @@ def check_quantized(m, x, plan, experts, w):
 @pytest.mark.parametrize("weighted", [False, True])
 @pytest.mark.parametrize("tokens,k,experts,cols,dropped", [
     (1, 8, 128, 2048, 0.0), (37, 8, 16, 32, 0.0), (300, 2, 3, 96, 0.2), (129, 3, 300, 160, 0.1),
-    (1021, 6, 8, 224, 0.0), (5, 1, 2, 1056, 1.0), (700, 1, 1, 128, 0.0)])
+    (1021, 6, 8, 224, 0.0), (5, 1, 2, 1056, 1.0), (700, 1, 1, 128, 0.0), (60, 40, 5, 544, 0.1),
+    (33, 2, 1000, 2592, 0.0), (6000, 2, 4, 256, 0.3)])
 def test_quantize_dispatch(m, tokens, k, experts, cols, dropped, weighted):
     plan = m.route(choices(tokens, tokens, k, experts, dropped).to(DEV), experts)
     x = values(12, tokens, cols, BF16)
     x[:, ::17] *= 30
     check_quantized(m, x, plan, experts, weights(13, tokens, k) if weighted else None)
+
+
+def test_quantize_dispatch_of_many_elements(m):
+    """2^27 elements and more, where both copies are made one after the other: against the grouped
+    quantizer on the dispatched rows."""
+    for tokens, k, cols in ((8192, 8, 2048), (5000, 7, 4096)):
+        plan = m.route(choices(34, tokens, k, 64, 0.0).to(DEV), 64)
+        x = torch.randn(tokens, cols, device=DEV).to(BF16)
+        x[17, 100:200] = float("inf")
+        spread = m.dispatch(x, plan)
+        got = m.quantize_dispatch_dual(x, plan)
+        want = m.quantize_grouped_dual(spread, plan.offsets)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+        off = plan.offsets.cpu().numpy()
+        tiles = int(((off[1:] - off[:-1] + 127) // 128).sum())
+        for a, b, per in ((got[1], want[1], -(-cols // 128)), (got[3], want[3], -(-cols // 128))):
+            assert torch.equal(a[:tiles * per * 512], b[:tiles * per * 512])
+            assert not a[tiles * per * 512:].any()
 
 
 def test_quantize_dispatch_of_nan_infinity_and_tiny_values(m):
@@ -304,9 +323,11 @@ def test_a_plan_of_other_rows_is_not_followed(m):
         assert torch.equal(got, call(right))
     m.dispatch(x, wrong)
     assert m.device_status() == m.ERR_BAD_OFFSETS
-    codes, _ = m.quantize_dispatch(x, wrong)
+    m.quantize_dispatch(x, wrong)
     assert m.device_status() == m.ERR_BAD_OFFSETS
-    assert not codes[0].any()
+    codes, _ = m.quantize_dispatch(x, wrong, m.COL)
+    assert m.device_status() == m.ERR_BAD_OFFSETS
+    assert not codes[:, 0].any()
 
 
 def test_no_tokens(m):

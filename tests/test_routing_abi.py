@@ -66,20 +66,20 @@ def test_dispatch(lib):
 
 
 def test_quantize_dispatch(lib):
-    def call(x=P, tokens=4, cols=64, k=2, w=P, entry_of=P, rows=64, offsets=P, experts=4, rc=P,
-             rs=P, cc=P, cs=P):
-        return lib.mxfp8_quantize_dispatch(x, tokens, cols, k, w, entry_of, rows, offsets,
+    def call(x=P, tokens=4, cols=64, k=2, w=P, row_of=P, entry_of=P, rows=64, offsets=P,
+             experts=4, rc=P, rs=P, cc=P, cs=P):
+        return lib.mxfp8_quantize_dispatch(x, tokens, cols, k, w, row_of, entry_of, rows, offsets,
                                            experts, rc, rs, cc, cs, None)
 
     none = dict(rc=None, rs=None)
-    for kw in (dict(x=None), dict(tokens=-1), dict(k=0), dict(entry_of=None), dict(rows=-32),
-               dict(offsets=None), dict(experts=0), dict(experts=1025), dict(rc=None),
+    for kw in (dict(x=None), dict(tokens=-1), dict(k=0), dict(row_of=None),
+               dict(entry_of=None), dict(rows=-32), dict(offsets=None), dict(experts=0), dict(experts=1025), dict(rc=None),
                dict(rs=None), dict(cc=None), dict(cs=None), dict(cols=-32),
                dict(rc=None, rs=None, cc=None, cs=None), dict(rows=65535 * 128),
-               dict(tokens=BIG), dict(cols=BIG)):
+               dict(tokens=BIG), dict(cols=BIG), dict(tokens=2 ** 20, cols=2 ** 15)):
         assert call(**kw) == m.ERR_INVALID_ARG, kw
     for kw in (dict(cols=40), dict(cols=36, **none), dict(rows=40), dict(x=HALF), dict(w=ODD),
-               dict(entry_of=ODD), dict(offsets=ODD), dict(rc=HALF), dict(rs=HALF),
+               dict(row_of=ODD), dict(entry_of=ODD), dict(offsets=ODD), dict(rc=HALF), dict(rs=HALF),
                dict(cc=HALF), dict(cs=HALF)):
         assert call(**kw) == m.ERR_ALIGNMENT, kw
     assert call(rows=0, x=None) == m.OK
