@@ -725,35 +725,43 @@ def route(ids: torch.Tensor, num_experts: int, rows: Optional[int] = None,
     row_of = _new((tokens, top_k), torch.int32, dev, stream)
     entry_of = _new((rows,), torch.int32, dev, stream)
     _check(lib().mxfp8_route(_ptr(ids), tokens, top_k, num_experts, rows, _ptr(offsets),
-                             _ptr(row_of), _ptr(entry_of), _stream(stream)), "mxfp8_route")
+                             _ptr(row_of), _ptr(entry_of), _here(stream)), "mxfp8_route")
     return RoutePlan(offsets, row_of, entry_of)
 
 
-def _plan(plan: RoutePlan, weights, tokens: Optional[int] = None):
-    """A plan's tensors, and the weights beside them, checked. Returns (tokens, top_k, rows)."""
-    _require(plan.row_of, torch.int32, "plan.row_of")
-    _require(plan.entry_of, torch.int32, "plan.entry_of")
-    if plan.row_of.dim() != 2 or plan.row_of.shape[1] < 1:
-        raise ValueError(f"plan.row_of must be [tokens, top_k], got {tuple(plan.row_of.shape)}")
-    n, top_k = plan.row_of.shape
-    if tokens is not None and tokens != n:
-        raise ValueError(f"{tokens} rows of tokens; the plan is of {n}")
+def _here(stream):
+    """_stream, once a CUDA tensor on the current device has been seen."""
+    return _raw_stream(_device()) if stream is None else stream.cuda_stream
+
+
+def _plan(plan: RoutePlan, weights):
+    """A plan's rows, and the weights beside them, checked. Returns (tokens, top_k, rows)."""
+    row_of, entry_of = plan.row_of, plan.entry_of
+    _require(row_of, torch.int32, "plan.row_of")
+    _require(entry_of, torch.int32, "plan.entry_of")
+    shape = row_of.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"plan.row_of must be [tokens, top_k], got {tuple(shape)}")
     if weights is not None:
         _require(weights, torch.float32, "weights")
-        if weights.shape != plan.row_of.shape:
-            raise ValueError(f"weights are {tuple(weights.shape)}; the plan is of "
-                             f"{tuple(plan.row_of.shape)}")
-    return n, top_k, plan.entry_of.numel()
+        if weights.shape != shape:
+            raise ValueError(f"weights are {tuple(weights.shape)}; the plan is of {tuple(shape)}")
+    return shape[0], shape[1], entry_of.shape.numel()
 
 
-def _rows(t: torch.Tensor, name: str):
-    """Rows of a token or a segment: 2-D, BF16 or FP32. Returns the dtype code."""
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    _require(t, t.dtype, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
-    return OUT_BF16 if t.dtype == torch.bfloat16 else OUT_FP32
+def _rows(t: torch.Tensor, rows: Optional[int], name: str):
+    """Rows of the plan's tokens or segments: 2-D, BF16 or FP32. Returns (dtype, its code,
+    columns)."""
+    dt = t.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {dt}")
+    _require(t, dt, name)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {len(shape)}")
+    if shape[0] != rows:
+        raise ValueError(f"{name} has {shape[0]} rows; the plan has {rows}")
+    return dt, OUT_BF16 if dt is torch.bfloat16 else OUT_FP32, shape[1]
 
 
 def _optional(t):
@@ -765,52 +773,43 @@ def dispatch(x: torch.Tensor, plan: RoutePlan, weights: Optional[torch.Tensor] =
     """The tokens' rows x (BF16 or FP32 [tokens, cols]) in the plan's segments, [rows, cols]: row
     r holds its entry's token, times that entry's weight (float32 [tokens, top_k]) if given;
     padding rows are zero. The gradient of x without weights is combine(grad, plan)."""
-    dt = _rows(x, "x")
-    tokens, top_k, rows = _plan(plan, weights, x.shape[0])
-    cols = x.shape[1]
+    tokens, top_k, rows = _plan(plan, weights)
+    dt, code, cols = _rows(x, tokens, "x")
     if out is None:
-        out = _new((rows, cols), x.dtype, x.device, stream)
+        out = _new((rows, cols), dt, x.device, stream)
     else:
-        _buffer(out, x.dtype, rows * cols, "out")
-    _check(lib().mxfp8_dispatch(_ptr(x), dt, tokens, cols, top_k, _optional(weights),
+        _buffer(out, dt, rows * cols, "out")
+    _check(lib().mxfp8_dispatch(_ptr(x), code, tokens, cols, top_k, _optional(weights),
                                 _ptr(plan.row_of), _ptr(plan.entry_of), rows, _ptr(out),
-                                _stream(stream)), "mxfp8_dispatch")
+                                _here(stream)), "mxfp8_dispatch")
     return out
 
 
-def _quantize_dispatch(x, plan, weights, row, col, stream):
-    """Both copies' buffers; `row` and `col` are (codes, scales) with None to be allocated, or
-    None for a copy that is not made."""
-    _require(x, torch.bfloat16, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must have two dimensions, got {x.dim()}")
-    tokens, top_k, rows = _plan(plan, weights, x.shape[0])
-    _require(plan.offsets, torch.int32, "plan.offsets")
-    cols, e = x.shape[1], plan.offsets.numel() - 1
-    got = []
-    for axis, pair, name in ((ROW, row, "row"), (COL, col, "col")):
-        if pair is None:
-            got += [None, None]
-            continue
-        codes, scales = pair
-        need = grouped_scale_bytes(rows, cols, e, axis)
-        if codes is None:
-            codes = _new((rows, cols) if axis == ROW else (cols, rows), torch.uint8, x.device,
-                         stream)
-        else:
-            _buffer(codes, torch.uint8, rows * cols, f"{name} codes")
-        if scales is None:
-            scales = _new((need,), torch.uint8, x.device, stream)
-        else:
-            _buffer(scales, torch.uint8, need, f"{name} scales")
-        got += [codes, scales]
-    if rows and cols:
-        _check(lib().mxfp8_quantize_dispatch(_ptr(x), tokens, cols, top_k, _optional(weights),
-                                             _ptr(plan.row_of), _ptr(plan.entry_of), rows,
-                                             _ptr(plan.offsets), e,
-                                             *(_optional(t) for t in got), _stream(stream)),
+def _dispatch_copy(rows, cols, experts, axis, codes, scales, device, stream):
+    """Codes and scales of one grouped copy: given ones checked, absent ones allocated."""
+    need = lib().mxfp8_grouped_scale_bytes(rows, cols, experts, axis)
+    if need == 0 and cols:   # cols not a multiple of 32, or sizes that do not fit: as the call says
+        _check(ERR_ALIGNMENT if axis == ROW and cols % 32 else ERR_INVALID_ARG,
                "mxfp8_quantize_dispatch")
-    return got
+    shape = (rows, cols) if axis == ROW else (cols, rows)
+    if codes is None:
+        codes = _new(shape, torch.uint8, device, stream)
+    else:
+        _buffer(codes, torch.uint8, rows * cols, "codes")
+    if scales is None:
+        scales = _new((need,), torch.uint8, device, stream)
+    else:
+        _buffer(scales, torch.uint8, need, "scales")
+    return codes, scales
+
+
+def _dispatch_source(x, plan, weights):
+    """Checks quantize_dispatch's inputs. Returns (tokens, top_k, rows, cols, experts)."""
+    _require(x, torch.bfloat16, "x")
+    _require(plan.offsets, torch.int32, "plan.offsets")
+    tokens, top_k, rows = _plan(plan, weights)
+    cols = _rows(x, tokens, "x")[2]
+    return tokens, top_k, rows, cols, plan.offsets.shape.numel() - 1
 
 
 def quantize_dispatch(x: torch.Tensor, plan: RoutePlan, axis: int = ROW,
@@ -820,19 +819,33 @@ def quantize_dispatch(x: torch.Tensor, plan: RoutePlan, axis: int = ROW,
     are zero."""
     if axis not in (ROW, COL):
         raise ValueError(f"axis must be ROW or COL, got {axis}")
-    got = _quantize_dispatch(x, plan, weights, (out, scales) if axis == ROW else None,
-                             (out, scales) if axis == COL else None, stream)
-    return tuple(got[:2] if axis == ROW else got[2:])
+    tokens, top_k, rows, cols, e = _dispatch_source(x, plan, weights)
+    codes, scales = _dispatch_copy(rows, cols, e, axis, out, scales, x.device, stream)
+    a, b = _ptr(codes), _ptr(scales)
+    _check(lib().mxfp8_quantize_dispatch(_ptr(x), tokens, cols, top_k, _optional(weights),
+                                         _ptr(plan.row_of), _ptr(plan.entry_of), rows,
+                                         _ptr(plan.offsets), e,
+                                         *((a, b, None, None) if axis == ROW else
+                                           (None, None, a, b)), _here(stream)),
+           "mxfp8_quantize_dispatch")
+    return codes, scales
 
 
 def quantize_dispatch_dual(x: torch.Tensor, plan: RoutePlan,
                            weights: Optional[torch.Tensor] = None, row_out=None, row_scales=None,
                            col_out=None, col_scales=None, stream=None):
-    """quantize_dispatch ROW and COL from one read. Returns (row_codes, row_scales, col_codes,
+    """quantize_dispatch ROW and COL in one call. Returns (row_codes, row_scales, col_codes,
     col_scales): an expert layer's forward and weight-gradient operands; with x the gradient of
     combine's result and its weights, the operands of the layer before it."""
-    return tuple(_quantize_dispatch(x, plan, weights, (row_out, row_scales),
-                                    (col_out, col_scales), stream))
+    tokens, top_k, rows, cols, e = _dispatch_source(x, plan, weights)
+    row = _dispatch_copy(rows, cols, e, ROW, row_out, row_scales, x.device, stream)
+    col = _dispatch_copy(rows, cols, e, COL, col_out, col_scales, x.device, stream)
+    _check(lib().mxfp8_quantize_dispatch(_ptr(x), tokens, cols, top_k, _optional(weights),
+                                         _ptr(plan.row_of), _ptr(plan.entry_of), rows,
+                                         _ptr(plan.offsets), e, _ptr(row[0]), _ptr(row[1]),
+                                         _ptr(col[0]), _ptr(col[1]), _here(stream)),
+           "mxfp8_quantize_dispatch")
+    return row + col
 
 
 def combine(y: torch.Tensor, plan: RoutePlan, weights: Optional[torch.Tensor] = None, out=None,
@@ -840,17 +853,14 @@ def combine(y: torch.Tensor, plan: RoutePlan, weights: Optional[torch.Tensor] = 
     """The sum of each token's segment rows y (BF16 or FP32 [rows, cols]), weighted (float32
     [tokens, top_k]) if weights are given, [tokens, cols] of y's type: FP32 sums in the order of
     the choices, rounded once. A token without rows gets zeros."""
-    dt = _rows(y, "y")
     tokens, top_k, rows = _plan(plan, weights)
-    if y.shape[0] != rows:
-        raise ValueError(f"y has {y.shape[0]} rows; the plan has {rows}")
-    cols = y.shape[1]
+    dt, code, cols = _rows(y, rows, "y")
     if out is None:
-        out = _new((tokens, cols), y.dtype, y.device, stream)
+        out = _new((tokens, cols), dt, y.device, stream)
     else:
-        _buffer(out, y.dtype, tokens * cols, "out")
-    _check(lib().mxfp8_combine(_ptr(y), dt, rows, cols, tokens, top_k, _optional(weights),
-                               _ptr(plan.row_of), _ptr(out), _stream(stream)), "mxfp8_combine")
+        _buffer(out, dt, tokens * cols, "out")
+    _check(lib().mxfp8_combine(_ptr(y), code, rows, cols, tokens, top_k, _optional(weights),
+                               _ptr(plan.row_of), _ptr(out), _here(stream)), "mxfp8_combine")
     return out
 
 
@@ -860,31 +870,28 @@ def combine_backward(grad_out: torch.Tensor, y: torch.Tensor, plan: RoutePlan,
     """Gradients of combine(y, plan, weights): (grad_y [rows, cols] of y's type, padding rows
     zero; grad_weights float32 [tokens, top_k]). grad_rows=False leaves the first out (None):
     quantize_dispatch_dual(grad_out, plan, weights) gives it as the grouped GEMMs read it."""
-    dt = _rows(y, "y")
-    _require(grad_out, y.dtype, "grad_out")
     if weights is None:
         raise ValueError("weights are needed; without them grad_y is dispatch(grad_out, plan)")
     tokens, top_k, rows = _plan(plan, weights)
-    cols = y.shape[1]
-    if y.shape[0] != rows:
-        raise ValueError(f"y has {y.shape[0]} rows; the plan has {rows}")
-    if tuple(grad_out.shape) != (tokens, cols):
+    dt, code, cols = _rows(y, rows, "y")
+    _require(grad_out, dt, "grad_out")
+    if grad_out.shape != (tokens, cols):
         raise ValueError(f"grad_out must be {(tokens, cols)}, got {tuple(grad_out.shape)}")
     if not grad_rows:
         if out is not None:
             raise ValueError("out is given, but grad_rows is False")
     elif out is None:
-        out = _new((rows, cols), y.dtype, y.device, stream)
+        out = _new((rows, cols), dt, y.device, stream)
     else:
-        _buffer(out, y.dtype, rows * cols, "out")
+        _buffer(out, dt, rows * cols, "out")
     if out_weights is None:
         out_weights = _new((tokens, top_k), torch.float32, y.device, stream)
     else:
         _buffer(out_weights, torch.float32, tokens * top_k, "out_weights")
-    _check(lib().mxfp8_combine_backward(_ptr(grad_out), _ptr(y), dt, tokens, cols, top_k,
+    _check(lib().mxfp8_combine_backward(_ptr(grad_out), _ptr(y), code, tokens, cols, top_k,
                                         _ptr(weights), _ptr(plan.row_of), _ptr(plan.entry_of),
                                         rows, _optional(out), _ptr(out_weights),
-                                        _stream(stream)), "mxfp8_combine_backward")
+                                        _here(stream)), "mxfp8_combine_backward")
     return out, out_weights
 
 
@@ -913,19 +920,20 @@ def swiglu(gate_up: torch.Tensor, checkpoint: bool = True, rule: int = RULE_CEIL
     else:
         _buffer(out, torch.bfloat16, rows * width, "out")
     if checkpoint:
+        n, blocks = 2 * rows * width, width // 16
         if codes is None:
             codes = _new((rows, 2 * width), torch.uint8, dev, stream)
         else:
-            _buffer(codes, torch.uint8, 2 * rows * width, "codes")
+            _buffer(codes, torch.uint8, n, "codes")
         if scales is None:
-            scales = _new((rows, width // 16), torch.uint8, dev, stream)
+            scales = _new((rows, blocks), torch.uint8, dev, stream)
         else:
-            _buffer(scales, torch.uint8, rows * (width // 16), "scales")
+            _buffer(scales, torch.uint8, rows * blocks, "scales")
     elif codes is not None or scales is not None:
         raise ValueError("codes or scales are given, but checkpoint is False")
     if rows and width:
         _check(lib().mxfp8_swiglu(_ptr(gate_up), rows, width, _ptr(out), _optional(codes),
-                                  _optional(scales), rule, _stream(stream)), "mxfp8_swiglu")
+                                  _optional(scales), rule, _here(stream)), "mxfp8_swiglu")
     return Swiglu(out, codes, scales)
 
 
@@ -954,7 +962,7 @@ def swiglu_backward(grad_h: torch.Tensor, codes: torch.Tensor, scales: torch.Ten
     else:
         _buffer(out_h, torch.bfloat16, rows * width, "out_h")
     _check(lib().mxfp8_swiglu_backward(_ptr(grad_h), _ptr(codes), _ptr(scales), rows, width,
-                                       _ptr(out), _optional(out_h), _stream(stream)),
+                                       _ptr(out), _optional(out_h), _here(stream)),
            "mxfp8_swiglu_backward")
     return out, out_h
 

@@ -229,32 +229,25 @@ __device__ __forceinline__ TileRow tile_row_of(const SegmentView& seg, int E, in
 // Row copy of rows without an entry: zero codes, and zero bytes in the scale tiles, past the
 // segments' ends too. A warp takes 32 rows of a tile row; the lane of a row issues its copies
 // from a block of zeros.
-__device__ __forceinline__ void pad_units(const Params& p, const SegmentView& seg, const uint8_t* zeros) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // Neighbouring units go to different SMs: the padding that the last segment takes is one run,
-  // and an SM sends copies away at 22 bytes a clock at most.
-  const uint32_t units = static_cast<uint32_t>(p.row_tiles) * 4, step = gridDim.x * kWarps;
-  for (uint32_t u = warp * gridDim.x + blockIdx.x; u < units; u += step) {
-    const int tile_row = static_cast<int>(u >> 2), r = 32 * (u & 3) + lane;
-    bool none = true;
-    int64_t row = -1;
-    if (tile_row < seg.tile_base[p.E]) {
-      const TileRow q = tile_row_of(seg, p.E, tile_row);
-      if (r < q.rows) {
-        row = q.row0 + r;
-        none = p.entry_of[row] < 0;
-      }
-    }
-    if (!none) continue;
-    uint32_t* scales = reinterpret_cast<uint32_t*>(p.row_scales) +
-                       tile_row * p.col_tiles * kTile + (r & 31) * 4 + (r >> 5);
-    for (int64_t i = 0; i < p.col_tiles; ++i) scales[i * kTile] = 0;
-    if (row < 0) continue;
-    for (int64_t c = 0; c < p.cols; c += kZeros)
-      bulk_store(p.row_codes + row * p.cols + c, zeros,
-                 static_cast<uint32_t>(p.cols - c < kZeros ? p.cols - c : kZeros));
+__device__ __forceinline__ void pad_unit(const Params& p, const SegmentView& seg,
+                                         const uint8_t* zeros, uint32_t u) {
+  const int lane = threadIdx.x & 31;
+  const int tile_row = static_cast<int>(u >> 2), r = 32 * (u & 3) + lane;
+  uint8_t* scales = p.row_scales + tile_row * p.col_tiles * 512;
+  if (tile_row >= seg.tile_base[p.E]) {   // no segment's: a quarter of its tiles
+    uint4* quarter = reinterpret_cast<uint4*>(scales) + (u & 3) * p.col_tiles * 8;
+    for (int64_t i = lane; i < p.col_tiles * 8; i += 32) quarter[i] = make_uint4(0, 0, 0, 0);
+    return;
   }
-  bulk_commit_group();
+  const TileRow q = tile_row_of(seg, p.E, tile_row);
+  const int64_t row = q.row0 + r;
+  if (r < q.rows && p.entry_of[row] >= 0) return;
+  uint32_t* word = reinterpret_cast<uint32_t*>(scales) + (r & 31) * 4 + (r >> 5);
+  for (int64_t i = 0; i < p.col_tiles; ++i) word[i * kTile] = 0;
+  if (r >= q.rows) return;
+  for (int64_t c = 0; c < p.cols; c += kZeros)
+    bulk_store(p.row_codes + row * p.cols + c, zeros,
+               static_cast<uint32_t>(p.cols - c < kZeros ? p.cols - c : kZeros));
 }
 
 // Column copy of a run of 128 x 128 tiles beside one another. A thread holds 8 consecutive rows
@@ -461,11 +454,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_row_kernel(cons
   grid_launch_dependents();
   load_segments<kThreads>(seg, p.offsets, p.E, p.rows, p.status);   // ends in a barrier
   if (!seg.ok) return;
-  pad_units(p, seg, sh.zeros);
+  // Neighbouring units go to different SMs: the padding that the last segment takes is one run,
+  // and an SM sends copies away at 22 bytes a clock at most.
   const int warp = threadIdx.x >> 5;
+  const uint32_t units = p.token_units + static_cast<uint32_t>(p.row_tiles) * 4;   // below 2^32
   int buf = 0;
-  for (uint32_t u = blockIdx.x * kWarps + warp; u < p.token_units; u += gridDim.x * kWarps)
-    token_unit<kWeighted>(p, seg, sh.row[warp], u, buf);
+  for (uint32_t u = warp * gridDim.x + blockIdx.x; u < units; u += gridDim.x * kWarps) {
+    if (u < p.token_units) {
+      token_unit<kWeighted>(p, seg, sh.row[warp], u, buf);
+    } else {
+      pad_unit(p, seg, sh.zeros, u - p.token_units);
+      __syncwarp();
+      bulk_commit_group();
+    }
+  }
   bulk_wait_read_all();
 }
 
@@ -633,7 +635,7 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
     if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.parts = static_cast<uint32_t>(parts);
     p.token_units = static_cast<uint32_t>(units);
-    const int64_t work = units > 4 * p.row_tiles ? units : 4 * p.row_tiles;
+    const int64_t work = units + 4 * p.row_tiles;
     const cudaError_t e = launch(a.weights ? dispatch_row_kernel<true> : dispatch_row_kernel<false>,
                                  std::min(most, cdiv(work, kWarps)), sizeof(RowShared) + table, p, stream);
     if (e != cudaSuccess || !a.col_out) return e;
