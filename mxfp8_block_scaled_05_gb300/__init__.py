@@ -690,6 +690,9 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, stats: 
 
 # ------------------------------------------------------------- routing tokens to experts
 
+_INT32, _FP32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+
+
 class RoutePlan(NamedTuple):
     """Entries (token, choice) sorted by expert into segments padded to 32 rows (route). All
     int32, on the device."""
@@ -716,8 +719,12 @@ def route(ids: torch.Tensor, num_experts: int, rows: Optional[int] = None,
     if ids.dim() != 2 or ids.shape[1] < 1:
         raise ValueError(f"ids must be [tokens, top_k], got {tuple(ids.shape)}")
     tokens, top_k = ids.shape
+    n = tokens * top_k
     if rows is None:
-        rows = route_rows(tokens, top_k, num_experts)
+        if 0 < num_experts <= 1024 and n < 1 << 30:
+            rows = (n + 31 * min(n, num_experts)) // 32 * 32   # route_rows
+        else:
+            rows = route_rows(tokens, top_k, num_experts)
     elif rows < 0:
         raise ValueError(f"rows must not be negative, got {rows}")
     dev = ids.device
@@ -735,33 +742,37 @@ def _here(stream):
 
 
 def _plan(plan: RoutePlan, weights):
-    """A plan's rows, and the weights beside them, checked. Returns (tokens, top_k, rows)."""
+    """A plan's rows, and the weights beside them, checked: all that is right in one expression, as
+    a call of a few tokens takes as long in here as on the GPU. Returns (tokens, top_k, rows)."""
     row_of, entry_of = plan.row_of, plan.entry_of
-    _require(row_of, torch.int32, "plan.row_of")
-    _require(entry_of, torch.int32, "plan.entry_of")
+    if not (row_of.is_cuda and row_of.dtype is _INT32 is entry_of.dtype
+            and row_of.get_device() == _device() == entry_of.get_device()
+            and row_of.is_contiguous() and entry_of.is_contiguous()):
+        _require(row_of, _INT32, "plan.row_of")
+        _require(entry_of, _INT32, "plan.entry_of")
     shape = row_of.shape
     if len(shape) != 2 or shape[1] < 1:
         raise ValueError(f"plan.row_of must be [tokens, top_k], got {tuple(shape)}")
     if weights is not None:
-        _require(weights, torch.float32, "weights")
+        _require(weights, _FP32, "weights")
         if weights.shape != shape:
             raise ValueError(f"weights are {tuple(weights.shape)}; the plan is of {tuple(shape)}")
-    return shape[0], shape[1], entry_of.shape.numel()
+    return *shape, entry_of.numel()
 
 
 def _rows(t: torch.Tensor, rows: Optional[int], name: str):
     """Rows of the plan's tokens or segments: 2-D, BF16 or FP32. Returns (dtype, its code,
     columns)."""
     dt = t.dtype
-    if dt is not torch.bfloat16 and dt is not torch.float32:
+    if dt is not _BF16 and dt is not _FP32:
         raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {dt}")
     _require(t, dt, name)
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must have two dimensions, got {len(shape)}")
-    if shape[0] != rows:
-        raise ValueError(f"{name} has {shape[0]} rows; the plan has {rows}")
-    return dt, OUT_BF16 if dt is torch.bfloat16 else OUT_FP32, shape[1]
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    n, cols = t.shape
+    if n != rows:
+        raise ValueError(f"{name} has {n} rows; the plan has {rows}")
+    return dt, OUT_BF16 if dt is _BF16 else OUT_FP32, cols
 
 
 def _optional(t):

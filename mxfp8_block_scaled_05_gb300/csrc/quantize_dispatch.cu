@@ -11,11 +11,11 @@
 // on the expert: a warp reads a part of a row, converts it once and sends the codes to all of the
 // token's rows. The column copy's blocks mix the tokens of a segment, so it goes by 128 x 128 tiles
 // of the segments, whose rows come out of L2 for all but a token's first expert. Both copies
-// together go by tiles as in the grouped quantizer, or, where that is faster, one after the other.
-// Each kernel is persistent, so that a CTA derives the segments from the offsets once.
+// together go so side by side or in turn, or from one read of the tiles as in the grouped
+// quantizer: see the launcher. CTAs are persistent and derive the segments from the offsets once.
 //
-// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 36 us, column copy 60,
-// both 100. What bounds them: the row copy the rate at which an SM sends bulk copies away (22 bytes
+// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 35 us, column copy 60,
+// both 99. What bounds them: the row copy the rate at which an SM sends bulk copies away (22 bytes
 // a clock) and the scattered scale words (6 us); the column copy 268 MB read from L2 (27 us of
 // it), the ALU pipe and the L1 path, each busy half of the time, and two barriers a tile.
 // Loads in flight need the L1 cache: tables sized by the experts, one stage buffer and four CTAs
@@ -60,6 +60,7 @@ struct Params {
   uint32_t token_units;             // tokens * parts
   uint32_t run;                     // column tiles of a tile item
   uint32_t tile_items;
+  uint32_t col_ctas;                // that make the column copy
   int* status;
 };
 
@@ -77,6 +78,9 @@ struct TileShared {
   __align__(16) uint8_t stage[kTile * kTile];   // transposed codes of a tile
   __align__(16) uint8_t scales[512];            // and its scale tile
 };
+
+constexpr size_t kBuffers =
+    sizeof(RowShared) > sizeof(TileShared) ? sizeof(RowShared) : sizeof(TileShared);
 
 __device__ __forceinline__ uint32_t block_max(const uint32_t (&w)[8]) {
   return max_abs_bf16x2(
@@ -442,46 +446,43 @@ __device__ __forceinline__ void tile_item(const Params& p, const SegmentView& se
   }
 }
 
+// The first col_ctas CTAs make the column copy, the others the row copy: either alone, or both side
+// by side, three to one, as the row copy waits for its writes and the column copy for its reads.
 template <bool kWeighted>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_row_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_apart_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t dyn[];
-  RowShared& sh = *reinterpret_cast<RowShared*>(dyn);
-  SegmentView seg(reinterpret_cast<int32_t*>(dyn + sizeof(RowShared)), p.E);
-  static_assert(kZeros == 2 * kThreads, "one store a thread");
-  reinterpret_cast<uint16_t*>(sh.zeros)[threadIdx.x] = 0;
-  fence_proxy_async_smem();
+  SegmentView seg(reinterpret_cast<int32_t*>(dyn + kBuffers), p.E);
   grid_dependency_wait();
   grid_launch_dependents();
   load_segments<kThreads>(seg, p.offsets, p.E, p.rows, p.status);   // ends in a barrier
   if (!seg.ok) return;
-  // Neighbouring units go to different SMs: the padding that the last segment takes is one run,
-  // and an SM sends copies away at 22 bytes a clock at most.
-  const int warp = threadIdx.x >> 5;
-  const uint32_t units = p.token_units + static_cast<uint32_t>(p.row_tiles) * 4;   // below 2^32
-  int buf = 0;
-  for (uint32_t u = warp * gridDim.x + blockIdx.x; u < units; u += gridDim.x * kWarps) {
-    if (u < p.token_units) {
-      token_unit<kWeighted>(p, seg, sh.row[warp], u, buf);
-    } else {
-      pad_unit(p, seg, sh.zeros, u - p.token_units);
-      __syncwarp();
-      bulk_commit_group();
+  if (blockIdx.x < p.col_ctas) {
+    TileShared& sh = *reinterpret_cast<TileShared*>(dyn);
+    for (uint32_t item = blockIdx.x; item < p.tile_items; item += p.col_ctas)
+      tile_item<kWeighted>(p, seg, sh, item);
+  } else {
+    RowShared& sh = *reinterpret_cast<RowShared*>(dyn);
+    static_assert(kZeros == 2 * kThreads, "one store a thread");
+    reinterpret_cast<uint16_t*>(sh.zeros)[threadIdx.x] = 0;
+    fence_proxy_async_smem();
+    __syncthreads();
+    // Neighbouring units go to different SMs: the padding that the last segment takes is one run,
+    // and an SM sends copies away at 22 bytes a clock at most.
+    const int warp = threadIdx.x >> 5;
+    const uint32_t ctas = gridDim.x - p.col_ctas;
+    const uint32_t units = p.token_units + static_cast<uint32_t>(p.row_tiles) * 4;  // below 2^32
+    int buf = 0;
+    for (uint32_t u = warp * ctas + blockIdx.x - p.col_ctas; u < units; u += ctas * kWarps) {
+      if (u < p.token_units) {
+        token_unit<kWeighted>(p, seg, sh.row[warp], u, buf);
+      } else {
+        pad_unit(p, seg, sh.zeros, u - p.token_units);
+        __syncwarp();
+        bulk_commit_group();
+      }
     }
+    bulk_wait_read_all();
   }
-  bulk_wait_read_all();
-}
-
-template <bool kWeighted>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_col_kernel(const Params p) {
-  extern __shared__ __align__(16) uint8_t dyn[];
-  TileShared& sh = *reinterpret_cast<TileShared*>(dyn);
-  SegmentView seg(reinterpret_cast<int32_t*>(dyn + sizeof(TileShared)), p.E);
-  grid_dependency_wait();
-  grid_launch_dependents();
-  load_segments<kThreads>(seg, p.offsets, p.E, p.rows, p.status);
-  if (!seg.ok) return;
-  for (uint32_t item = blockIdx.x; item < p.tile_items; item += gridDim.x)
-    tile_item<kWeighted>(p, seg, sh, item);
 }
 
 // Both copies by tiles from one read of a tile, as the grouped quantizer makes them.
@@ -613,19 +614,25 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
 #ifndef TWO
 #define TWO 0
 #endif
-  // Both copies from one read of the tiles, or one after the other. Apart, each is made the way that
-  // suits it, which pays for large copies of tokens with several experts, unweighted: 8192 tokens of
-  // 2048 columns, 8 experts each, 100 us and 110 in one; 16384, 4 experts, 107 and 111; but 4096
-  // tokens, 8 experts, 65 and 65; 8192, 4 experts, 71 and 66; 16384 of 4096, 2 experts, 116 and 101;
-  // 256, 8 experts, 29 and 26.
-  const bool apart = a.top_k >= 4 && !a.weights && p.entries * a.cols >= int64_t{1} << 27;
-  if (a.row_out && a.col_out && !apart) {
+  auto apart = a.weights ? dispatch_apart_kernel<true> : dispatch_apart_kernel<false>;
+  auto dual = a.weights ? dispatch_dual_kernel<true> : dispatch_dual_kernel<false>;
+  const bool both = a.row_out && a.col_out;
+  // Both copies: from one read of the tiles where the row copy's own way saves no conversions (one or
+  // two experts a token, or weights) and there is much of it; else each its own way, side by side
+  // or, of very much, in turn, as the row copy's writes drive the tokens out of L2 that the column
+  // copy reads. Times, us, from one read, side by side, in turn (tokens x experts of each x columns):
+  //   37 x 8 x 2048: 19, 15, 22     256 x 8 x 2048: 25, 18, 29     1000 x 1 x 2048: 15, 13, -
+  //   4096 x 8 x 2048: 65, 57, 65   8192 x 8 x 2048: 109, 112, 99  8192 x 6 x 4096: 158, -, 150
+  //   16384 x 2 x 1024: 35, 41, -   16384 x 1 x 2048: 45, 53, 54   16384 x 2 x 4096: 101, 118, 116
+  //   512 x 8 x 2048 with weights: 31, 26, -        4096 x 8 x 2048 with weights: 76, 85, -
+  const int64_t values = p.entries * a.cols;
+  if (both && (a.top_k <= 2 || a.weights) && values >= int64_t{1} << 24) {
     const int64_t items = p.row_tiles * p.col_tiles;
     if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.tile_items = static_cast<uint32_t>(items);
-    return launch(a.weights ? dispatch_dual_kernel<true> : dispatch_dual_kernel<false>,
-                  std::min(most, items), sizeof(DualShared) + table, p, stream);
+    return launch(dual, std::min(most, items), sizeof(DualShared) + table, p, stream);
   }
+  int64_t row_ctas = 0, col_ctas = 0;
   if (a.row_out) {
     // parts of a row as long as the buffers take, while each warp keeps a unit
     p.part_cols = (a.weights ? 2 : 4) * kPiece;
@@ -635,19 +642,27 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
     if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.parts = static_cast<uint32_t>(parts);
     p.token_units = static_cast<uint32_t>(units);
-    const int64_t work = units + 4 * p.row_tiles;
-    const cudaError_t e = launch(a.weights ? dispatch_row_kernel<true> : dispatch_row_kernel<false>,
-                                 std::min(most, cdiv(work, kWarps)), sizeof(RowShared) + table, p, stream);
-    if (e != cudaSuccess || !a.col_out) return e;
+    row_ctas = std::min(most, cdiv(units + 4 * p.row_tiles, kWarps));
   }
-  // neighbouring tiles are joined into items while each CTA keeps four
-  const int64_t run = p.row_tiles * p.col_tiles / (4 * most);
-  p.run = static_cast<uint32_t>(run < 1 ? 1 : run > 8 ? 8 : run);
-  const int64_t items = p.row_tiles * cdiv(p.col_tiles, p.run);
-  if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  p.tile_items = static_cast<uint32_t>(items);
-  return launch(a.weights ? dispatch_col_kernel<true> : dispatch_col_kernel<false>, std::min(most, items),
-                sizeof(TileShared) + table, p, stream);
+  if (a.col_out) {   // neighbouring tiles are joined into items while each CTA keeps four
+    const int64_t run = p.row_tiles * p.col_tiles / (4 * most);
+    p.run = static_cast<uint32_t>(run < 1 ? 1 : run > 8 ? 8 : run);
+    const int64_t items = p.row_tiles * cdiv(p.col_tiles, p.run);
+    if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    p.tile_items = static_cast<uint32_t>(items);
+    col_ctas = std::min(most, items);
+  }
+  const size_t dyn = kBuffers + table;
+  if (both && values < int64_t{1} << 27) {   // side by side
+    col_ctas = std::min(col_ctas, most * 3 / 4);
+    row_ctas = std::min(row_ctas, most - most * 3 / 4);
+  } else if (both) {   // one after the other
+    const cudaError_t e = launch(apart, row_ctas, dyn, p, stream);
+    if (e != cudaSuccess) return e;
+    row_ctas = 0;
+  }
+  p.col_ctas = static_cast<uint32_t>(col_ctas);
+  return launch(apart, col_ctas + row_ctas, dyn, p, stream);
 }
 
 }  // namespace mxfp8

@@ -255,14 +255,18 @@ def test_quantize_dispatch(m, tokens, k, experts, cols, dropped, weighted):
 
 
 def test_quantize_dispatch_of_many_elements(m):
-    """2^27 elements and more, where both copies are made one after the other: against the grouped
-    quantizer on the dispatched rows."""
-    for tokens, k, cols in ((8192, 8, 2048), (5000, 7, 4096)):
+    """Each way that both copies are made, on either side of the sizes that choose between them:
+    against the grouped quantizer on the dispatched rows."""
+    for tokens, k, cols, weighted in ((8192, 8, 2048, False), (5000, 7, 4096, False),
+                                      (8191, 8, 2048, False), (4096, 2, 2048, False),
+                                      (4095, 2, 2048, False), (2048, 8, 1056, True),
+                                      (1000, 8, 1056, True), (16384, 1, 1024, False)):
         plan = m.route(choices(34, tokens, k, 64, 0.0).to(DEV), 64)
         x = torch.randn(tokens, cols, device=DEV).to(BF16)
         x[17, 100:200] = float("inf")
-        spread = m.dispatch(x, plan)
-        got = m.quantize_dispatch_dual(x, plan)
+        w = weights(35, tokens, k).to(DEV) if weighted else None
+        spread = m.dispatch(x, plan, w)
+        got = m.quantize_dispatch_dual(x, plan, w)
         want = m.quantize_grouped_dual(spread, plan.offsets)
         assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
         off = plan.offsets.cpu().numpy()
