@@ -300,11 +300,11 @@ __device__ __forceinline__ void load_patch(const Params& p, const PatchRows& row
 }
 
 // Eight codes of each of two columns (low and high halves) of eight rows, scaled by mul's halves.
-__device__ __forceinline__ void convert_pair(const uint32_t (&x)[8], uint32_t mul, uint2& o0,
+__device__ __forceinline__ void convert_pair(const Patch& t, int h, uint32_t mul, uint2& o0,
                                              uint2& o1) {
   uint32_t b[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = mul_bf16x2(x[i], mul);
+  for (int i = 0; i < 8; ++i) b[i] = mul_bf16x2(t.x[i][h], mul);
   const auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
   const auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
   o0.x = e4m3x4_f32(lo(b[0]), lo(b[1]), lo(b[2]), lo(b[3]));
@@ -314,14 +314,14 @@ __device__ __forceinline__ void convert_pair(const uint32_t (&x)[8], uint32_t mu
 }
 
 // The same where a block of the two columns holds a NaN or an infinity (scale byte 0xFF).
-__device__ __forceinline__ void convert_pair_nan(const uint32_t (&x)[8], uint32_t s0, uint32_t s1,
-                                                 uint2& o0, uint2& o1) {
+__device__ __forceinline__ void convert_pair_nan(const Patch& t, int h, uint32_t s0,
+                                                 uint32_t s1, uint2& o0, uint2& o1) {
   const float mul0 = inv_scale(s0), mul1 = inv_scale(s1);
   uint32_t lo[4], hi[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    lo[i] = __byte_perm(x[2 * i], x[2 * i + 1], 0x5410);
-    hi[i] = __byte_perm(x[2 * i], x[2 * i + 1], 0x7632);
+    lo[i] = __byte_perm(t.x[2 * i][h], t.x[2 * i + 1][h], 0x5410);
+    hi[i] = __byte_perm(t.x[2 * i][h], t.x[2 * i + 1][h], 0x7632);
   }
   o0.x = s0 == 0xFFu ? nan4(lo[0], lo[1]) : e4m3x4(lo[0], lo[1], mul0);
   o0.y = s0 == 0xFFu ? nan4(lo[2], lo[3]) : e4m3x4(lo[2], lo[3], mul0);
@@ -371,7 +371,7 @@ __device__ __forceinline__ void tile_item(const Params& p, const SegmentView& se
   if (rows_ok) load_patch(p, rows, bx0 * kTile + c, t);
   const int out_row = tid >> 3, chunk = tid & 7;   // a column of the tile, 16 rows of it
   uint8_t* out = p.col_codes + (bx0 * kTile + out_row) * p.rows + q.row0 + 16 * chunk;
-  const int64_t tile0 = p.col_tiles * q.seg_base + q.index;
+  const int64_t tile0 = p.col_tiles * q.seg_base + q.index, rows32 = 32 * p.rows;
   for (int64_t bx = bx0; bx < bx1; ++bx) {
     const int64_t col0 = bx * kTile;
     const int cols = static_cast<int>(p.cols - col0 < kTile ? p.cols - col0 : kTile);
@@ -406,40 +406,48 @@ __device__ __forceinline__ void tile_item(const Params& p, const SegmentView& se
     if (rows_ok) {
       const bool finite = worst < 0x7F800000u && (worst & 0xFFFFu) < 0x7F80u;
       uint8_t* stage = sh.stage + c * kTile + 8 * ((4 * block + sub) ^ (2 * vec));
+      // columns past the last are zeros, whose scale byte is 0 as it should be
+      const uint32_t e = (sub & 2 ? (sub & 1 ? exps[3] : exps[2]) : (sub & 1 ? exps[1] : exps[0])) -
+                         0x04000400u;
+      if (__builtin_expect(finite, 1)) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {   // columns c + 2h (low halves) and c + 2h + 1
-        uint32_t x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = t.x[i][h];
-        uint2 o0, o1;
-        if (__builtin_expect(finite, 1)) {
-          convert_pair(x, 0x83008300u - exps[h], o0, o1);
-        } else {
-          const uint32_t e0 = (exps[h] >> 7) & 0xFFu, e1 = exps[h] >> 23;
-          convert_pair_nan(x, e0 == 0xFFu ? 0xFFu : e0 - 8, e1 == 0xFFu ? 0xFFu : e1 - 8, o0, o1);
+        for (int h = 0; h < 4; ++h) {   // columns c + 2h (low halves) and c + 2h + 1
+          uint2 o0, o1;
+          convert_pair(t, h, 0x83008300u - exps[h], o0, o1);
+          *reinterpret_cast<uint2*>(stage + 2 * h * kTile) = o0;
+          *reinterpret_cast<uint2*>(stage + (2 * h + 1) * kTile) = o1;
         }
-        *reinterpret_cast<uint2*>(stage + 2 * h * kTile) = o0;
-        *reinterpret_cast<uint2*>(stage + (2 * h + 1) * kTile) = o1;
+        scale_to[0] = static_cast<uint8_t>(e >> 7);
+        scale_to[16] = static_cast<uint8_t>(e >> 23);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const uint32_t e0 = (exps[h] >> 7) & 0xFFu, e1 = exps[h] >> 23;
+          uint2 o0, o1;
+          convert_pair_nan(t, h, e0 == 0xFFu ? 0xFFu : e0 - 8, e1 == 0xFFu ? 0xFFu : e1 - 8, o0,
+                           o1);
+          *reinterpret_cast<uint2*>(stage + 2 * h * kTile) = o0;
+          *reinterpret_cast<uint2*>(stage + (2 * h + 1) * kTile) = o1;
+        }
+        scale_to[0] = static_cast<uint8_t>((e >> 7 & 0xFFu) == 0xF7u ? 0xFFu : e >> 7);
+        scale_to[16] = static_cast<uint8_t>(e >> 23 == 0xF7u ? 0xFFu : e >> 23);
       }
-      const uint32_t e = sub == 0 ? exps[0] : sub == 1 ? exps[1] : sub == 2 ? exps[2] : exps[3];
-      const uint32_t e0 = (e >> 7) & 0xFFu, e1 = e >> 23;
-      const bool valid = a < cols;    // cols % 8 == 0
-      scale_to[0] = static_cast<uint8_t>(!valid ? 0u : e0 == 0xFFu ? 0xFFu : e0 - 8);
-      scale_to[16] = static_cast<uint8_t>(!valid ? 0u : e1 == 0xFFu ? 0xFFu : e1 - 8);
     } else {
       scale_to[0] = scale_to[16] = 0;
     }
     if (rows_ok && bx + 1 < bx1) load_patch(p, rows, col0 + kTile + c, t);
     __syncthreads();
     if (16 * chunk < q.rows) {
+      const uint8_t* from = sh.stage + out_row * kTile;
+      uint8_t* to = out;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i, to += rows32) {
         if (out_row + 32 * i < cols)
-          *reinterpret_cast<uint4*>(out + 32 * i * p.rows) = *reinterpret_cast<const uint4*>(
-              sh.stage + (out_row + 32 * i) * kTile +
-              16 * (chunk ^ (((out_row + 32 * i) >> 3) & 7)));
+          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(
+              from + 32 * i * kTile + 16 * (chunk ^ (((out_row >> 3) + 4 * i) & 7)));
+      }
     }
-    out += kTile * p.rows;
+    out += 4 * rows32;
     if (tid < 32)
       reinterpret_cast<uint4*>(p.col_scales + (tile0 + bx * q.seg_tiles) * 512)[tid] =
           reinterpret_cast<const uint4*>(sh.scales)[tid];
