@@ -7,20 +7,20 @@
 // written: that saves a write of 2 bytes and a read of 2 for each element. Format and layouts as
 // in quantize.cu.
 //
-// The row copy alone goes by tokens, because what a token's row becomes row-wise does not depend
-// on the expert: a warp reads a part of a row, converts it once and sends the codes to all of the
-// token's rows. The column copy's blocks mix the tokens of a segment, so it goes by 128 x 128 tiles
-// of the segments, whose rows come out of L2 for all but a token's first expert. Both copies
-// together go so side by side or in turn, or from one read of the tiles as in the grouped
-// quantizer: see the launcher. CTAs are persistent and derive the segments from the offsets once.
+// The row copy goes by tokens, because what a token's row becomes row-wise does not depend on the
+// expert: a warp reads a part of a row, converts it once and sends the codes to all of the token's
+// rows. The column copy's blocks mix the tokens of a segment, so it goes by 128 x 128 tiles of the
+// segments, whose rows come out of L2 for all but a token's first expert. Both copies together go
+// so, side by side or in turn. CTAs are persistent and derive the segments from the offsets once.
 //
-// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 35 us, column copy 60,
-// both 99. What bounds them: the row copy the rate at which an SM sends bulk copies away (22 bytes
+// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 35 us, column copy 49,
+// both 85. What bounds them: the row copy the rate at which an SM sends bulk copies away (22 bytes
 // a clock) and the scattered scale words (6 us); the column copy 268 MB read from L2 (27 us of
-// it), the ALU pipe and the L1 path, each busy half of the time, and two barriers a tile.
-// Loads in flight need the L1 cache: tables sized by the experts, one stage buffer and four CTAs
-// an SM took 60 us where two buffers of 52 KB a CTA took 87, and both copies in five CTAs 116,
-// in six 148.
+// it), the ALU pipe and the L1 path, each busy half of the time, and two barriers a tile. What
+// counted most: results leave by lines that L2 evicts first, so that the tokens' rows stay in it
+// (column copy 58 us without), and loads in flight need the L1 cache, so that tables are sized by
+// the experts and a CTA holds one stage buffer (87 us with two buffers of 52 KB a CTA). One read of
+// a tile for both copies, as the grouped quantizer makes them, took 105 us.
 
 #include <algorithm>
 #include <cstdint>
@@ -31,12 +31,12 @@
 #include "internal.h"
 #include "mxfp8.h"
 #include "segments.cuh"
-#include "tile_passes.cuh"
 
 namespace mxfp8 {
 namespace {
 
-constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 128;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4;
 constexpr int kPiece = 512;   // columns a warp converts at once, 16 a lane
 constexpr int kZeros = 512;   // bytes of zeros that padding rows are copied from
@@ -167,7 +167,7 @@ __device__ __forceinline__ void token_unit(const Params& p, const SegmentView& s
   };
   const auto store = [&](int32_t row, int64_t scales_at) {
     bulk_store(p.row_codes + row * p.cols + c0, st.codes + buf * kPart,
-               static_cast<uint32_t>(cols));
+               static_cast<uint32_t>(cols), evict_first_policy());
     uint32_t* to = reinterpret_cast<uint32_t*>(p.row_scales) + scales_at + c0;
     for (int c = 0; c < cols; c += kTile)   // 128 words a tile of 128 columns
       to[c] = st.words[buf * (kPart / kTile) + c / kTile];
@@ -251,7 +251,8 @@ __device__ __forceinline__ void pad_unit(const Params& p, const SegmentView& seg
   if (r >= q.rows) return;
   for (int64_t c = 0; c < p.cols; c += kZeros)
     bulk_store(p.row_codes + row * p.cols + c, zeros,
-               static_cast<uint32_t>(p.cols - c < kZeros ? p.cols - c : kZeros));
+               static_cast<uint32_t>(p.cols - c < kZeros ? p.cols - c : kZeros),
+               evict_first_policy());
 }
 
 // Column copy of a run of 128 x 128 tiles beside one another. A thread holds 8 consecutive rows
@@ -271,7 +272,6 @@ struct PatchRows {
   uint32_t there;
   bool all;      // of the warp's rows
 };
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 __device__ __forceinline__ void load_patch(const Params& p, const PatchRows& rows, int64_t col,
                                            Patch& t) {
@@ -443,8 +443,9 @@ __device__ __forceinline__ void tile_item(const Params& p, const SegmentView& se
 #pragma unroll
       for (int i = 0; i < 4; ++i, to += rows32) {
         if (out_row + 32 * i < cols)
-          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(
-              from + 32 * i * kTile + 16 * (chunk ^ (((out_row >> 3) + 4 * i) & 7)));
+          __stcs(reinterpret_cast<uint4*>(to),   // 52 us, 58 with stores that stay in L2
+                 *reinterpret_cast<const uint4*>(
+                     from + 32 * i * kTile + 16 * (chunk ^ (((out_row >> 3) + 4 * i) & 7))));
       }
     }
     out += 4 * rows32;
@@ -457,7 +458,7 @@ __device__ __forceinline__ void tile_item(const Params& p, const SegmentView& se
 // The first col_ctas CTAs make the column copy, the others the row copy: either alone, or both side
 // by side, three to one, as the row copy waits for its writes and the column copy for its reads.
 template <bool kWeighted>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_apart_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_dispatch_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t dyn[];
   SegmentView seg(reinterpret_cast<int32_t*>(dyn + kBuffers), p.E);
   grid_dependency_wait();
@@ -490,87 +491,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_apart_kernel(co
       }
     }
     bulk_wait_read_all();
-  }
-}
-
-// Both copies by tiles from one read of a tile, as the grouped quantizer makes them.
-struct DualShared {
-  __align__(16) uint16_t tile[kTile][kTilePitch];
-  __align__(16) uint8_t scales_r[512];
-  __align__(16) uint8_t scales_c[512];
-  uint32_t at[kTile];   // of each row of the tile: its place in x in units of 8 values
-  float weight[kTile];
-};
-
-template <bool kWeighted>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) dispatch_dual_kernel(const Params p) {
-  extern __shared__ __align__(16) uint8_t dyn[];
-  DualShared& sh = *reinterpret_cast<DualShared*>(dyn);
-  SegmentView seg(reinterpret_cast<int32_t*>(dyn + sizeof(DualShared)), p.E);
-  grid_dependency_wait();
-  grid_launch_dependents();
-  load_segments<kThreads>(seg, p.offsets, p.E, p.rows, p.status);
-  if (!seg.ok) return;
-  const int t = threadIdx.x, v = t & 15, rsub = t >> 4;
-  const uint32_t row_tiles = static_cast<uint32_t>(p.row_tiles);
-  const QOut ro{p.row_codes, p.row_scales, 0}, co{p.col_codes, p.col_scales, 0};
-  for (uint32_t item = blockIdx.x; item < p.tile_items; item += gridDim.x) {
-    const uint32_t bx = item / row_tiles;
-    const int tile_row = static_cast<int>(item - bx * row_tiles);
-    if (tile_row >= seg.tile_base[p.E]) {   // no segment's: the tail of the scales
-      const int64_t at = (tile_row * p.col_tiles + bx) * 512;
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      if (t < 32) reinterpret_cast<uint4*>(p.row_scales + at)[t] = none;
-      if (t >= 32 && t < 64) reinterpret_cast<uint4*>(p.col_scales + at)[t - 32] = none;
-      continue;
-    }
-    const TileRow q = tile_row_of(seg, p.E, tile_row);
-    const int64_t col0 = static_cast<int64_t>(bx) * kTile;
-    const int cols = static_cast<int>(p.cols - col0 < kTile ? p.cols - col0 : kTile);
-    if (t < kTile) {
-      int32_t entry = t < q.rows ? p.entry_of[q.row0 + t] : -1;
-      if (entry >= p.entries) {   // a plan of other sizes
-        latch_error(p.status, MXFP8_ERR_BAD_OFFSETS);
-        entry = -1;
-      }
-      sh.at[t] = entry < 0 ? kNoRow
-                           : static_cast<uint32_t>(entry) / p.k * static_cast<uint32_t>(p.cols / 8);
-      if (kWeighted) sh.weight[t] = entry < 0 ? 0.f : p.weights[entry];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = rsub + 16 * j;
-      const uint32_t at = sh.at[r];
-      const bool ok = 8 * v < cols && at != kNoRow;
-      cp_async16(&sh.tile[r][8 * v],
-                 ok ? p.src + static_cast<uint64_t>(at) * 8 + col0 + 8 * v : p.src, ok);
-    }
-    cp_async_wait_all();
-    if constexpr (kWeighted) {   // each thread on the vectors that it copied itself
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = rsub + 16 * j;
-        uint4* at = reinterpret_cast<uint4*>(&sh.tile[r][8 * v]);
-        const uint4 x = *at;
-        const float w = sh.weight[r];
-        *at = make_uint4(weigh(x.x, w), weigh(x.y, w), weigh(x.z, w), weigh(x.w, w));
-      }
-    }
-    __syncthreads();
-    row_pass_smem<true>(sh.tile, sh.scales_r, ro, p.cols, q.row0, q.rows, col0, cols,
-                        MXFP8_RULE_FLOOR);
-    col_pass_smem<true>(sh.tile, sh.scales_c, co, p.rows, q.row0, q.rows, col0, cols,
-                        MXFP8_RULE_FLOOR);
-    __syncthreads();
-    if (t < 32)
-      reinterpret_cast<uint4*>(p.row_scales + (tile_row * p.col_tiles + bx) * 512)[t] =
-          reinterpret_cast<const uint4*>(sh.scales_r)[t];
-    if (t >= 32 && t < 64)
-      reinterpret_cast<uint4*>(p.col_scales +
-                               (p.col_tiles * q.seg_base + bx * q.seg_tiles + q.index) *
-                                   512)[t - 32] =
-          reinterpret_cast<const uint4*>(sh.scales_c)[t - 32];
   }
 }
 
@@ -622,24 +542,7 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
 #ifndef TWO
 #define TWO 0
 #endif
-  auto apart = a.weights ? dispatch_apart_kernel<true> : dispatch_apart_kernel<false>;
-  auto dual = a.weights ? dispatch_dual_kernel<true> : dispatch_dual_kernel<false>;
-  const bool both = a.row_out && a.col_out;
-  // Both copies: from one read of the tiles where the row copy's own way saves no conversions (one or
-  // two experts a token, or weights) and there is much of it; else each its own way, side by side
-  // or, of very much, in turn, as the row copy's writes drive the tokens out of L2 that the column
-  // copy reads. Times, us, from one read, side by side, in turn (tokens x experts of each x columns):
-  //   37 x 8 x 2048: 19, 15, 22     256 x 8 x 2048: 25, 18, 29     1000 x 1 x 2048: 15, 13, -
-  //   4096 x 8 x 2048: 65, 57, 65   8192 x 8 x 2048: 109, 112, 99  8192 x 6 x 4096: 158, -, 150
-  //   16384 x 2 x 1024: 35, 41, -   16384 x 1 x 2048: 45, 53, 54   16384 x 2 x 4096: 101, 118, 116
-  //   512 x 8 x 2048 with weights: 31, 26, -        4096 x 8 x 2048 with weights: 76, 85, -
-  const int64_t values = p.entries * a.cols;
-  if (both && (a.top_k <= 2 || a.weights) && values >= int64_t{1} << 24) {
-    const int64_t items = p.row_tiles * p.col_tiles;
-    if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    p.tile_items = static_cast<uint32_t>(items);
-    return launch(dual, std::min(most, items), sizeof(DualShared) + table, p, stream);
-  }
+  auto k = a.weights ? quantize_dispatch_kernel<true> : quantize_dispatch_kernel<false>;
   int64_t row_ctas = 0, col_ctas = 0;
   if (a.row_out) {
     // parts of a row as long as the buffers take, while each warp keeps a unit
@@ -652,8 +555,8 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
     p.token_units = static_cast<uint32_t>(units);
     row_ctas = std::min(most, cdiv(units + 4 * p.row_tiles, kWarps));
   }
-  if (a.col_out) {   // neighbouring tiles are joined into items while each CTA keeps four
-    const int64_t run = p.row_tiles * p.col_tiles / (4 * most);
+  if (a.col_out) {   // neighbouring tiles are joined into items while each CTA keeps two
+    const int64_t run = p.row_tiles * p.col_tiles / (2 * most);
     p.run = static_cast<uint32_t>(run < 1 ? 1 : run > 8 ? 8 : run);
     const int64_t items = p.row_tiles * cdiv(p.col_tiles, p.run);
     if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
@@ -661,16 +564,25 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
     col_ctas = std::min(most, items);
   }
   const size_t dyn = kBuffers + table;
-  if (both && values < int64_t{1} << 27) {   // side by side
-    col_ctas = std::min(col_ctas, most * 3 / 4);
-    row_ctas = std::min(row_ctas, most - most * 3 / 4);
-  } else if (both) {   // one after the other
-    const cudaError_t e = launch(apart, row_ctas, dyn, p, stream);
-    if (e != cudaSuccess) return e;
-    row_ctas = 0;
+  // Both copies side by side, or in turn where there is much of them: the row copy's warps, a
+  // quarter of all, would be last, sooner with few experts a token or with weights, as they
+  // convert more for what they write. Times, us, side by side and in turn (tokens x experts of each x
+  // columns): 37 x 8 x 2048: 13, 23; 4096 x 8 x 2048: 51, 55; 8192 x 8 x 2048: 91, 85; 8192 x 6 x
+  // 4096: 140, 131; 2000 x 2 x 4096: 30, 34; 16384 x 2 x 1024: 40, 33; 16384 x 1 x 2048: 52, 49;
+  // 1024 x 8 x 2048 with weights: 36, 34; 4096 x 8 x 2048 with weights: 88, 73.
+  const int64_t much = int64_t{1} << (a.weights ? 23 : a.top_k <= 2 ? 25 : 27);
+  if (a.row_out && a.col_out) {
+    if (p.entries * a.cols < much) {
+      col_ctas = std::min(col_ctas, most * 3 / 4);
+      row_ctas = std::min(row_ctas, most - most * 3 / 4);
+    } else {
+      const cudaError_t e = launch(k, row_ctas, dyn, p, stream);
+      if (e != cudaSuccess) return e;
+      row_ctas = 0;
+    }
   }
   p.col_ctas = static_cast<uint32_t>(col_ctas);
-  return launch(apart, col_ctas + row_ctas, dyn, p, stream);
+  return launch(k, col_ctas + row_ctas, dyn, p, stream);
 }
 
 }  // namespace mxfp8
