@@ -606,8 +606,8 @@ int mxfp8_route(const int64_t* ids_dev, int64_t tokens, int top_k, int num_exper
  *   weights_dev  float [tokens][top_k], or NULL for 1 (the values then move unchanged). Products
  *                are FP32, rounded once.
  *   out_dev      [total_rows][cols], of x's type, written in full; may not overlap x
- * Any cols; the fast path needs rows of a multiple of 16 bytes. x and out start on 16 bytes.
- * A plan whose rows do not fit total_rows is not followed there: MXFP8_ERR_BAD_OFFSETS is latched
+ * Up to 2097120 cols (65535 * 32); rows of a multiple of 16 bytes are the fastest, of an odd
+ * number of BF16 values the slowest. x and out start on 16 bytes. A plan whose rows do not fit total_rows is not followed there: MXFP8_ERR_BAD_OFFSETS is latched
  * and the row skipped.
  */
 int mxfp8_dispatch(const void* x_dev, int dtype, int64_t tokens, int64_t cols, int top_k,

@@ -7,6 +7,10 @@ rounds a partial sum that is at most sum |w y|, so FP32 is off by at most (k + 1
 BF16 results add half a step, 2^-8 of the result. A weight's gradient is a sum of `cols`
 products: a thread adds at most cols / 128 + 128 of them, then at most 16 joins follow:
 (cols / 128 + 144) 2^-24 sum |g y|."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -54,7 +58,8 @@ def check_plan(m, ids, experts, rows=None):
     (0, 2, 4, 0.0), (1, 1, 1, 0.0), (1, 8, 128, 0.0), (1, 8, 128, 1.0), (5, 3, 2, 0.3),
     (37, 8, 128, 0.0), (33, 1, 1024, 0.1), (509, 6, 60, 0.1), (700, 6, 1000, 0.0),
     (1021, 8, 8, 0.5), (4096, 2, 16, 0.0), (4099, 4, 256, 0.2), (8192, 8, 128, 0.0),
-    (30011, 7, 1024, 0.1), (131072, 8, 64, 0.0), (16400, 8, 100, 0.0)]
+    (30011, 7, 1024, 0.1), (131072, 8, 64, 0.0), (16400, 8, 100, 0.0),
+    (150001, 8, 1000, 0.1)]
     # every size of the kernel's shared memory: runs of 32 to 512 entries a warp
     + [(8 * 32 * 32 * n // 4, 4, e, 0.02) for n in range(1, 34) for e in (16, 130)])
 def test_route(m, tokens, k, experts, dropped):
@@ -364,8 +369,8 @@ def test_no_tokens(m):
     assert not no_cols[1].any()
 
 
-def test_captured_and_replayed_on_new_choices(m):
-    tokens, k, experts, cols = 300, 4, 12, 160
+@pytest.mark.parametrize("tokens,k,experts,cols", [(300, 4, 12, 160), (9000, 8, 128, 64)])
+def test_captured_and_replayed_on_new_choices(m, tokens, k, experts, cols):
     ids = choices(25, tokens, k, experts).to(DEV)
     x, w = values(26, tokens, cols, BF16).to(DEV), weights(27, tokens, k).to(DEV)
 
@@ -392,6 +397,44 @@ def test_captured_and_replayed_on_new_choices(m):
         torch.cuda.synchronize()
         for a, b in zip(held, step()):
             assert torch.equal(a, b)
+
+
+def test_launches_back_to_back_keep_their_order(m):
+    """Each launch reads what the one before wrote, and overwrites what the one before read, with no
+    host synchronization between; and again without programmatic launches, in a child process."""
+    tokens, k, experts, cols = 2000, 4, 12, 96
+    ids = [choices(40 + i, tokens, k, experts, 0.1).to(DEV) for i in range(4)]
+    w = weights(44, tokens, k).to(DEV)
+    x0 = values(45, tokens, cols, BF16).to(DEV)
+
+    def chain(wait):
+        x, sums = x0.clone(), []
+        rows = R.rows_for(tokens, k, experts)
+        y = torch.empty(rows, cols, dtype=BF16, device=DEV)
+        for i in range(12):
+            plan = m.route(ids[i % 4], experts)
+            wait()
+            m.dispatch(x, plan, w, out=y)
+            wait()
+            sums.append(m.quantize_dispatch_dual(x, plan)[0].clone())
+            wait()
+            m.combine(y, plan, w, out=x)
+            wait()
+            m.combine_backward(x, y, plan, w, out=y)
+            wait()
+            m.combine(y, plan, out=x)
+            wait()
+        return [x] + sums
+
+    for a, b in zip(chain(lambda: None), chain(torch.cuda.synchronize)):
+        assert torch.equal(a, b)
+
+
+def test_without_programmatic_launches():
+    r = subprocess.run(
+        [sys.executable, "-m", "pytest", "-q", "-x", __file__, "-k", "order or captured or another"],
+        env=dict(os.environ, MXFP8_PDL="0"), capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:]
 
 
 def test_on_another_stream(m):

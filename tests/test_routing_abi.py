@@ -61,6 +61,7 @@ def test_dispatch(lib):
     for kw in (dict(x=HALF), dict(w=ODD), dict(row_of=ODD), dict(entry_of=ODD), dict(rows=40),
                dict(out=HALF)):
         assert call(**kw) == m.ERR_ALIGNMENT, kw
+    assert call(cols=65535 * 32 + 1) == m.ERR_INVALID_ARG
     assert call(rows=0, out=None, entry_of=None) == m.OK
     assert call(cols=0, x=None, out=None) == m.OK
 
