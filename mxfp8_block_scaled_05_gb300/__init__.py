@@ -741,38 +741,37 @@ def _here(stream):
     return _raw_stream(_device()) if stream is None else stream.cuda_stream
 
 
-def _plan(plan: RoutePlan, weights):
-    """A plan's rows, and the weights beside them, checked: all that is right in one expression, as
-    a call of a few tokens takes as long in here as on the GPU. Returns (tokens, top_k, rows)."""
-    row_of, entry_of = plan.row_of, plan.entry_of
-    if not (row_of.is_cuda and row_of.dtype is _INT32 is entry_of.dtype
-            and row_of.get_device() == _device() == entry_of.get_device()
-            and row_of.is_contiguous() and entry_of.is_contiguous()):
-        _require(row_of, _INT32, "plan.row_of")
-        _require(entry_of, _INT32, "plan.entry_of")
-    shape = row_of.shape
-    if len(shape) != 2 or shape[1] < 1:
-        raise ValueError(f"plan.row_of must be [tokens, top_k], got {tuple(shape)}")
-    if weights is not None:
-        _require(weights, _FP32, "weights")
-        if weights.shape != shape:
-            raise ValueError(f"weights are {tuple(weights.shape)}; the plan is of {tuple(shape)}")
-    return *shape, entry_of.numel()
-
-
-def _rows(t: torch.Tensor, rows: Optional[int], name: str):
-    """Rows of the plan's tokens or segments: 2-D, BF16 or FP32. Returns (dtype, its code,
-    columns)."""
-    dt = t.dtype
-    if dt is not _BF16 and dt is not _FP32:
-        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {dt}")
-    _require(t, dt, name)
+def _plan_refused(t, plan: RoutePlan, weights, name: str):
+    """Says what is wrong with a call on a plan."""
+    if t.dtype not in (_BF16, _FP32):
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    _require(t, t.dtype, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
-    n, cols = t.shape
-    if n != rows:
-        raise ValueError(f"{name} has {n} rows; the plan has {rows}")
-    return dt, OUT_BF16 if dt is _BF16 else OUT_FP32, cols
+    _require(plan.row_of, _INT32, "plan.row_of")
+    _require(plan.entry_of, _INT32, "plan.entry_of")
+    if plan.row_of.dim() != 2 or plan.row_of.shape[1] < 1:
+        raise ValueError(f"plan.row_of must be [tokens, top_k], got {tuple(plan.row_of.shape)}")
+    _require(weights, _FP32, "weights")
+    raise ValueError(f"weights are {tuple(weights.shape)}; the plan is of "
+                     f"{tuple(plan.row_of.shape)}")
+
+
+def _planned(t, plan: RoutePlan, weights, name: str):
+    """Rows `t` of tokens or of segments, the plan and the weights beside it, checked: what is right
+    passes in two expressions, as a call of a few tokens takes longer in here than on the GPU.
+    Returns (tokens, top_k, rows, t's rows, its columns, its dtype)."""
+    row_of, entry_of = plan.row_of, plan.entry_of
+    dt, dev, of = t.dtype, t.get_device(), row_of.shape
+    if not ((dt is _BF16 or dt is _FP32) and row_of.dtype is _INT32 is entry_of.dtype
+            and dev >= 0 and dev == _device() == row_of.get_device() == entry_of.get_device()
+            and t.is_contiguous() and row_of.is_contiguous() and entry_of.is_contiguous()
+            and len(of) == 2 and of[1] > 0 and t.dim() == 2) or (
+            weights is not None and not (
+                weights.dtype is _FP32 and weights.get_device() == dev
+                and weights.is_contiguous() and weights.shape == of)):
+        _plan_refused(t, plan, weights, name)
+    return *of, entry_of.numel(), *t.shape, dt
 
 
 def _optional(t):
@@ -784,15 +783,17 @@ def dispatch(x: torch.Tensor, plan: RoutePlan, weights: Optional[torch.Tensor] =
     """The tokens' rows x (BF16 or FP32 [tokens, cols]) in the plan's segments, [rows, cols]: row
     r holds its entry's token, times that entry's weight (float32 [tokens, top_k]) if given;
     padding rows are zero. The gradient of x without weights is combine(grad, plan)."""
-    tokens, top_k, rows = _plan(plan, weights)
-    dt, code, cols = _rows(x, tokens, "x")
+    tokens, top_k, rows, n, cols, dt = _planned(x, plan, weights, "x")
+    if n != tokens:
+        raise ValueError(f"x has {n} rows; the plan is of {tokens} tokens")
     if out is None:
         out = _new((rows, cols), dt, x.device, stream)
     else:
         _buffer(out, dt, rows * cols, "out")
-    _check(lib().mxfp8_dispatch(_ptr(x), code, tokens, cols, top_k, _optional(weights),
-                                _ptr(plan.row_of), _ptr(plan.entry_of), rows, _ptr(out),
-                                _here(stream)), "mxfp8_dispatch")
+    _check(lib().mxfp8_dispatch(x.data_ptr(), OUT_BF16 if dt is _BF16 else OUT_FP32, tokens, cols,
+                                top_k, _optional(weights), plan.row_of.data_ptr(),
+                                plan.entry_of.data_ptr(), rows, out.data_ptr(), _here(stream)),
+           "mxfp8_dispatch")
     return out
 
 
@@ -802,9 +803,8 @@ def _dispatch_copy(rows, cols, experts, axis, codes, scales, device, stream):
     if need == 0 and cols:   # cols not a multiple of 32, or sizes that do not fit: as the call says
         _check(ERR_ALIGNMENT if axis == ROW and cols % 32 else ERR_INVALID_ARG,
                "mxfp8_quantize_dispatch")
-    shape = (rows, cols) if axis == ROW else (cols, rows)
     if codes is None:
-        codes = _new(shape, torch.uint8, device, stream)
+        codes = _new((rows, cols) if axis == ROW else (cols, rows), torch.uint8, device, stream)
     else:
         _buffer(codes, torch.uint8, rows * cols, "codes")
     if scales is None:
@@ -816,11 +816,14 @@ def _dispatch_copy(rows, cols, experts, axis, codes, scales, device, stream):
 
 def _dispatch_source(x, plan, weights):
     """Checks quantize_dispatch's inputs. Returns (tokens, top_k, rows, cols, experts)."""
-    _require(x, torch.bfloat16, "x")
-    _require(plan.offsets, torch.int32, "plan.offsets")
-    tokens, top_k, rows = _plan(plan, weights)
-    cols = _rows(x, tokens, "x")[2]
-    return tokens, top_k, rows, cols, plan.offsets.shape.numel() - 1
+    tokens, top_k, rows, n, cols, dt = _planned(x, plan, weights, "x")
+    if n != tokens:
+        raise ValueError(f"x has {n} rows; the plan is of {tokens} tokens")
+    if dt is not _BF16:
+        raise ValueError(f"x must be torch.bfloat16, got {dt}")
+    offsets = plan.offsets
+    _require(offsets, _INT32, "plan.offsets")
+    return tokens, top_k, rows, cols, offsets.numel() - 1
 
 
 def quantize_dispatch(x: torch.Tensor, plan: RoutePlan, axis: int = ROW,
@@ -832,13 +835,12 @@ def quantize_dispatch(x: torch.Tensor, plan: RoutePlan, axis: int = ROW,
         raise ValueError(f"axis must be ROW or COL, got {axis}")
     tokens, top_k, rows, cols, e = _dispatch_source(x, plan, weights)
     codes, scales = _dispatch_copy(rows, cols, e, axis, out, scales, x.device, stream)
-    a, b = _ptr(codes), _ptr(scales)
-    _check(lib().mxfp8_quantize_dispatch(_ptr(x), tokens, cols, top_k, _optional(weights),
-                                         _ptr(plan.row_of), _ptr(plan.entry_of), rows,
-                                         _ptr(plan.offsets), e,
-                                         *((a, b, None, None) if axis == ROW else
-                                           (None, None, a, b)), _here(stream)),
-           "mxfp8_quantize_dispatch")
+    a, b = codes.data_ptr(), scales.data_ptr()
+    ra, rb, ca, cb = (a, b, None, None) if axis == ROW else (None, None, a, b)
+    _check(lib().mxfp8_quantize_dispatch(x.data_ptr(), tokens, cols, top_k, _optional(weights),
+                                         plan.row_of.data_ptr(), plan.entry_of.data_ptr(), rows,
+                                         plan.offsets.data_ptr(), e, ra, rb, ca, cb,
+                                         _here(stream)), "mxfp8_quantize_dispatch")
     return codes, scales
 
 
@@ -851,11 +853,11 @@ def quantize_dispatch_dual(x: torch.Tensor, plan: RoutePlan,
     tokens, top_k, rows, cols, e = _dispatch_source(x, plan, weights)
     row = _dispatch_copy(rows, cols, e, ROW, row_out, row_scales, x.device, stream)
     col = _dispatch_copy(rows, cols, e, COL, col_out, col_scales, x.device, stream)
-    _check(lib().mxfp8_quantize_dispatch(_ptr(x), tokens, cols, top_k, _optional(weights),
-                                         _ptr(plan.row_of), _ptr(plan.entry_of), rows,
-                                         _ptr(plan.offsets), e, _ptr(row[0]), _ptr(row[1]),
-                                         _ptr(col[0]), _ptr(col[1]), _here(stream)),
-           "mxfp8_quantize_dispatch")
+    _check(lib().mxfp8_quantize_dispatch(x.data_ptr(), tokens, cols, top_k, _optional(weights),
+                                         plan.row_of.data_ptr(), plan.entry_of.data_ptr(), rows,
+                                         plan.offsets.data_ptr(), e, row[0].data_ptr(),
+                                         row[1].data_ptr(), col[0].data_ptr(), col[1].data_ptr(),
+                                         _here(stream)), "mxfp8_quantize_dispatch")
     return row + col
 
 
@@ -864,14 +866,16 @@ def combine(y: torch.Tensor, plan: RoutePlan, weights: Optional[torch.Tensor] = 
     """The sum of each token's segment rows y (BF16 or FP32 [rows, cols]), weighted (float32
     [tokens, top_k]) if weights are given, [tokens, cols] of y's type: FP32 sums in the order of
     the choices, rounded once. A token without rows gets zeros."""
-    tokens, top_k, rows = _plan(plan, weights)
-    dt, code, cols = _rows(y, rows, "y")
+    tokens, top_k, rows, n, cols, dt = _planned(y, plan, weights, "y")
+    if n != rows:
+        raise ValueError(f"y has {n} rows; the plan has {rows}")
     if out is None:
         out = _new((tokens, cols), dt, y.device, stream)
     else:
         _buffer(out, dt, tokens * cols, "out")
-    _check(lib().mxfp8_combine(_ptr(y), code, rows, cols, tokens, top_k, _optional(weights),
-                               _ptr(plan.row_of), _ptr(out), _here(stream)), "mxfp8_combine")
+    _check(lib().mxfp8_combine(y.data_ptr(), OUT_BF16 if dt is _BF16 else OUT_FP32, rows, cols,
+                               tokens, top_k, _optional(weights), plan.row_of.data_ptr(),
+                               out.data_ptr(), _here(stream)), "mxfp8_combine")
     return out
 
 
@@ -883,8 +887,9 @@ def combine_backward(grad_out: torch.Tensor, y: torch.Tensor, plan: RoutePlan,
     quantize_dispatch_dual(grad_out, plan, weights) gives it as the grouped GEMMs read it."""
     if weights is None:
         raise ValueError("weights are needed; without them grad_y is dispatch(grad_out, plan)")
-    tokens, top_k, rows = _plan(plan, weights)
-    dt, code, cols = _rows(y, rows, "y")
+    tokens, top_k, rows, n, cols, dt = _planned(y, plan, weights, "y")
+    if n != rows:
+        raise ValueError(f"y has {n} rows; the plan has {rows}")
     _require(grad_out, dt, "grad_out")
     if grad_out.shape != (tokens, cols):
         raise ValueError(f"grad_out must be {(tokens, cols)}, got {tuple(grad_out.shape)}")
@@ -899,10 +904,12 @@ def combine_backward(grad_out: torch.Tensor, y: torch.Tensor, plan: RoutePlan,
         out_weights = _new((tokens, top_k), torch.float32, y.device, stream)
     else:
         _buffer(out_weights, torch.float32, tokens * top_k, "out_weights")
-    _check(lib().mxfp8_combine_backward(_ptr(grad_out), _ptr(y), code, tokens, cols, top_k,
-                                        _ptr(weights), _ptr(plan.row_of), _ptr(plan.entry_of),
-                                        rows, _optional(out), _ptr(out_weights),
-                                        _here(stream)), "mxfp8_combine_backward")
+    _check(lib().mxfp8_combine_backward(grad_out.data_ptr(), y.data_ptr(),
+                                        OUT_BF16 if dt is _BF16 else OUT_FP32, tokens, cols,
+                                        top_k, weights.data_ptr(), plan.row_of.data_ptr(),
+                                        plan.entry_of.data_ptr(), rows, _optional(out),
+                                        out_weights.data_ptr(), _here(stream)),
+           "mxfp8_combine_backward")
     return out, out_weights
 
 
@@ -921,11 +928,11 @@ def swiglu(gate_up: torch.Tensor, checkpoint: bool = True, rule: int = RULE_CEIL
     gate_up kept in MXFP8 for swiglu_backward: quantize(gate_up, ROW, LINEAR, rule=rule) byte for
     byte, from the same read. checkpoint=False keeps nothing."""
     _require(gate_up, torch.bfloat16, "gate_up")
-    if gate_up.dim() != 2 or gate_up.shape[1] % 64:
+    shape = gate_up.shape
+    if len(shape) != 2 or shape[1] % 64:
         raise ValueError(f"gate_up must be [rows, 2 * width], width a multiple of 32, got "
                          f"{tuple(gate_up.shape)}")
-    rows, width = gate_up.shape[0], gate_up.shape[1] // 2
-    dev = gate_up.device
+    rows, width, dev = shape[0], shape[1] // 2, gate_up.device
     if out is None:
         out = _new((rows, width), torch.bfloat16, dev, stream)
     else:
