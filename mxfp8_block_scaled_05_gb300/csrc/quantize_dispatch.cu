@@ -13,16 +13,18 @@
 // segments, whose rows come out of L2 for all but a token's first expert. Both copies together go
 // so, side by side or in turn. CTAs are persistent and derive the segments from the offsets once.
 //
-// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 35 us, column copy 49,
-// both 85. What bounds them: the row copy the rate at which an SM sends bulk copies away (22 bytes
-// a clock) and the scattered scale words (6 us); the column copy 268 MB read from L2 (27 us of
-// it), the ALU pipe and the L1 path, each busy half of the time, and two barriers a tile. What
-// counted most: results leave by lines that L2 evicts first, so that the tokens' rows stay in it
-// (column copy 58 us without), and loads in flight need the L1 cache, so that tables are sized by
-// the experts and a CTA holds one stage buffer (87 us with two buffers of 52 KB a CTA). One read of
-// a tile for both copies, as the grouped quantizer makes them, took 105 us.
+// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 33 us, column copy 50,
+// both 85 (with weights 57, 62 and 118). What bounds them: the row copy the rate at which an SM
+// sends bulk copies away (22 bytes a clock) and the scattered scale words (6 us); the column copy
+// 268 MB read from L2 (27 us of it), the ALU pipe and the L1 path, each busy half of the time, and
+// two barriers a tile. What counted most: results leave by lines that L2 evicts first, so that the
+// tokens' rows stay in it (column copy 58 us without), and loads in flight need the L1 cache, so
+// that tables are sized by the experts and a CTA holds one stage buffer (87 us with two buffers of
+// 52 KB a CTA). One read of a tile for both copies, as the grouped quantizer makes them, took 105
+// us.
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -260,7 +262,8 @@ __device__ __forceinline__ void pad_unit(const Params& p, const SegmentView& seg
 // two values at once, here from two rows, which leaves a column's 8 codes in 8 consecutive bytes.
 // They pass through shared memory (8-byte units, their index XORed with twice the column's
 // eighth, so that both the writes and the reads of 16 bytes are free of bank conflicts) and leave
-// as rows of 128 bytes; the next tile's loads are in flight meanwhile.
+// as rows of 128 bytes; the next tile's loads are in flight meanwhile. A warp that keeps 16 rows of 4
+// columns a thread needs neither the stage nor a barrier, but its stores of 32 bytes took 77 us.
 struct Patch {
   uint32_t x[8][4];
 };
@@ -443,7 +446,7 @@ __device__ __forceinline__ void tile_item(const Params& p, const SegmentView& se
 #pragma unroll
       for (int i = 0; i < 4; ++i, to += rows32) {
         if (out_row + 32 * i < cols)
-          __stcs(reinterpret_cast<uint4*>(to),   // 52 us, 58 with stores that stay in L2
+          __stcs(reinterpret_cast<uint4*>(to),   // 50 us, 58 with stores that stay in L2
                  *reinterpret_cast<const uint4*>(
                      from + 32 * i * kTile + 16 * (chunk ^ (((out_row >> 3) + 4 * i) & 7))));
       }
@@ -456,7 +459,7 @@ __device__ __forceinline__ void tile_item(const Params& p, const SegmentView& se
 }
 
 // The first col_ctas CTAs make the column copy, the others the row copy: either alone, or both side
-// by side, three to one, as the row copy waits for its writes and the column copy for its reads.
+// by side, as the row copy waits for its writes and the column copy for its reads.
 template <bool kWeighted>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_dispatch_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -539,9 +542,6 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
   p.status = a.status;
   const int64_t most = int64_t{kCtasPerSm} * num_sms();   // CTAs
   const size_t table = sizeof(int32_t) * SegmentView::words(p.E);
-#ifndef TWO
-#define TWO 0
-#endif
   auto k = a.weights ? quantize_dispatch_kernel<true> : quantize_dispatch_kernel<false>;
   int64_t row_ctas = 0, col_ctas = 0;
   if (a.row_out) {
@@ -564,17 +564,24 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
     col_ctas = std::min(most, items);
   }
   const size_t dyn = kBuffers + table;
-  // Both copies side by side, or in turn where there is much of them: the row copy's warps, a
-  // quarter of all, would be last, sooner with few experts a token or with weights, as they
-  // convert more for what they write. Times, us, side by side and in turn (tokens x experts of each x
-  // columns): 37 x 8 x 2048: 13, 23; 4096 x 8 x 2048: 51, 55; 8192 x 8 x 2048: 91, 85; 8192 x 6 x
-  // 4096: 140, 131; 2000 x 2 x 4096: 30, 34; 16384 x 2 x 1024: 40, 33; 16384 x 1 x 2048: 52, 49;
-  // 1024 x 8 x 2048 with weights: 36, 34; 4096 x 8 x 2048 with weights: 88, 73.
-  const int64_t much = int64_t{1} << (a.weights ? 23 : a.top_k <= 2 ? 25 : 27);
+  // Both copies side by side, in shares of the CTAs after what each copy costs: ns for 1024
+  // values, fitted to each alone (a token converts once, with weights once an expert, and goes out
+  // once an expert; a segment's last tile costs as much as a full one). Shares go by eighths, so
+  // that the SMs hold like mixtures: a share of 28% in place of 25 or 37 costs up to 7%. Where
+  // there is much, the copies go in turn, as the tokens' rows leave L2 sooner with both at work.
+  // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 13, 23;
+  // 4096 x 8 x 2048: 49, 55; 8192 x 8 x 2048: 85, 86; 16384 x 8 x 2048: 172, 166; 16384 x 8 x
+  // 7168: 743, 650; 16384 x 4 x 4096: 189, 180; 16384 x 2 x 4096: 104, 124; 16384 x 1 x 2048: 44,
+  // 49; with weights 1024 x 8 x 2048: 32, 34; 8192 x 8 x 2048: 118, 120; 16384 x 4 x 4096: 237, 228.
   if (a.row_out && a.col_out) {
-    if (p.entries * a.cols < much) {
-      col_ctas = std::min(col_ctas, most * 3 / 4);
-      row_ctas = std::min(row_ctas, most - most * 3 / 4);
+    if (p.entries * a.cols < int64_t{1} << 28) {
+      const double x = static_cast<double>(a.tokens), y = static_cast<double>(p.entries);
+      const double pad = static_cast<double>(std::max<int64_t>(a.rows - p.entries, 0));
+      const double row = (a.weights ? 0.58 * x + 0.44 * y : 0.37 * x + 0.21 * y) + 0.12 * pad;
+      const double col = 0.35 * x + (a.weights ? 0.36 : 0.28) * (a.rows + 0.5 * kTile * p.E);
+      const int64_t eighths = std::max<int64_t>(2, std::llround(8 * row / (row + col)));
+      row_ctas = std::min(row_ctas, most * eighths / 8);
+      col_ctas = std::min(col_ctas, most - row_ctas);
     } else {
       const cudaError_t e = launch(k, row_ctas, dyn, p, stream);
       if (e != cudaSuccess) return e;

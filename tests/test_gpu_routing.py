@@ -281,6 +281,21 @@ def test_quantize_dispatch_of_many_elements(m):
             assert not a[tiles * per * 512:].any()
 
 
+@pytest.mark.parametrize("tokens,k,cols,experts,weighted", [
+    (1024, 8, 2048, 128, False), (4096, 8, 2048, 128, False), (16384, 2, 1024, 64, False),
+    (4096, 2, 4096, 8, True), (16384, 1, 5120, 16, True), (16384, 4, 4096, 32, False),
+    (16383, 4, 4096, 32, True), (8192, 8, 4096, 3, True)])
+def test_quantize_dispatch_shares(m, tokens, k, cols, experts, weighted):
+    """Both copies in any share of the CTAs, and in turn, are the bytes of each alone."""
+    plan = m.route(choices(36, tokens, k, experts, 0.1).to(DEV), experts)
+    x = torch.randn(tokens, cols, device=DEV).to(BF16)
+    w = weights(37, tokens, k).to(DEV) if weighted else None
+    got = m.quantize_dispatch_dual(x, plan, w)
+    for a, b in zip(got, (*m.quantize_dispatch(x, plan, m.ROW, w),
+                          *m.quantize_dispatch(x, plan, m.COL, w))):
+        assert torch.equal(a, b)
+
+
 def test_quantize_dispatch_of_nan_infinity_and_tiny_values(m):
     tokens, k, experts, cols = 200, 2, 4, 128
     plan = m.route(choices(14, tokens, k, experts).to(DEV), experts)
