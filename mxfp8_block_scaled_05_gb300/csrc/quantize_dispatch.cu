@@ -13,8 +13,8 @@
 // segments, whose rows come out of L2 for all but a token's first expert. Both copies together go
 // so, side by side or in turn. CTAs are persistent and derive the segments from the offsets once.
 //
-// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 33 us, column copy 50,
-// both 85 (with weights 57, 62 and 118). What bounds them: the row copy the rate at which an SM
+// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 32 us, column copy 50,
+// both 85 (with weights 58, 62 and 115). What bounds them: the row copy the rate at which an SM
 // sends bulk copies away (22 bytes a clock) and the scattered scale words (6 us); the column copy
 // 268 MB read from L2 (27 us of it), the ALU pipe and the L1 path, each busy half of the time, and
 // two barriers a tile. What counted most: results leave by lines that L2 evicts first, so that the
@@ -60,6 +60,7 @@ struct Params {
   int64_t col_tiles, row_tiles;     // 128 x 128 tiles; row_tiles: the most that segments have
   uint32_t parts, part_cols;        // of a token's row: how many, and their columns
   uint32_t token_units;             // tokens * parts
+  uint32_t pad_cols, pad_units;     // of a padding unit, and how many units
   uint32_t run;                     // column tiles of a tile item
   uint32_t tile_items;
   uint32_t col_ctas;                // that make the column copy
@@ -233,28 +234,32 @@ __device__ __forceinline__ TileRow tile_row_of(const SegmentView& seg, int E, in
 }
 
 // Row copy of rows without an entry: zero codes, and zero bytes in the scale tiles, past the
-// segments' ends too. A warp takes 32 rows of a tile row; the lane of a row issues its copies
-// from a block of zeros.
+// segments' ends too. A warp takes a part of 32 rows of a tile row; the lane of a row issues its
+// copies from a block of zeros.
 __device__ __forceinline__ void pad_unit(const Params& p, const SegmentView& seg,
                                          const uint8_t* zeros, uint32_t u) {
   const int lane = threadIdx.x & 31;
+  const uint32_t quarters = static_cast<uint32_t>(p.row_tiles) * 4, part = u / quarters;
+  u -= part * quarters;
+  const int64_t c0 = static_cast<int64_t>(part) * p.pad_cols;
+  const int64_t c1 = c0 + p.pad_cols < p.cols ? c0 + p.pad_cols : p.cols;
+  const int64_t tiles = (c1 - c0 + kTile - 1) / kTile;
   const int tile_row = static_cast<int>(u >> 2), r = 32 * (u & 3) + lane;
-  uint8_t* scales = p.row_scales + tile_row * p.col_tiles * 512;
+  uint8_t* scales = p.row_scales + (tile_row * p.col_tiles + c0 / kTile) * 512;
   if (tile_row >= seg.tile_base[p.E]) {   // no segment's: a quarter of its tiles
-    uint4* quarter = reinterpret_cast<uint4*>(scales) + (u & 3) * p.col_tiles * 8;
-    for (int64_t i = lane; i < p.col_tiles * 8; i += 32) quarter[i] = make_uint4(0, 0, 0, 0);
+    uint4* quarter = reinterpret_cast<uint4*>(scales) + (u & 3) * tiles * 8;
+    for (int64_t i = lane; i < tiles * 8; i += 32) quarter[i] = make_uint4(0, 0, 0, 0);
     return;
   }
   const TileRow q = tile_row_of(seg, p.E, tile_row);
   const int64_t row = q.row0 + r;
   if (r < q.rows && p.entry_of[row] >= 0) return;
   uint32_t* word = reinterpret_cast<uint32_t*>(scales) + (r & 31) * 4 + (r >> 5);
-  for (int64_t i = 0; i < p.col_tiles; ++i) word[i * kTile] = 0;
+  for (int64_t i = 0; i < tiles; ++i) word[i * kTile] = 0;
   if (r >= q.rows) return;
-  for (int64_t c = 0; c < p.cols; c += kZeros)
+  for (int64_t c = c0; c < c1; c += kZeros)
     bulk_store(p.row_codes + row * p.cols + c, zeros,
-               static_cast<uint32_t>(p.cols - c < kZeros ? p.cols - c : kZeros),
-               evict_first_policy());
+               static_cast<uint32_t>(c1 - c < kZeros ? c1 - c : kZeros), evict_first_policy());
 }
 
 // Column copy of a run of 128 x 128 tiles beside one another. A thread holds 8 consecutive rows
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_dispatch_kernel
     // and an SM sends copies away at 22 bytes a clock at most.
     const int warp = threadIdx.x >> 5;
     const uint32_t ctas = gridDim.x - p.col_ctas;
-    const uint32_t units = p.token_units + static_cast<uint32_t>(p.row_tiles) * 4;  // below 2^32
+    const uint32_t units = p.token_units + p.pad_units;   // each below 2^31
     int buf = 0;
     for (uint32_t u = warp * ctas + blockIdx.x - p.col_ctas; u < units; u += ctas * kWarps) {
       if (u < p.token_units) {
@@ -550,10 +555,17 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
     while (p.part_cols > kPiece && a.tokens * cdiv(a.cols, p.part_cols) < most * kWarps)
       p.part_cols /= 2;
     const int64_t parts = cdiv(a.cols, p.part_cols), units = a.tokens * parts;
-    if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    // The same of padding, whose rows wait for nothing: 8 tokens of 4096 columns, 2 of 8 experts
+    // each, 10.3 to 3.9 us (37 of 2048 columns, 8 of 128: 7.4 to 5.8; 8192: 33.5 to 32.0).
+    p.pad_cols = 4 * kPiece;
+    while (p.pad_cols > kPiece && 4 * p.row_tiles * cdiv(a.cols, p.pad_cols) < most * kWarps)
+      p.pad_cols /= 2;
+    const int64_t pads = 4 * p.row_tiles * cdiv(a.cols, p.pad_cols);
+    if (units > 0x7FFFFFFF || pads > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.parts = static_cast<uint32_t>(parts);
     p.token_units = static_cast<uint32_t>(units);
-    row_ctas = std::min(most, cdiv(units + 4 * p.row_tiles, kWarps));
+    p.pad_units = static_cast<uint32_t>(pads);
+    row_ctas = std::min(most, cdiv(units + pads, kWarps));
   }
   if (a.col_out) {   // neighbouring tiles are joined into items while each CTA keeps two
     const int64_t run = p.row_tiles * p.col_tiles / (2 * most);
@@ -571,8 +583,8 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
   // there is much, the copies go in turn, as the tokens' rows leave L2 sooner with both at work.
   // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 13, 23;
   // 4096 x 8 x 2048: 49, 55; 8192 x 8 x 2048: 85, 86; 16384 x 8 x 2048: 172, 166; 16384 x 8 x
-  // 7168: 743, 650; 16384 x 4 x 4096: 189, 180; 16384 x 2 x 4096: 104, 124; 16384 x 1 x 2048: 44,
-  // 49; with weights 1024 x 8 x 2048: 32, 34; 8192 x 8 x 2048: 118, 120; 16384 x 4 x 4096: 237, 228.
+  // 7168: 743, 650; 16384 x 4 x 4096: 189, 180; 16384 x 2 x 4096: 102, 124; 16384 x 1 x 2048: 44,
+  // 49; with weights 1024 x 8 x 2048: 32, 34; 8192 x 8 x 2048: 115, 120; 16384 x 4 x 4096: 237, 228.
   if (a.row_out && a.col_out) {
     if (p.entries * a.cols < int64_t{1} << 28) {
       const double x = static_cast<double>(a.tokens), y = static_cast<double>(p.entries);
