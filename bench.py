@@ -287,7 +287,7 @@ class DenseStep:
 
 
 KERNEL_SOURCES = {"mxfp8_gemm": ("gemm.cu", "device.cuh"),
-                  "quantize_dual": ("quantize.cu", "device.cuh")}
+                  "quantize_dual": ("quantize.cu", "convert.cuh", "segments.cuh", "device.cuh")}
 
 
 def source_sha(kernel_key: str):

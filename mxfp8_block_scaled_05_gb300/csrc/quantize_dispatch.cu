@@ -267,8 +267,8 @@ __device__ __forceinline__ void pad_unit(const Params& p, const SegmentView& seg
 // two values at once, here from two rows, which leaves a column's 8 codes in 8 consecutive bytes.
 // They pass through shared memory (8-byte units, their index XORed with twice the column's
 // eighth, so that both the writes and the reads of 16 bytes are free of bank conflicts) and leave
-// as rows of 128 bytes; the next tile's loads are in flight meanwhile. A warp that keeps 16 rows of 4
-// columns a thread needs neither the stage nor a barrier, but its stores of 32 bytes took 77 us.
+// as rows of 128 bytes; the next tile's loads are in flight meanwhile. A warp that keeps 16 rows of
+// 4 columns a thread needs neither the stage nor a barrier, but its stores of 32 bytes took 77 us.
 struct Patch {
   uint32_t x[8][4];
 };
@@ -581,8 +581,8 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
   // once an expert; a segment's last tile costs as much as a full one). Shares go by eighths, so
   // that the SMs hold like mixtures: a share of 28% in place of 25 or 37 costs up to 7%. Where
   // there is much, the copies go in turn, as the tokens' rows leave L2 sooner with both at work.
-  // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 13, 23;
-  // 4096 x 8 x 2048: 49, 55; 8192 x 8 x 2048: 85, 86; 16384 x 8 x 2048: 172, 166; 16384 x 8 x
+  // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 14,
+  // 23; 4096 x 8 x 2048: 49, 55; 8192 x 8 x 2048: 85, 86; 16384 x 8 x 2048: 172, 166; 16384 x 8 x
   // 7168: 743, 650; 16384 x 4 x 4096: 189, 180; 16384 x 2 x 4096: 102, 124; 16384 x 1 x 2048: 44,
   // 49; with weights 1024 x 8 x 2048: 32, 34; 8192 x 8 x 2048: 115, 120; 16384 x 4 x 4096: 237, 228.
   if (a.row_out && a.col_out) {

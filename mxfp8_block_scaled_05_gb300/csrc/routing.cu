@@ -56,8 +56,10 @@ struct RouteParams {
 // per expert then turns the counters into places (over the warps of a CTA, then over the CTAs,
 // whose totals go round through distributed shared memory), and the entries take them, in the
 // order of their rows through shared memory: an SM stores to one line a clock, and scattered
-// stores of 4 bytes took 4 us of 12 on 8 CTAs. Runs that do not fit the registers are read twice. One launch, no workspace, and nothing depends on timing: only
-// one warp adds to a counter, group by group. Bound by the chain of these steps, each 0.3 to 1 us.
+// stores of 4 bytes took 4 us of 12 on 8 CTAs. Runs that do not fit the registers are read twice.
+// One launch, no workspace, and nothing depends on timing: only one warp adds to a counter, group
+// by group. Bound by the chain of these steps, each 0.3 to 1 us: 8 entries of 128 experts 3.2 us,
+// 8192 4.8, 65536 8.5, 524288 39.
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
   extern __shared__ __align__(16) uint32_t dyn[];
   uint32_t* total = dyn;                                  // [CTAs][E], every CTA's
@@ -307,7 +309,8 @@ __device__ __forceinline__ typename Pack<T, V>::raw pack(const float (&x)[V]) {
     uint32_t w[sizeof(r) / 4];
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(r) / 4); ++i)
-      w[i] = sizeof(T) == 4 ? __float_as_uint(x[i]) : cvt_bf16x2(x[(2 * i + 1) % V], x[(2 * i) % V]);
+      w[i] = sizeof(T) == 4 ? __float_as_uint(x[i])
+                            : cvt_bf16x2(x[(2 * i + 1) % V], x[(2 * i) % V]);
     memcpy(&r, w, sizeof(r));
   }
   return r;
@@ -364,7 +367,8 @@ template <size_t kBytes>
 constexpr int kDispatchU = kBytes >= 4 ? 64 / static_cast<int>(kBytes) : 16;
 
 // A warp reads a piece of a token's row once and writes it to the token's k rows; the rows of
-// no entry are zeroed on the side. Bound by the writes.
+// no entry are zeroed on the side. Bound by the writes: 8192 tokens of 2048 BF16 columns, 8 experts
+// each, 50 us (6.4 TB/s); 1021 tokens of 1999 FP32 columns, 4-byte accesses, 13.7 (5.3).
 template <typename T, int V, bool kWeighted>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowsParams p) {
   using raw = typename Pack<T, V>::raw;
@@ -417,7 +421,8 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowsParams p) 
 // ------------------------------------------------------------------------------- combine
 
 // A warp sums a piece (kC times 32 lanes x V columns) of a token's k rows, kU of them at a time:
-// enough of both that a lane has 128 bytes on their way. Bound by the reads.
+// enough of both that a lane has 128 bytes on their way. Bound by the reads: 8192 tokens of 2048
+// BF16 columns, 8 experts each, 46 us (6.5 TB/s); with 1999 columns, 2-byte accesses, 67 (4.4).
 template <typename T, int V, bool kWeighted, int kU, int kC>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const RowsParams p) {
   using raw = typename Pack<T, V>::raw;
@@ -501,7 +506,8 @@ __device__ __forceinline__ float sums_of(float (&x)[N], int lane) {
 // A group of kGroup threads (a warp, or the CTA) takes a token: it reads dout[t] and the token's
 // rows of y, kU rows and kC times kGroup accesses of each at a time, writes w dout[t] to the rows'
 // gradients and sums the products for the weights'. The sums are joined over the lanes, then over
-// the warps in order. Bound by memory.
+// the warps in order. Bound by memory: 8192 tokens of 2048 BF16 columns, 8 experts each, 91 us (6.5
+// TB/s); 509 tokens of 1033 FP32 columns, 2 each, 4.7 us (4.2 TB/s, of which 2 are the launch).
 template <typename T, int V, int kGroup, bool kRows, int kU, int kC>
 __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const RowsParams p) {
   using raw = typename Pack<T, V>::raw;

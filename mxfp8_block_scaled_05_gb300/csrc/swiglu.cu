@@ -14,9 +14,10 @@
 // 2^-9. Beyond it (g < -88) s is 0. A gate of -inf gives NaN (-inf * 0).
 //
 // Bound by memory: forward 4 bytes read and 2 + 2.0625 written for each value of h, backward
-// 2 + 2.0625 read and 4 (with h' 6) written. A thread holds 16 gates and the 16 ups beside them: half
-// a block each, so a block's maximum takes one exchange between neighbours, and every access is
-// 16 or 32 bytes.
+// 2 + 2.0625 read and 4 (with h' 6) written: 4096 x 12288 values of h take 59 us forward (6.9 TB/s),
+// 61 backward and 76 with h' (6.7 TB/s). A thread holds 16 gates and the 16 ups beside them: half a
+// block each, so a block's maximum takes one exchange between neighbours, and every access is 16
+// or 32 bytes.
 
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -105,8 +106,9 @@ __device__ __forceinline__ Place place(int64_t rows, int64_t width) {
 // Half a block's codes and scale: the maximum is the block's, shared with the other half.
 __device__ __forceinline__ void keep_half(const uint32_t (&w)[8], uint8_t* codes, uint8_t* scale,
                                           int rule, bool valid) {
-  uint32_t m2 = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3])),
-                               max_abs_bf16x2(max_abs_bf16x2(w[4], w[5]), max_abs_bf16x2(w[6], w[7])));
+  uint32_t m2 = max_abs_bf16x2(
+      max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3])),
+      max_abs_bf16x2(max_abs_bf16x2(w[4], w[5]), max_abs_bf16x2(w[6], w[7])));
   m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 1)) & kAbs2;
   const uint32_t s = scale_byte(max(m2 & 0xFFFFu, m2 >> 16), rule);
   uint4 o;
