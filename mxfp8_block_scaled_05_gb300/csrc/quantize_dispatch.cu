@@ -13,8 +13,8 @@
 // segments, whose rows come out of L2 for all but a token's first expert. Both copies together go
 // so, side by side or in turn. CTAs are persistent and derive the segments from the offsets once.
 //
-// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 32 us, column copy 50,
-// both 85 (with weights 58, 62 and 115). What bounds them: the row copy the rate at which an SM
+// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 32 us, column copy 51,
+// both 79 (with weights 58, 64 and 116). What bounds them: the row copy the rate at which an SM
 // sends bulk copies away (22 bytes a clock) and the scattered scale words (6 us); the column copy
 // 268 MB read from L2 (27 us of it), the ALU pipe and the L1 path, each busy half of the time, and
 // two barriers a tile. What counted most: results leave by lines that L2 evicts first, so that the
@@ -61,8 +61,6 @@ struct Params {
   uint32_t parts, part_cols;        // of a token's row: how many, and their columns
   uint32_t token_units;             // tokens * parts
   uint32_t pad_cols, pad_units;     // of a padding unit, and how many units
-  uint32_t run;                     // column tiles of a tile item
-  uint32_t tile_items;
   uint32_t col_ctas;                // that make the column copy
   int* status;
 };
@@ -338,22 +336,11 @@ __device__ __forceinline__ void convert_pair_nan(const Patch& t, int h, uint32_t
 }
 
 template <bool kWeighted>
-__device__ __forceinline__ void tile_item(const Params& p, const SegmentView& seg, TileShared& sh,
-                                          uint32_t item) {
+__device__ __forceinline__ void tile_run(const Params& p, const SegmentView& seg, TileShared& sh,
+                                         int tile_row, int64_t bx0, int64_t bx1) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int block = warp >> 1, sub = lane >> 3, vec = lane & 7;
   const int c = 64 * (warp & 1) + 8 * vec;   // the thread's first column of a tile
-  const uint32_t row_tiles = static_cast<uint32_t>(p.row_tiles);
-  const uint32_t part = item / row_tiles;
-  const int tile_row = static_cast<int>(item - part * row_tiles);
-  const int64_t bx0 = static_cast<int64_t>(part) * p.run;
-  const int64_t bx1 = bx0 + p.run < p.col_tiles ? bx0 + p.run : p.col_tiles;
-  if (tile_row >= seg.tile_base[p.E]) {   // no segment's: the tail of the scales
-    uint4* tail = reinterpret_cast<uint4*>(p.col_scales + (tile_row * p.col_tiles + bx0) * 512);
-    for (int i = tid; i < static_cast<int>(bx1 - bx0) * 32; i += kThreads)
-      tail[i] = make_uint4(0, 0, 0, 0);
-    return;
-  }
   const TileRow q = tile_row_of(seg, p.E, tile_row);
   const bool rows_ok = 32 * block < q.rows;  // segments are multiples of 32 rows
   uint32_t token = 0;
@@ -475,8 +462,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_dispatch_kernel
   if (!seg.ok) return;
   if (blockIdx.x < p.col_ctas) {
     TileShared& sh = *reinterpret_cast<TileShared*>(dyn);
-    for (uint32_t item = blockIdx.x; item < p.tile_items; item += p.col_ctas)
-      tile_item<kWeighted>(p, seg, sh, item);
+    // Items of up to 8 tiles beside one another, all rows of a part of the columns before the next
+    // part, so that the CTAs read the same columns of the tokens at a time and find them in L2
+    // (16384 tokens of 7168 columns: 342 us, 564 with a contiguous share a CTA). What does not
+    // fill a last round of the CTAs is cut into as many pieces as do.
+    const uint32_t ctas = p.col_ctas, rows = seg.tile_base[p.E];
+    const uint32_t col_tiles = static_cast<uint32_t>(p.col_tiles), tiles = rows * col_tiles;
+    uint32_t run = tiles / (2 * ctas);
+    run = run < 1 ? 1 : run > 8 ? 8 : run;
+    const uint32_t items = rows * ((col_tiles + run - 1) / run);
+    const uint32_t rest = items % ctas, whole = items - rest;
+    uint32_t pieces = rest ? ctas / rest : 1;
+    if (pieces > run) pieces = run;
+    const uint32_t step = (run + pieces - 1) / pieces;
+    for (uint32_t i = blockIdx.x; i < whole + rest * pieces; i += ctas) {
+      uint32_t item = i, from = 0, to = run;
+      if (i >= whole) {
+        const uint32_t piece = (i - whole) / rest;
+        item = i - piece * rest;
+        from = piece * step;
+        to = from + step < run ? from + step : run;
+      }
+      const uint32_t part = item / rows;
+      from += part * run;
+      to += part * run;
+      if (to > col_tiles) to = col_tiles;
+      if (from < to) tile_run<kWeighted>(p, seg, sh, item - part * rows, from, to);
+    }
+    // the scales past the segments' tiles
+    uint4* tail = reinterpret_cast<uint4*>(p.col_scales) + int64_t{tiles} * 32;
+    const uint64_t n = (p.row_tiles * p.col_tiles - tiles) * 32;
+    for (uint64_t i = blockIdx.x * kThreads + threadIdx.x; i < n; i += p.col_ctas * kThreads)
+      tail[i] = make_uint4(0, 0, 0, 0);
   } else {
     RowShared& sh = *reinterpret_cast<RowShared*>(dyn);
     static_assert(kZeros == 2 * kThreads, "one store a thread");
@@ -504,13 +521,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_dispatch_kernel
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+static_assert(kBuffers + sizeof(int32_t) * SegmentView::words(kMaxExperts) <= 48 * 1024,
+              "no leave needed for the shared memory");
+
 cudaError_t launch(void (*k)(const Params), int64_t wanted, size_t dyn, const Params& p,
                    cudaStream_t stream) {
-  if (dyn > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(dyn));
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(wanted), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -567,13 +582,9 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
     p.pad_units = static_cast<uint32_t>(pads);
     row_ctas = std::min(most, cdiv(units + pads, kWarps));
   }
-  if (a.col_out) {   // neighbouring tiles are joined into items while each CTA keeps two
-    const int64_t run = p.row_tiles * p.col_tiles / (2 * most);
-    p.run = static_cast<uint32_t>(run < 1 ? 1 : run > 8 ? 8 : run);
-    const int64_t items = p.row_tiles * cdiv(p.col_tiles, p.run);
-    if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    p.tile_items = static_cast<uint32_t>(items);
-    col_ctas = std::min(most, items);
+  if (a.col_out) {
+    if (p.row_tiles * p.col_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    col_ctas = std::min(most, p.row_tiles * p.col_tiles);
   }
   const size_t dyn = kBuffers + table;
   // Both copies side by side, in shares of the CTAs after what each copy costs: ns for 1024
@@ -582,9 +593,10 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
   // that the SMs hold like mixtures: a share of 28% in place of 25 or 37 costs up to 7%. Where
   // there is much, the copies go in turn, as the tokens' rows leave L2 sooner with both at work.
   // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 14,
-  // 23; 4096 x 8 x 2048: 49, 55; 8192 x 8 x 2048: 85, 86; 16384 x 8 x 2048: 172, 166; 16384 x 8 x
-  // 7168: 743, 650; 16384 x 4 x 4096: 189, 180; 16384 x 2 x 4096: 102, 124; 16384 x 1 x 2048: 44,
-  // 49; with weights 1024 x 8 x 2048: 32, 34; 8192 x 8 x 2048: 115, 120; 16384 x 4 x 4096: 237, 228.
+  // 18; 4096 x 8 x 2048: 49, 50; 8192 x 8 x 2048: 79, 85; 16384 x 8 x 2048: 173, 163; 16384 x 8 x
+  // 7168: 741, 633; 16384 x 4 x 4096: 184, 175; 16384 x 2 x 4096: 104, 110; 16384 x 1 x 2048: 42,
+  // 47; with weights 4096 x 8 x 2048: 67, 70; 8192 x 8 x 2048: 116, 121; 16384 x 4 x 4096: 225,
+  // 222.
   if (a.row_out && a.col_out) {
     if (p.entries * a.cols < int64_t{1} << 28) {
       const double x = static_cast<double>(a.tokens), y = static_cast<double>(p.entries);
