@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_dispatch_kernel
     // fill a last round of the CTAs is cut into as many pieces as do.
     const uint32_t ctas = p.col_ctas, rows = seg.tile_base[p.E];
     const uint32_t col_tiles = static_cast<uint32_t>(p.col_tiles), tiles = rows * col_tiles;
-    uint32_t run = tiles / (2 * ctas);
+    uint32_t run = tiles / ctas;   // at half of it 37 x 8 x 2048: 14 us, 12.8 so
     run = run < 1 ? 1 : run > 8 ? 8 : run;
     const uint32_t items = rows * ((col_tiles + run - 1) / run);
     const uint32_t rest = items % ctas, whole = items - rest;
@@ -592,7 +592,7 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
   // once an expert; a segment's last tile costs as much as a full one). Shares go by eighths, so
   // that the SMs hold like mixtures: a share of 28% in place of 25 or 37 costs up to 7%. Where
   // there is much, the copies go in turn, as the tokens' rows leave L2 sooner with both at work.
-  // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 14,
+  // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 13,
   // 18; 4096 x 8 x 2048: 49, 50; 8192 x 8 x 2048: 79, 85; 16384 x 8 x 2048: 173, 163; 16384 x 8 x
   // 7168: 741, 633; 16384 x 4 x 4096: 184, 175; 16384 x 2 x 4096: 104, 110; 16384 x 1 x 2048: 42,
   // 47; with weights 4096 x 8 x 2048: 67, 70; 8192 x 8 x 2048: 116, 121; 16384 x 4 x 4096: 225,
