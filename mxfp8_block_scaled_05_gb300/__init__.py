@@ -799,7 +799,10 @@ def dispatch(x: torch.Tensor, plan: RoutePlan, weights: Optional[torch.Tensor] =
 
 def _dispatch_copy(rows, cols, experts, axis, codes, scales, device, stream):
     """Codes and scales of one grouped copy: given ones checked, absent ones allocated."""
-    need = lib().mxfp8_grouped_scale_bytes(rows, cols, experts, axis)
+    if experts > 0 and rows % 32 == 0 == cols % 32:   # grouped_scale_bytes
+        need = (-(-rows // 128) + experts) * -(-cols // 128) * 512
+    else:
+        need = lib().mxfp8_grouped_scale_bytes(rows, cols, experts, axis)
     if need == 0 and cols:   # cols not a multiple of 32, or sizes that do not fit: as the call says
         _check(ERR_ALIGNMENT if axis == ROW and cols % 32 else ERR_INVALID_ARG,
                "mxfp8_quantize_dispatch")
