@@ -599,11 +599,12 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
   // 222.
   if (a.row_out && a.col_out) {
     if (p.entries * a.cols < int64_t{1} << 28) {
-      const double x = static_cast<double>(a.tokens), y = static_cast<double>(p.entries);
-      const double pad = static_cast<double>(std::max<int64_t>(a.rows - p.entries, 0));
+      const double x = static_cast<double>(a.tokens);
+      const double y = static_cast<double>(std::min(p.entries, a.rows));
+      const double pad = static_cast<double>(a.rows) - y;
       const double row = (a.weights ? 0.58 * x + 0.44 * y : 0.37 * x + 0.21 * y) + 0.12 * pad;
       const double col = 0.35 * x + (a.weights ? 0.36 : 0.28) * (a.rows + 0.5 * kTile * p.E);
-      const int64_t eighths = std::max<int64_t>(2, std::llround(8 * row / (row + col)));
+      const int64_t eighths = std::clamp<int64_t>(std::llround(8 * row / (row + col)), 2, 6);
       row_ctas = std::min(row_ctas, most * eighths / 8);
       col_ctas = std::min(col_ctas, most - row_ctas);
     } else {

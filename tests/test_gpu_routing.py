@@ -296,6 +296,26 @@ def test_quantize_dispatch_shares(m, tokens, k, cols, experts, weighted):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("tokens,k,weighted", [
+    (4096, 40, True), (30000, 40, True), (30000, 40, False), (30000, 1, True), (3, 1000, True)])
+def test_quantize_dispatch_of_few_rows_of_many_entries(m, tokens, k, weighted):
+    """Nearly all entries of no expert, and no more rows than the others need: both copies are
+    written whole."""
+    ids = torch.full((tokens, k), -1, dtype=torch.int64)
+    ids[::tokens // 3, 0] = 1
+    plan = m.route(ids.to(DEV), 2, rows=32)
+    x = values(38, tokens, 96, BF16).to(DEV)
+    w = weights(39, tokens, k).to(DEV) if weighted else None
+    bytes_ = [torch.full((n,), 0xA5, dtype=torch.uint8, device=DEV) for n in
+              (32 * 96, m.grouped_scale_bytes(32, 96, 2, m.ROW),
+               32 * 96, m.grouped_scale_bytes(32, 96, 2, m.COL))]
+    m.quantize_dispatch_dual(x, plan, w, *bytes_)
+    for got, want in zip(bytes_, (*m.quantize_dispatch(x, plan, m.ROW, w),
+                                  *m.quantize_dispatch(x, plan, m.COL, w))):
+        assert torch.equal(got, want.flatten())
+    assert m.device_status() == m.OK
+
+
 def test_quantize_dispatch_of_nan_infinity_and_tiny_values(m):
     tokens, k, experts, cols = 200, 2, 4, 128
     plan = m.route(choices(14, tokens, k, experts).to(DEV), experts)
