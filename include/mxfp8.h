@@ -607,8 +607,9 @@ int mxfp8_route(const int64_t* ids_dev, int64_t tokens, int top_k, int num_exper
  *                are FP32, rounded once.
  *   out_dev      [total_rows][cols], of x's type, written in full; may not overlap x
  * Up to 2097120 cols (65535 * 32); rows of a multiple of 16 bytes are the fastest, of an odd
- * number of BF16 values the slowest. x and out start on 16 bytes. A plan whose rows do not fit total_rows is not followed there: MXFP8_ERR_BAD_OFFSETS is latched
- * and the row skipped.
+ * number of BF16 values the slowest. x and out start on 16 bytes. A plan whose rows do not fit
+ * total_rows is not followed there: MXFP8_ERR_BAD_OFFSETS is latched and the row skipped. Of a plan
+ * that mxfp8_route did not write, no two entries may share a row, and row_of and entry_of agree.
  */
 int mxfp8_dispatch(const void* x_dev, int dtype, int64_t tokens, int64_t cols, int top_k,
                    const float* weights_dev, const int32_t* row_of_dev,
@@ -623,7 +624,7 @@ int mxfp8_dispatch(const void* x_dev, int dtype, int64_t tokens, int64_t cols, i
  * mxfp8_grouped_scale_bytes(total_rows, cols, num_experts, axis) bytes and are written in full:
  * zeros follow the last block. Invalid offsets latch MXFP8_ERR_BAD_OFFSETS and write nothing.
  * total_rows == 0 or cols == 0 is a no-op. tokens * cols below 2^35, at most 65535 - num_experts
- * tiles of 128 rows.
+ * tiles of 128 rows. x and all four outputs start on 16 bytes; none overlaps another.
  */
 int mxfp8_quantize_dispatch(const void* x_dev, int64_t tokens, int64_t cols, int top_k,
                             const float* weights_dev, const int32_t* row_of_dev,
@@ -671,7 +672,8 @@ int mxfp8_combine_backward(const void* grad_out_dev, const void* y_dev, int dtyp
  *               MXFP8_RULE_CEIL saturates nothing: every value of a block is then within 2^-4 of
  *               itself or within 2^-17 of the block's largest.
  * A gate of -inf gives NaN; sigmoids below 2^-126 are 0.
- * All buffers start on 16 bytes (scales_dev anywhere). rows == 0 or width == 0 is a no-op.
+ * All buffers start on 16 bytes (scales_dev anywhere), and no two overlap. rows == 0 or width == 0
+ * is a no-op.
  */
 int mxfp8_swiglu(const void* x_dev, int64_t rows, int64_t width, void* h_dev, void* codes_dev,
                  void* scales_dev, int scale_rule, void* stream);
@@ -706,9 +708,9 @@ int mxfp8_set_wait_limit_ns(uint64_t ns);
  * Synchronizes `stream`, then returns and clears the current device's status word:
  * MXFP8_OK, or the first device-side error latched since the last call
  * (MXFP8_ERR_BAD_OFFSETS, MXFP8_ERR_TIMEOUT, MXFP8_ERR_BAD_TARGET, MXFP8_ERR_BAD_EXPERT), or
- * MXFP8_ERR_CUDA if the synchronization itself failed. The word is read and cleared in one atomic exchange, enqueued on
- * `stream` after its earlier work. An error that a kernel on another stream latches
- * concurrently is reported by this call or by the next one; it is never cleared unread.
+ * MXFP8_ERR_CUDA if the synchronization itself failed. The word is read and cleared in one atomic
+ * exchange, enqueued on `stream` after its earlier work. An error that a kernel on another stream
+ * latches concurrently is reported by this call or by the next one; it is never cleared unread.
  */
 int mxfp8_get_device_status(void* stream);
 
