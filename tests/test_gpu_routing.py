@@ -512,3 +512,18 @@ def test_rows_past_two_to_the_31_elements(m):
     assert torch.equal(grad_w[:, 0], x[:, 0].float() ** 2 + x[:, -1].float() ** 2)
     assert torch.equal(y[:, -1].float(),
                        2 * torch.where(entry < 0, 0.0, x[:, -1][entry.clamp(min=0)].float()))
+
+
+def test_quantize_dispatch_past_two_to_the_31_bytes(m):
+    """Both copies of 66000 rows and more of 33024 columns: the grouped quantizer's."""
+    tokens, k, cols, experts = 33000, 2, 33024, 3
+    plan = m.route(choices(40, tokens, k, experts).to(DEV), experts)
+    assert plan.entry_of.numel() * cols > 2 ** 31
+    x = torch.randn(tokens, cols, device=DEV, dtype=BF16)
+    got = m.quantize_dispatch_dual(x, plan)
+    want = m.quantize_grouped_dual(m.dispatch(x, plan), plan.offsets)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    off = plan.offsets.cpu()
+    used = int(((off[1:] - off[:-1] + 127) // 128).sum()) * (cols // 128) * 512
+    for a, b in ((got[1], want[1]), (got[3], want[3])):
+        assert torch.equal(a[:used], b[:used]) and not a[used:].any()
