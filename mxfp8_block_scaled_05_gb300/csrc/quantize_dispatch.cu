@@ -391,6 +391,8 @@ __device__ __forceinline__ void tile_run(const Params& p, const SegmentView& seg
                            max_abs_bf16x2(t.x[6][h], t.x[7][h])));
         m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 8));
         m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 16));
+        // past the columns zeros, which a weight that is no number would have turned into NaN
+        if (kWeighted && col0 + c >= p.cols) m2 = 0;
         exps[h] = max_u16x2(m2 & 0x7F807F80u, 0x04000400u);
         worst = max_u16x2(worst, exps[h]);
       }

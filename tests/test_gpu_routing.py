@@ -327,6 +327,25 @@ def test_quantize_dispatch_of_nan_infinity_and_tiny_values(m):
     check_quantized(m, x, plan, experts, weights(16, tokens, k))
 
 
+def test_quantize_dispatch_of_every_magnitude(m):
+    """Rows and weights over the exponents of their types, subnormals, zeros, infinities and NaN
+    among the weights; within a row values down to 2^-20 of the largest."""
+    tokens, k, experts, cols = 3000, 5, 4, 96
+    g = torch.Generator().manual_seed(41)
+    plan = m.route(choices(42, tokens, k, experts, 0.1).to(DEV), experts)
+    rand = lambda *n: torch.rand(*n, generator=g, dtype=torch.float64)  # noqa: E731
+    sign = lambda *n: torch.where(rand(*n) < 0.5, -1.0, 1.0).double()  # noqa: E731
+    level = torch.floor(rand(tokens, 1) * 266 - 138) - torch.floor(rand(tokens, cols) * 21)
+    x = (sign(tokens, cols) * (1 + rand(tokens, cols)) * 2.0 ** level).to(BF16)
+    x[torch.isinf(x)] = 1.5
+    w = (sign(tokens, k) * (1 + rand(tokens, k))
+         * 2.0 ** torch.floor(rand(tokens, k) * 276 - 149)).float()
+    w[::2] = (sign(1500, k) * (1 + rand(1500, k)) * 2.0 ** torch.floor(
+        rand(1500, k) * 40 - 20 - level[::2].max(1, keepdim=True).values.clamp(-100, 100))).float()
+    w[7, 0], w[9, 1], w[11, 2], w[13, 3] = 0.0, -0.0, float("inf"), float("nan")
+    check_quantized(m, x, plan, experts, w)
+
+
 def test_quantize_dispatch_column_copy_of_a_narrow_width(m):
     """The column copy alone takes any multiple of 8 columns."""
     plan = m.route(choices(17, 90, 2, 4).to(DEV), 4)
