@@ -96,9 +96,9 @@ __device__ __forceinline__ uint32_t e4m3x4_pow2(uint32_t w0, uint32_t w1, uint32
 }
 
 // A BF16 pair times a pair of powers of two, widened to FP32 in one expression each. Exact; -0 is
-// added, so that -0 stays -0. Where the pairs are a lane's neighbouring columns this is 1 to 4%
+// added, so that -0 stays -0. Where the pairs are a lane's neighbouring columns this is 1 to 2%
 // faster than the packed product and two unpackings (a row copy of 69504 x 2048: 33.4 and 33.9
-// us, 57.5 and 59.3 with weights); where they are pairs of rows it makes no difference.
+// us); where they are pairs of rows it makes no difference.
 __device__ __forceinline__ void scale_bf16x2(uint32_t w, uint32_t mul2, float& lo, float& hi) {
   asm("{\n\t.reg .b16 a, b, m, n;\n\t"
       "mov.b32 {a, b}, %2;\n\tmov.b32 {m, n}, %3;\n\t"

@@ -14,7 +14,7 @@
 // so, side by side or in turn. CTAs are persistent and derive the segments from the offsets once.
 //
 // 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 32 us, column copy 51,
-// both 79 (with weights 58, 64 and 116). What bounds them: the row copy the rate at which an SM
+// both 79 (with weights 54, 63 and 113). What bounds them: the row copy the rate at which an SM
 // sends bulk copies away (22 bytes a clock) and the scattered scale words (6 us); the column copy
 // 268 MB read from L2 (27 us of it), the ALU pipe and the L1 path, each busy half of the time, and
 // two barriers a tile. What counted most: results leave by lines that L2 evicts first, so that the
@@ -95,17 +95,23 @@ __device__ __forceinline__ uint32_t weigh(uint32_t x, float w) {
                     __fmul_rn(__uint_as_float(x << 16), w));
 }
 
-// 16 columns a lane: the lane's codes, and the scale bytes of the four blocks of its eight lanes
-// in one word (zero past the columns).
-__device__ __forceinline__ uint4 convert_piece(const uint32_t (&w)[8], bool valid,
-                                               uint32_t& scale_word) {
-  uint32_t m2 = block_max(w);
-  m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 1)) & kAbs2;
-  const uint32_t s = scale_byte(max(m2 & 0xFFFFu, m2 >> 16), MXFP8_RULE_FLOOR);
+// The scale bytes of the four blocks of a lane's eight lanes in one word, from each lane's own (zero
+// past the columns).
+__device__ __forceinline__ uint32_t scale_word_of(uint32_t s, bool valid) {
   uint32_t word = valid ? s << (8 * ((threadIdx.x >> 1) & 3)) : 0u;
   word |= __shfl_xor_sync(kFull, word, 2);
-  word |= __shfl_xor_sync(kFull, word, 4);
-  scale_word = word;
+  return word | __shfl_xor_sync(kFull, word, 4);
+}
+
+// Magnitude of the largest of a block's values, two lanes' 16 each, as BF16 bits.
+__device__ __forceinline__ uint32_t row_block_max(const uint32_t (&w)[8]) {
+  uint32_t m2 = block_max(w);
+  m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 1)) & kAbs2;
+  return max(m2 & 0xFFFFu, m2 >> 16);
+}
+
+// 16 columns a lane of a block with scale byte s: the lane's codes.
+__device__ __forceinline__ uint4 convert_piece(const uint32_t (&w)[8], uint32_t s) {
   if (__builtin_expect(s != 0xFFu, 1)) {
     const uint32_t mul2 = inv_scale_bf16(s) * 0x10001u;
     float f[16];
@@ -116,6 +122,35 @@ __device__ __forceinline__ uint4 convert_piece(const uint32_t (&w)[8], bool vali
                       e4m3x4_f32(f[12], f[13], f[14], f[15]));
   }
   return make_uint4(nan4(w[0], w[1]), nan4(w[2], w[3]), nan4(w[4], w[5]), nan4(w[6], w[7]));
+}
+
+// The same of a block times a weight. Rounding is monotone, so the products' largest magnitude is
+// that of x, `amax`, times the weight's, rounded like them: it is found once for all weights.
+// The power of two of the block's scale goes into the weight: products and their roundings to FP32
+// and BF16 are the same times that power, as long as neither the scaled weight nor a product that a
+// code other than 0 comes from leaves the normal numbers. Codes of 2^-10 and more of the scale are
+// normal BF16 products from scale byte 11 on, and the scaled weight is about 2^8 / amax, finite
+// where amax has an exponent field of 10 or more. Found anew for each weight, maximum and scale
+// included, 69504 x 2048 took 58 us in place of 54.
+__device__ __forceinline__ uint4 weigh_piece(const uint32_t (&x)[8], uint32_t amax, float w,
+                                             uint32_t& s) {
+  const uint32_t top = cvt_bf16x2(0.f, __fmul_rn(__uint_as_float(amax << 16), fabsf(w)));
+  s = scale_byte(top & 0x7FFFu, MXFP8_RULE_FLOOR);
+  uint32_t y[8];
+  if (__builtin_expect(s >= 12 && s != 0xFFu && amax >= 10u << 7, 1)) {
+    const float sw = __fmul_rn(w, inv_scale(s));
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = weigh(x[2 * i], sw), b = weigh(x[2 * i + 1], sw);
+      o[i] = e4m3x4_f32(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u),
+                        __uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = weigh(x[i], w);
+  return convert_piece(y, s);
 }
 
 // Row copy. A warp takes a part of a token's row: it converts it once (once for each weight, with
@@ -144,7 +179,12 @@ __device__ __forceinline__ void token_unit(const Params& p, const SegmentView& s
       for (int h = 0; h < 8; ++h) v[i][h] = 0;
     }
   }
-  const auto convert = [&](float w) {
+  uint32_t amax[kPieces];
+  if constexpr (kWeighted) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) amax[i] = row_block_max(v[i]);
+  }
+  const auto convert = [&](float w, uint32_t* scales_to) {
     if (kWeighted) {
       buf ^= 1;
       bulk_wait_read_but_one();
@@ -156,24 +196,31 @@ __device__ __forceinline__ void token_unit(const Params& p, const SegmentView& s
     for (int i = 0; i < kPieces; ++i) {
       if (kPiece * i >= cols) break;
       const int c = kPiece * i + 16 * lane;
-      uint32_t wv[8], word;
-#pragma unroll
-      for (int h = 0; h < 8; ++h) wv[h] = kWeighted ? weigh(v[i][h], w) : v[i][h];
-      const uint4 o = convert_piece(wv, c < cols, word);
+      uint32_t scale;
+      uint4 o;
+      if constexpr (kWeighted) {
+        o = weigh_piece(v[i], amax[i], w, scale);
+      } else {
+        scale = scale_byte(row_block_max(v[i]), MXFP8_RULE_FLOOR);
+        o = convert_piece(v[i], scale);
+      }
+      const uint32_t word = scale_word_of(scale, c < cols);
       if (c < cols) *reinterpret_cast<uint4*>(st.codes + buf * kPart + c) = o;
-      if ((lane & 7) == 0) st.words[buf * (kPart / kTile) + c / kTile] = word;
+      if constexpr (kWeighted) {
+        if ((lane & 7) == 0 && c < cols) scales_to[c] = word;
+      } else {
+        if ((lane & 7) == 0) st.words[c / kTile] = word;
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
   };
-  const auto store = [&](int32_t row, int64_t scales_at) {
+  const auto store = [&](int32_t row) {
     bulk_store(p.row_codes + row * p.cols + c0, st.codes + buf * kPart,
                static_cast<uint32_t>(cols), evict_first_policy());
-    uint32_t* to = reinterpret_cast<uint32_t*>(p.row_scales) + scales_at + c0;
-    for (int c = 0; c < cols; c += kTile)   // 128 words a tile of 128 columns
-      to[c] = st.words[buf * (kPart / kTile) + c / kTile];
   };
-  if (!kWeighted) convert(1.f);
+  uint32_t* scale_words = reinterpret_cast<uint32_t*>(p.row_scales) + c0;  // 128 a tile
+  if (!kWeighted) convert(1.f, nullptr);
   for (uint32_t j0 = 0; j0 < p.k; j0 += 32) {
     int32_t row = -1;
     float w = 1.f;
@@ -200,12 +247,15 @@ __device__ __forceinline__ void token_unit(const Params& p, const SegmentView& s
     if constexpr (kWeighted) {
       for (unsigned live = __ballot_sync(kFull, row >= 0); live; live &= live - 1) {
         const int j = __ffs(live) - 1;
-        convert(__shfl_sync(kFull, w, j));
-        if (lane == j) store(row, scales);
+        convert(__shfl_sync(kFull, w, j), scale_words + __shfl_sync(kFull, scales, j));
+        if (lane == j) store(row);
         bulk_commit_group();
       }
     } else {
-      if (row >= 0) store(row, scales);
+      if (row >= 0) {
+        store(row);
+        for (int c = 0; c < cols; c += kTile) scale_words[scales + c] = st.words[c / kTile];
+      }
     }
   }
   if (!kWeighted) bulk_commit_group();
@@ -391,8 +441,6 @@ __device__ __forceinline__ void tile_run(const Params& p, const SegmentView& seg
                            max_abs_bf16x2(t.x[6][h], t.x[7][h])));
         m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 8));
         m2 = max_abs_bf16x2(m2, __shfl_xor_sync(kFull, m2, 16));
-        // past the columns zeros, which a weight that is no number would have turned into NaN
-        if (kWeighted && col0 + c >= p.cols) m2 = 0;
         exps[h] = max_u16x2(m2 & 0x7F807F80u, 0x04000400u);
         worst = max_u16x2(worst, exps[h]);
       }
@@ -403,9 +451,11 @@ __device__ __forceinline__ void tile_run(const Params& p, const SegmentView& seg
     if (rows_ok) {
       const bool finite = worst < 0x7F800000u && (worst & 0xFFFFu) < 0x7F80u;
       uint8_t* stage = sh.stage + c * kTile + 8 * ((4 * block + sub) ^ (2 * vec));
-      // columns past the last are zeros, whose scale byte is 0 as it should be
-      const uint32_t e = (sub & 2 ? (sub & 1 ? exps[3] : exps[2]) : (sub & 1 ? exps[1] : exps[0])) -
-                         0x04000400u;
+      // columns past the last are zeros, whose scale byte is 0 as it should be, unless a weight that
+      // is no number has made them NaN
+      uint32_t e = (sub & 2 ? (sub & 1 ? exps[3] : exps[2]) : (sub & 1 ? exps[1] : exps[0])) -
+                   0x04000400u;
+      if (kWeighted && c >= cols) e = 0;
       if (__builtin_expect(finite, 1)) {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {   // columns c + 2h (low halves) and c + 2h + 1
@@ -597,14 +647,14 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
   // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 13,
   // 18; 4096 x 8 x 2048: 49, 50; 8192 x 8 x 2048: 79, 85; 16384 x 8 x 2048: 173, 163; 16384 x 8 x
   // 7168: 741, 633; 16384 x 4 x 4096: 184, 175; 16384 x 2 x 4096: 104, 110; 16384 x 1 x 2048: 42,
-  // 47; with weights 4096 x 8 x 2048: 67, 70; 8192 x 8 x 2048: 116, 121; 16384 x 4 x 4096: 225,
+  // 47; with weights 4096 x 8 x 2048: 67, 70; 8192 x 8 x 2048: 113, 121; 16384 x 4 x 4096: 225,
   // 222.
   if (a.row_out && a.col_out) {
     if (p.entries * a.cols < int64_t{1} << 28) {
       const double x = static_cast<double>(a.tokens);
       const double y = static_cast<double>(std::min(p.entries, a.rows));
       const double pad = static_cast<double>(a.rows) - y;
-      const double row = (a.weights ? 0.58 * x + 0.44 * y : 0.37 * x + 0.21 * y) + 0.12 * pad;
+      const double row = (a.weights ? 0.58 * x + 0.38 * y : 0.37 * x + 0.21 * y) + 0.12 * pad;
       const double col = 0.35 * x + (a.weights ? 0.36 : 0.28) * (a.rows + 0.5 * kTile * p.E);
       const int64_t eighths = std::clamp<int64_t>(std::llround(8 * row / (row + col)), 2, 6);
       row_ctas = std::min(row_ctas, most * eighths / 8);
