@@ -9,16 +9,16 @@
 //
 // The row copy goes by tokens, because what a token's row becomes row-wise does not depend on the
 // expert: a warp reads a part of a row, converts it once and sends the codes to all of the token's
-// rows. The column copy's blocks mix the tokens of a segment, so it goes by 128 x 128 tiles of the
+// rows. The column copy's blocks mix the tokens of a segment, so it goes by half tiles of the
 // segments, whose rows come out of L2 for all but a token's first expert. Both copies together go
 // so, side by side or in turn. CTAs are persistent and derive the segments from the offsets once.
 //
-// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 32 us, column copy 51,
-// both 79 (with weights 54, 63 and 113). What bounds them: the row copy the rate at which an SM
+// 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 32 us, column copy 45,
+// both 75 (with weights 56, 60 and 111). What bounds them: the row copy the rate at which an SM
 // sends bulk copies away (22 bytes a clock) and the scattered scale words (6 us); the column copy
 // 268 MB read from L2 (27 us of it), the ALU pipe and the L1 path, each busy half of the time, and
 // two barriers a tile. What counted most: results leave by lines that L2 evicts first, so that the
-// tokens' rows stay in it (column copy 58 us without), and loads in flight need the L1 cache, so
+// tokens' rows stay in it (column copy 58 us without, 50 with), and loads in flight need the L1 cache, so
 // that tables are sized by the experts and a CTA holds one stage buffer (87 us with two buffers of
 // 52 KB a CTA). One read of a tile for both copies, as the grouped quantizer makes them, took 105
 // us.
@@ -38,8 +38,9 @@ namespace mxfp8 {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 4;
+constexpr int kHalf = 64;   // columns that a CTA takes at a time for the column copy
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 8;
 constexpr int kPiece = 512;   // columns a warp converts at once, 16 a lane
 constexpr int kZeros = 512;   // bytes of zeros that padding rows are copied from
 constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -76,8 +77,8 @@ struct RowShared {
 };
 
 struct TileShared {
-  __align__(16) uint8_t stage[kTile * kTile];   // transposed codes of a tile
-  __align__(16) uint8_t scales[512];            // and its scale tile
+  __align__(16) uint8_t stage[kHalf * kTile];   // transposed codes of a half tile
+  __align__(16) uint8_t scales[256];             // and its half of the scale tile
 };
 
 constexpr size_t kBuffers =
@@ -310,7 +311,8 @@ __device__ __forceinline__ void pad_unit(const Params& p, const SegmentView& seg
                static_cast<uint32_t>(c1 - c < kZeros ? c1 - c : kZeros), evict_first_policy());
 }
 
-// Column copy of a run of 128 x 128 tiles beside one another. A thread holds 8 consecutive rows
+// Column copy of a run of half tiles, 128 rows x 64 columns, beside one another: with half a tile and
+// four warps between two barriers it takes 45 us, with a whole one and eight 50. A thread holds 8 consecutive rows
 // of 8 columns; the four lanes that hold a block's 32 rows share its maximum. The conversion takes
 // two values at once, here from two rows, which leaves a column's 8 codes in 8 consecutive bytes.
 // They pass through shared memory (8-byte units, their index XORed with twice the column's
@@ -389,8 +391,8 @@ template <bool kWeighted>
 __device__ __forceinline__ void tile_run(const Params& p, const SegmentView& seg, TileShared& sh,
                                          int tile_row, int64_t bx0, int64_t bx1) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int block = warp >> 1, sub = lane >> 3, vec = lane & 7;
-  const int c = 64 * (warp & 1) + 8 * vec;   // the thread's first column of a tile
+  const int block = warp, sub = lane >> 3, vec = lane & 7;
+  const int c = 8 * vec;   // the thread's first column of a half tile
   const TileRow q = tile_row_of(seg, p.E, tile_row);
   const bool rows_ok = 32 * block < q.rows;  // segments are multiples of 32 rows
   uint32_t token = 0;
@@ -413,13 +415,13 @@ __device__ __forceinline__ void tile_run(const Params& p, const SegmentView& seg
   for (int i = 0; i < 8; ++i) rows.at[i] = __shfl_sync(kFull, token, 8 * sub + i) * row_units;
 
   Patch t;
-  if (rows_ok) load_patch(p, rows, bx0 * kTile + c, t);
+  if (rows_ok) load_patch(p, rows, bx0 * kHalf + c, t);
   const int out_row = tid >> 3, chunk = tid & 7;   // a column of the tile, 16 rows of it
-  uint8_t* out = p.col_codes + (bx0 * kTile + out_row) * p.rows + q.row0 + 16 * chunk;
-  const int64_t tile0 = p.col_tiles * q.seg_base + q.index, rows32 = 32 * p.rows;
+  uint8_t* out = p.col_codes + (bx0 * kHalf + out_row) * p.rows + q.row0 + 16 * chunk;
+  const int64_t tile0 = p.col_tiles * q.seg_base + q.index, rows16 = 16 * p.rows;
   for (int64_t bx = bx0; bx < bx1; ++bx) {
-    const int64_t col0 = bx * kTile;
-    const int cols = static_cast<int>(p.cols - col0 < kTile ? p.cols - col0 : kTile);
+    const int64_t col0 = bx * kHalf;   // may pass the last column: half of a tile's scales
+    const int cols = static_cast<int>(p.cols - col0 < kHalf ? p.cols - col0 : kHalf);
     if (kWeighted && rows_ok) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -447,7 +449,7 @@ __device__ __forceinline__ void tile_run(const Params& p, const SegmentView& seg
     }
     __syncthreads();   // the tile before has left the stage
     const int a = c + 2 * sub;   // each of the four lanes writes the scale bytes of a column pair
-    uint8_t* scale_to = sh.scales + (a & 31) * 16 + (a >> 5) * 4 + block;
+    uint8_t* scale_to = sh.scales + (a & 31) * 8 + (a >> 5) * 4 + block;
     if (rows_ok) {
       const bool finite = worst < 0x7F800000u && (worst & 0xFFFFu) < 0x7F80u;
       uint8_t* stage = sh.stage + c * kTile + 8 * ((4 * block + sub) ^ (2 * vec));
@@ -465,7 +467,7 @@ __device__ __forceinline__ void tile_run(const Params& p, const SegmentView& seg
           *reinterpret_cast<uint2*>(stage + (2 * h + 1) * kTile) = o1;
         }
         scale_to[0] = static_cast<uint8_t>(e >> 7);
-        scale_to[16] = static_cast<uint8_t>(e >> 23);
+        scale_to[8] = static_cast<uint8_t>(e >> 23);
       } else {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -477,28 +479,28 @@ __device__ __forceinline__ void tile_run(const Params& p, const SegmentView& seg
           *reinterpret_cast<uint2*>(stage + (2 * h + 1) * kTile) = o1;
         }
         scale_to[0] = static_cast<uint8_t>((e >> 7 & 0xFFu) == 0xF7u ? 0xFFu : e >> 7);
-        scale_to[16] = static_cast<uint8_t>(e >> 23 == 0xF7u ? 0xFFu : e >> 23);
+        scale_to[8] = static_cast<uint8_t>(e >> 23 == 0xF7u ? 0xFFu : e >> 23);
       }
     } else {
-      scale_to[0] = scale_to[16] = 0;
+      scale_to[0] = scale_to[8] = 0;
     }
-    if (rows_ok && bx + 1 < bx1) load_patch(p, rows, col0 + kTile + c, t);
+    if (rows_ok && bx + 1 < bx1) load_patch(p, rows, col0 + kHalf + c, t);
     __syncthreads();
     if (16 * chunk < q.rows) {
       const uint8_t* from = sh.stage + out_row * kTile;
       uint8_t* to = out;
 #pragma unroll
-      for (int i = 0; i < 4; ++i, to += rows32) {
-        if (out_row + 32 * i < cols)
+      for (int i = 0; i < 4; ++i, to += rows16) {
+        if (out_row + 16 * i < cols)
           __stcs(reinterpret_cast<uint4*>(to),   // 50 us, 58 with stores that stay in L2
                  *reinterpret_cast<const uint4*>(
-                     from + 32 * i * kTile + 16 * (chunk ^ (((out_row >> 3) + 4 * i) & 7))));
+                     from + 16 * i * kTile + 16 * (chunk ^ (((out_row >> 3) + 2 * i) & 7))));
       }
     }
-    out += 4 * rows32;
+    out += 4 * rows16;
     if (tid < 32)
-      reinterpret_cast<uint4*>(p.col_scales + (tile0 + bx * q.seg_tiles) * 512)[tid] =
-          reinterpret_cast<const uint4*>(sh.scales)[tid];
+      *reinterpret_cast<uint2*>(p.col_scales + (tile0 + (bx >> 1) * q.seg_tiles) * 512 + 16 * tid +
+                                8 * (bx & 1)) = reinterpret_cast<const uint2*>(sh.scales)[tid];
   }
 }
 
@@ -514,15 +516,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_dispatch_kernel
   if (!seg.ok) return;
   if (blockIdx.x < p.col_ctas) {
     TileShared& sh = *reinterpret_cast<TileShared*>(dyn);
-    // Items of up to 8 tiles beside one another, all rows of a part of the columns before the next
-    // part, so that the CTAs read the same columns of the tokens at a time and find them in L2
-    // (16384 tokens of 7168 columns: 342 us, 564 with a contiguous share a CTA). What does not
-    // fill a last round of the CTAs is cut into as many pieces as do.
+    // Items of up to 8 half tiles beside one another, all rows of a part of the columns before the
+    // next part, so that the CTAs read the same columns of the tokens at a time and find them in
+    // L2 (with whole tiles and 16384 tokens of 7168 columns: 342 us, 564 with a contiguous share a
+    // CTA). What does not fill a last round of the CTAs is cut into as many pieces as do.
     const uint32_t ctas = p.col_ctas, rows = seg.tile_base[p.E];
-    const uint32_t col_tiles = static_cast<uint32_t>(p.col_tiles), tiles = rows * col_tiles;
-    uint32_t run = tiles / ctas;   // at half of it 37 x 8 x 2048: 14 us, 12.8 so
+    const uint32_t halves = 2 * static_cast<uint32_t>(p.col_tiles), all = rows * halves;
+    uint32_t run = all / ctas;   // at half of it 37 x 8 x 2048: 14 us, 12.8 so
     run = run < 1 ? 1 : run > 8 ? 8 : run;
-    const uint32_t items = rows * ((col_tiles + run - 1) / run);
+    const uint32_t parts = (halves + run - 1) / run;
+    run = (halves + parts - 1) / parts;
+    const uint32_t items = rows * parts;
     const uint32_t rest = items % ctas, whole = items - rest;
     uint32_t pieces = rest ? ctas / rest : 1;
     if (pieces > run) pieces = run;
@@ -538,18 +542,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quantize_dispatch_kernel
       const uint32_t part = item / rows;
       from += part * run;
       to += part * run;
-      if (to > col_tiles) to = col_tiles;
+      if (to > halves) to = halves;
       if (from < to) tile_run<kWeighted>(p, seg, sh, item - part * rows, from, to);
     }
     // the scales past the segments' tiles
-    uint4* tail = reinterpret_cast<uint4*>(p.col_scales) + int64_t{tiles} * 32;
-    const uint64_t n = (p.row_tiles * p.col_tiles - tiles) * 32;
+    uint4* tail = reinterpret_cast<uint4*>(p.col_scales) + int64_t{all} * 16;
+    const uint64_t n = (p.row_tiles * p.col_tiles * 2 - all) * 16;
     for (uint64_t i = blockIdx.x * kThreads + threadIdx.x; i < n; i += p.col_ctas * kThreads)
       tail[i] = make_uint4(0, 0, 0, 0);
   } else {
     RowShared& sh = *reinterpret_cast<RowShared*>(dyn);
-    static_assert(kZeros == 2 * kThreads, "one store a thread");
-    reinterpret_cast<uint16_t*>(sh.zeros)[threadIdx.x] = 0;
+    static_assert(kZeros == 4 * kThreads, "one store a thread");
+    reinterpret_cast<uint32_t*>(sh.zeros)[threadIdx.x] = 0;
     fence_proxy_async_smem();
     __syncthreads();
     // Neighbouring units go to different SMs: the padding that the last segment takes is one run,
@@ -635,8 +639,8 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
     row_ctas = std::min(most, cdiv(units + pads, kWarps));
   }
   if (a.col_out) {
-    if (p.row_tiles * p.col_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    col_ctas = std::min(most, p.row_tiles * p.col_tiles);
+    if (p.row_tiles * p.col_tiles * 2 > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    col_ctas = std::min(most, p.row_tiles * p.col_tiles * 2);
   }
   const size_t dyn = kBuffers + table;
   // Both copies side by side, in shares of the CTAs after what each copy costs: ns for 1024
@@ -644,18 +648,17 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
   // once an expert; a segment's last tile costs as much as a full one). Shares go by eighths, so
   // that the SMs hold like mixtures: a share of 28% in place of 25 or 37 costs up to 7%. Where
   // there is much, the copies go in turn, as the tokens' rows leave L2 sooner with both at work.
-  // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 13,
-  // 18; 4096 x 8 x 2048: 49, 50; 8192 x 8 x 2048: 79, 85; 16384 x 8 x 2048: 173, 163; 16384 x 8 x
-  // 7168: 741, 633; 16384 x 4 x 4096: 184, 175; 16384 x 2 x 4096: 104, 110; 16384 x 1 x 2048: 42,
-  // 47; with weights 4096 x 8 x 2048: 67, 70; 8192 x 8 x 2048: 113, 121; 16384 x 4 x 4096: 225,
-  // 222.
+  // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 12,
+  // 18; 4096 x 8 x 2048: 43, 48; 8192 x 8 x 2048: 75, 81; 16384 x 8 x 2048: 157, 156; 16384 x 8 x
+  // 7168: 702, 566; 16384 x 2 x 4096: 96, 102; 16384 x 1 x 2048: 40, 45; with weights 4096 x 8 x
+  // 2048: 64, 66; 8192 x 8 x 2048: 111, 115; 16384 x 4 x 4096: 217, 213.
   if (a.row_out && a.col_out) {
     if (p.entries * a.cols < int64_t{1} << 28) {
       const double x = static_cast<double>(a.tokens);
       const double y = static_cast<double>(std::min(p.entries, a.rows));
       const double pad = static_cast<double>(a.rows) - y;
       const double row = (a.weights ? 0.58 * x + 0.38 * y : 0.37 * x + 0.21 * y) + 0.12 * pad;
-      const double col = 0.35 * x + (a.weights ? 0.36 : 0.28) * (a.rows + 0.5 * kTile * p.E);
+      const double col = 0.32 * x + (a.weights ? 0.33 : 0.25) * (a.rows + 0.5 * kTile * p.E);
       const int64_t eighths = std::clamp<int64_t>(std::llround(8 * row / (row + col)), 2, 6);
       row_ctas = std::min(row_ctas, most * eighths / 8);
       col_ctas = std::min(col_ctas, most - row_ctas);
