@@ -15,6 +15,8 @@
 // Products and sums are FP32, each result is rounded once. Sums over a token's choices run in
 // the order of j, sums over columns in an order that depends on the sizes alone.
 
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -712,6 +714,29 @@ cudaError_t launch_combine_grad_v(const RowsArgs& a, cudaStream_t stream) {
     return launcher<__nv_bfloat16, 1>(a, stream);                                         \
   } while (0)
 
+// Leave for the largest launch of route_kernel, asked for once a device. The attributes are the
+// function's, not a launch's: one that followed each launch's own size would take leave away from
+// another host thread's larger launch.
+cudaError_t route_leave() {
+  constexpr int kMost = static_cast<int>(
+      sizeof(uint32_t) * kMaxExperts * kMaxRouteCtas +
+      std::max(sizeof(uint32_t) * kMaxExperts * kRouteWarps,
+               sizeof(uint2) * 32 * kBatch * kRouteWarps));
+  static_assert(kMost + 9 * 1024 <= 227 * 1024, "with the static part, an SM's shared memory");
+  static std::atomic<bool> given[64] = {};  // per device; asking twice is harmless
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && given[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(route_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  if (known) given[dev].store(true, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
@@ -725,17 +750,12 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
   const size_t counters = sizeof(uint32_t) * a.num_experts * kRouteWarps;
   const size_t sorted = p.per_warp <= 32 * kBatch ? sizeof(uint2) * p.per_warp * kRouteWarps : 0;
   const size_t dyn = sizeof(uint32_t) * ((static_cast<size_t>(a.num_experts) * ctas + 3) / 4 * 4) +
-                     (counters > sorted ? counters : sorted);
+                     std::max(counters, sorted);
   // Beyond 8 CTAs, the portable limit: 8192 x 8 entries of 128 experts take 8.5 us on 16 and 12.7
-  // on 8, 16384 x 8 13.0 and 21.5, 1024 x 8 4.8 on 8.
-  if (ctas > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        route_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
-  if (dyn > 32 * 1024) {   // 48 KB without leave, the static part of 8.3 KB among them
-    const cudaError_t e = cudaFuncSetAttribute(
-        route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dyn));
+  // on 8, 16384 x 8 13.0 and 21.5, 1024 x 8 4.8 on 8. 48 KB without leave, the static part of 8.3 KB
+  // among them.
+  if (ctas > 8 || dyn > 32 * 1024) {
+    const cudaError_t e = route_leave();
     if (e != cudaSuccess) return e;
   }
   return launch(route_kernel, dim3(static_cast<unsigned>(ctas)), kRouteThreads, ctas, dyn, stream,
