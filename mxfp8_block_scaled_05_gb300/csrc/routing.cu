@@ -278,6 +278,14 @@ __device__ __forceinline__ uint2 load_once(const uint2* p) { return __ldg(p); }
 __device__ __forceinline__ uint32_t load_once(const uint32_t* p) { return __ldg(p); }
 __device__ __forceinline__ uint16_t load_once(const uint16_t* p) { return __ldg(p); }
 
+// The same of memory that the kernel itself may overwrite (a result in place of what it is made
+// from): an ordinary load, since a non-coherent one need not stay before the store.
+template <bool kMayBeWritten, typename R>
+__device__ __forceinline__ R load_operand(const R* p) {
+  if constexpr (kMayBeWritten) return *p;
+  return load_once(p);
+}
+
 __device__ __forceinline__ void zero(uint4& v) { v = make_uint4(0, 0, 0, 0); }
 __device__ __forceinline__ void zero(uint2& v) { v = make_uint2(0, 0); }
 __device__ __forceinline__ void zero(uint32_t& v) { v = 0; }
@@ -522,7 +530,8 @@ __device__ __forceinline__ float sums_of(float (&x)[N], int lane) {
 // A group of kGroup threads (a warp, or the CTA) takes a token: it reads dout[t] and the token's
 // rows of y, kU rows and kC times kGroup accesses of each at a time, writes w dout[t] to the rows'
 // gradients and sums the products for the weights'. The sums are joined over the lanes, then over
-// the warps in order. Bound by memory: 8192 tokens of 2048 BF16 columns, 8 experts each, 91 us (6.5
+// the warps in order. The rows' gradient may stand in y's place: a thread reads what it overwrites
+// first. Bound by memory: 8192 tokens of 2048 BF16 columns, 8 experts each, 91 us (6.5
 // TB/s); 509 tokens of 1033 FP32 columns, 2 each, 4.7 us (4.2 TB/s, of which 2 are the launch).
 template <typename T, int V, int kGroup, bool kRows, int kU, int kC>
 __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const RowsParams p) {
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const RowsPa
 #pragma unroll
           for (int q = 0; q < kC; ++q)
             if (r[u] >= 0 && c0 + kGroup * q < vecs)
-              v[u][q] = load_once(y + r[u] * vecs + c0 + kGroup * q);
+              v[u][q] = load_operand<kRows>(y + r[u] * vecs + c0 + kGroup * q);
 #pragma unroll
         for (int q = 0; q < kC; ++q) {
           const int64_t c = c0 + kGroup * q;
