@@ -60,6 +60,22 @@ __device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[8]) {
   }
 }
 
+// The same of memory that the kernel itself may overwrite: ordinary loads, since non-coherent ones
+// need not stay before the stores to their addresses.
+template <bool kWide>
+__device__ __forceinline__ void load16_operand(const uint16_t* p, uint32_t (&w)[8]) {
+  if constexpr (kWide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(p) : "memory");
+  } else {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+}
+
 template <bool kWide>
 __device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8]) {
   if constexpr (kWide) {
@@ -174,7 +190,11 @@ __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(const SwigluParam
   const int64_t at = q.row * 2 * p.width + q.c;
   const int64_t block = q.row * (p.width / 16) + q.c / 32;
   uint32_t d[8];
-  load16<kWide>(p.grad + q.row * p.width + q.c, d);
+  if constexpr (kAgain) {   // h may stand in the gradient's place
+    load16_operand<kWide>(p.grad + q.row * p.width + q.c, d);
+  } else {
+    load16<kWide>(p.grad + q.row * p.width + q.c, d);
+  }
   const uint4 gc = ld_nc_v4(p.codes + at), uc = ld_nc_v4(p.codes + at + p.width);
   const float gs = scale_of(p.scales[block]), us = scale_of(p.scales[block + p.width / 32]);
   const uint32_t gw[4] = {gc.x, gc.y, gc.z, gc.w}, uw[4] = {uc.x, uc.y, uc.z, uc.w};

@@ -57,6 +57,33 @@ def test_rows_gradient_in_place(m, tokens, k, dtype, cols):
         assert torch.isfinite(a).all() and torch.equal(a, b)
 
 
+@pytest.mark.parametrize("rows,width,start", [(333, 96, 0), (333, 96, 8), (64, 4128, 0),
+                                              (64, 4128, 8), (2000, 32, 8)])
+def test_activation_in_place_of_its_rows_gradient(m, rows, width, start):
+    """Buffers that start on 32 bytes, and on 16 alone."""
+    g = torch.Generator().manual_seed(width)
+    kept = [m.swiglu(torch.randn(rows, 2 * width, generator=g).to(BF16).to(DEV))
+            for _ in range(2)]
+    dh0 = torch.randn(rows, width, generator=g).to(BF16).to(DEV)
+
+    def buffer():
+        return torch.empty(start + rows * width, dtype=BF16, device=DEV)[start:].view(rows, width)
+
+    def chain(in_place):
+        dh, grads = buffer().copy_(dh0), []
+        for i in range(10):
+            grad, h = m.swiglu_backward(dh, *kept[i % 2][1:], recompute=True,
+                                        out_h=dh if in_place else buffer())
+            grads.append(grad)
+            dh = h     # the next call's gradient
+            if not in_place:
+                torch.cuda.synchronize()
+        return grads + [dh]
+
+    for a, b in zip(chain(True), chain(False)):
+        assert torch.equal(a, b)
+
+
 def test_without_programmatic_launches():
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", __file__, "-k", "rows_gradient"],
                        env=dict(os.environ, MXFP8_PDL="0"), capture_output=True, text=True,

@@ -29,3 +29,14 @@ def test_rows_gradient_in_place_of_the_rows():
     assert not [a for a in reads(kernel, NON_COHERENT) if re.match(r"y\b", a)]
     helper = body("routing.cu", "load_operand")
     assert re.search(r"if constexpr \(kMayBeWritten\) return \*p;", helper)
+
+
+def test_activation_in_place_of_its_gradient():
+    kernel = body("swiglu.cu", "swiglu_grad_kernel")
+    again = re.search(r"if constexpr \(kAgain\) \{(.*?)\} else \{(.*?)\}", kernel, re.S)
+    assert again and reads(again[1], "load16_operand") == ["p.grad + q.row * p.width + q.c"]
+    rest = kernel.replace(again[0], "")   # nor is it read anywhere else
+    assert "p.grad " not in rest and "p.grad," not in rest
+    helper = body("swiglu.cu", "load16_operand")
+    assert not re.search(NON_COHERENT, helper) and ".nc" not in helper
+    assert '"memory"' in helper           # no store moves before it
