@@ -670,7 +670,9 @@ int mxfp8_combine_backward(const void* grad_out_dev, const void* y_dev, int dtyp
  *   codes_dev   E4M3 [rows][2 * width], scales_dev [rows][2 * width / 32]: the bytes of
  *               mxfp8_quantize_rule(x, ROW, LINEAR, scale_rule); both NULL: not kept.
  *               MXFP8_RULE_CEIL saturates nothing: every value of a block is then within 2^-4 of
- *               itself or within 2^-17 of the block's largest.
+ *               itself or within 2^-17 of the block's largest where that is 2^-120 or more (within
+ *               2^-137 where it is less). BF16's largest numbers, from 1.9375 * 2^127, are kept as
+ *               2^128.
  * A gate of -inf gives NaN; sigmoids below 2^-126 are 0.
  * All buffers start on 16 bytes (scales_dev anywhere), and no two overlap. rows == 0 or width == 0
  * is a no-op.
@@ -681,7 +683,8 @@ int mxfp8_swiglu(const void* x_dev, int64_t rows, int64_t width, void* h_dev, vo
 /*
  * Gradient of mxfp8_swiglu from what it kept: with g, u the kept values, s = 1 / (1 + e^-g),
  *   grad_x = [grad_h u s (1 + g (1 - s)) | grad_h g s], and h = g s u again,
- * FP32, each rounded to BF16 once. A block kept with a NaN scale gives NaN.
+ * FP32, each rounded to BF16 once. A kept value of 2^128 or more counts as FP32's largest number. A
+ * block kept with a NaN scale gives NaN.
  *   grad_h_dev  BF16 [rows][width]
  *   grad_x_dev  BF16 [rows][2 * width]; may not overlap the inputs
  *   h_dev       BF16 [rows][width], or NULL: not wanted. May be grad_h itself.
