@@ -181,25 +181,32 @@ __device__ __forceinline__ void e4m3x2_values(uint32_t codes, float& a, float& b
       : "=f"(a), "=f"(b) : "r"(h2));
 }
 
-// dg, du and h of a gate, an up and the gradient of h.
+constexpr float kLargest = 3.402823466e38f;   // of FP32
+
+// dg, du and h of a gate, an up and the gradient of h. kFar: where dh u passes FP32, dg need not, as
+// its factor is small below zero. Then |dh| and |u| are 1 at least, so that u times the factor, which is
+// 2^-126 at least or 0, loses nothing, and passes FP32 only where dg does.
+template <bool kFar>
 __device__ __forceinline__ void value_grads(float g, float u, float dh, float& dg, float& du,
                                             float& h) {
   const float s = sigmoid(g), silu = g * s;
-  dg = dh * u * (s * fmaf(g, 1.f - s, 1.f));
+  const float factor = s * fmaf(g, 1.f - s, 1.f), product = dh * u;
+  const bool passed = kFar && fabsf(product) > kLargest && fabsf(dh) <= kLargest;
+  dg = passed ? u * factor * dh : product * factor;
   du = dh * silu;
   h = silu * u;
 }
 
 // The largest number of FP32 for an infinity; NaN stays.
 __device__ __forceinline__ float at_most_largest(float v) {
-  asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(v) : "f"(3.402823466e38f));
+  asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(v) : "f"(kLargest));
   return v;
 }
 
-// A thread's results where one of them is an infinity or NaN, from its operands again. Kept values past
-// FP32 (the round-up rule keeps BF16 values of 1.9375 x 2^127 and more as 2^128) count as its largest
-// number: as infinities they met factors of 0. Two values at a time: the registers are the kernel's
-// to have (care in its own loop took 80 us in place of 75, with 51 registers in place of 48).
+// A thread's results where one of them is an infinity or NaN, from its operands again, with kFar. Kept
+// values past FP32 (the round-up rule keeps BF16 values of 1.9375 x 2^127 and more as 2^128) count as
+// its largest number: as infinities they met factors of 0. Two values at a time: the registers are the
+// kernel's to have (care in its own loop took 80 us in place of 75, with 51 registers in place of 48).
 template <bool kAgain>
 __device__ __forceinline__ void grads_again(const SwigluParams& p, const Place& q) {
   const int64_t at = q.row * 2 * p.width + q.c, h_at = q.row * p.width + q.c;
@@ -213,8 +220,8 @@ __device__ __forceinline__ void grads_again(const SwigluParams& p, const Place& 
     e4m3x2_values(*reinterpret_cast<const uint16_t*>(p.codes + at + p.width + i), u[0], u[1]);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      value_grads(at_most_largest(g[j] * gs), at_most_largest(u[j] * us), j ? hi(d) : lo(d), a[j],
-                  b[j], c[j]);
+      value_grads<true>(at_most_largest(g[j] * gs), at_most_largest(u[j] * us),
+                        j ? hi(d) : lo(d), a[j], b[j], c[j]);
     *reinterpret_cast<uint32_t*>(p.grad_x + at + i) = cvt_bf16x2(a[1], a[0]);
     *reinterpret_cast<uint32_t*>(p.grad_x + at + p.width + i) = cvt_bf16x2(b[1], b[0]);
     if (kAgain) *reinterpret_cast<uint32_t*>(p.h + h_at + i) = cvt_bf16x2(c[1], c[0]);
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(const SwigluParam
     e4m3x2_values(uw[i / 2] >> (16 * (i & 1)), u[0], u[1]);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      value_grads(g[j] * gs, u[j] * us, j ? hi(d[i]) : lo(d[i]), a[j], b[j], c[j]);
+      value_grads<false>(g[j] * gs, u[j] * us, j ? hi(d[i]) : lo(d[i]), a[j], b[j], c[j]);
     dg[i] = cvt_bf16x2(a[1], a[0]);
     du[i] = cvt_bf16x2(b[1], b[0]);
     top = max_abs_bf16x2(top, max_abs_bf16x2(dg[i], du[i]));

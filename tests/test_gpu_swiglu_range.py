@@ -1,5 +1,5 @@
-"""The gated activation at the ends of its types' ranges: kept values of 2^128, and blocks near the
-least scale.
+"""The gated activation at the ends of its types' ranges: kept values of 2^128, gradients whose
+products pass FP32 on the way to a result that does not, and blocks near the least scale.
 Tolerances as in test_gpu_swiglu.py."""
 import numpy as np
 import pytest
@@ -71,6 +71,19 @@ def test_kept_values_past_fp32(m):
     x[:, 32:] = torch.where(torch.arange(32) % 2 == 0, top, -top)
     kept = check_backward(m, x.to(BF16), dh)
     assert (np.abs(kept[:, 32:]) == 2.0 ** 128).all()
+
+
+@pytest.mark.parametrize("up,grad", [(2.0 ** 100, 2.0 ** 40), (2.0 ** 40, -2.0 ** 100),
+                                     (-1.5 * 2.0 ** 126, 1.75 * 2.0 ** 70),
+                                     (2.0 ** 127, 2.0 ** 3), (2.0 ** 90, 2.0 ** 30)])
+def test_gradient_of_large_products(m, up, grad):
+    """dh u past FP32's range, times the small factor of a gate far below zero."""
+    gates = torch.tensor([-300.0, -100, -88, -80, -72, -64, -56, -48, -40, -30, -5, 4])
+    x = torch.zeros(gates.numel(), 64)
+    x[:, :32] = gates[:, None]
+    x[:, 32:] = up
+    dh = torch.full((gates.numel(), 32), grad).to(BF16)
+    check_backward(m, x.to(BF16), dh)
 
 
 @pytest.mark.parametrize("peak", [-126, -123, -121, -120, -119, -110, 0, 120])
