@@ -701,9 +701,14 @@ class RoutePlan(NamedTuple):
     entry_of: torch.Tensor  # [rows], the entry (token * top_k + choice) of each row; -1: padding
 
 
+_MOST_ROUTED, _MOST_EXPERTS = 0x7FFFFF00, 1024   # mxfp8_route's limits
+
+
 def route_rows(tokens: int, top_k: int, num_experts: int) -> int:
     """Rows that the segments of any choice of experts fit in."""
-    rows = int(lib().mxfp8_route_rows(tokens, top_k, num_experts))
+    rows = 0
+    if 0 < tokens <= _MOST_ROUTED >= top_k > 0 < num_experts <= _MOST_EXPERTS:   # C's types hold them
+        rows = int(lib().mxfp8_route_rows(tokens, top_k, num_experts))
     if rows == 0 and tokens != 0:
         raise ValueError(f"no segments for tokens={tokens} top_k={top_k} "
                          f"num_experts={num_experts}")
@@ -719,16 +724,20 @@ def route(ids: torch.Tensor, num_experts: int, rows: Optional[int] = None,
     if ids.dim() != 2 or ids.shape[1] < 1:
         raise ValueError(f"ids must be [tokens, top_k], got {tuple(ids.shape)}")
     tokens, top_k = ids.shape
+    if top_k > _MOST_ROUTED or not 0 < num_experts <= _MOST_EXPERTS:
+        if rows is None:
+            route_rows(tokens, top_k, num_experts)
+        _check(ERR_INVALID_ARG, "mxfp8_route")
     n = tokens * top_k
     if rows is None:
-        if 0 < num_experts <= 1024 and n < 1 << 30:
+        if n < 1 << 30:
             rows = (n + 31 * min(n, num_experts)) // 32 * 32   # route_rows
         else:
             rows = route_rows(tokens, top_k, num_experts)
     elif rows < 0:
         raise ValueError(f"rows must not be negative, got {rows}")
     dev = ids.device
-    offsets = _new((max(num_experts, 0) + 1,), torch.int32, dev, stream)
+    offsets = _new((num_experts + 1,), torch.int32, dev, stream)
     row_of = _new((tokens, top_k), torch.int32, dev, stream)
     entry_of = _new((rows,), torch.int32, dev, stream)
     _check(lib().mxfp8_route(_ptr(ids), tokens, top_k, num_experts, rows, _ptr(offsets),
@@ -750,8 +759,9 @@ def _plan_refused(t, plan: RoutePlan, weights, name: str):
         raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
     _require(plan.row_of, _INT32, "plan.row_of")
     _require(plan.entry_of, _INT32, "plan.entry_of")
-    if plan.row_of.dim() != 2 or plan.row_of.shape[1] < 1:
-        raise ValueError(f"plan.row_of must be [tokens, top_k], got {tuple(plan.row_of.shape)}")
+    if plan.row_of.dim() != 2 or not 0 < plan.row_of.shape[1] <= _MOST_ROUTED:
+        raise ValueError(f"plan.row_of must be [tokens, top_k], top_k 1 to {_MOST_ROUTED}, got "
+                         f"{tuple(plan.row_of.shape)}")
     _require(weights, _FP32, "weights")
     raise ValueError(f"weights are {tuple(weights.shape)}; the plan is of "
                      f"{tuple(plan.row_of.shape)}")
@@ -766,7 +776,7 @@ def _planned(t, plan: RoutePlan, weights, name: str):
     if not ((dt is _BF16 or dt is _FP32) and row_of.dtype is _INT32 is entry_of.dtype
             and dev >= 0 and dev == _device() == row_of.get_device() == entry_of.get_device()
             and t.is_contiguous() and row_of.is_contiguous() and entry_of.is_contiguous()
-            and len(of) == 2 and of[1] > 0 and t.dim() == 2) or (
+            and len(of) == 2 and 0 < of[1] <= _MOST_ROUTED and t.dim() == 2) or (
             weights is not None and not (
                 weights.dtype is _FP32 and weights.get_device() == dev
                 and weights.is_contiguous() and weights.shape == of)):
@@ -953,6 +963,8 @@ def swiglu(gate_up: torch.Tensor, checkpoint: bool = True, rule: int = RULE_CEIL
     elif codes is not None or scales is not None:
         raise ValueError("codes or scales are given, but checkpoint is False")
     if rows and width:
+        if rule not in (RULE_FLOOR, RULE_CEIL):
+            _check(ERR_INVALID_ARG, "mxfp8_swiglu")
         _check(lib().mxfp8_swiglu(_ptr(gate_up), rows, width, _ptr(out), _optional(codes),
                                   _optional(scales), rule, _here(stream)), "mxfp8_swiglu")
     return Swiglu(out, codes, scales)
