@@ -715,6 +715,11 @@ def route_rows(tokens: int, top_k: int, num_experts: int) -> int:
     return rows
 
 
+def _plan_rows(n, experts):
+    """mxfp8_route_rows of n entries, fewer than 2^30, without the call."""
+    return (n + 31 * min(n, experts)) // 32 * 32
+
+
 def route(ids: torch.Tensor, num_experts: int, rows: Optional[int] = None,
           stream=None) -> RoutePlan:
     """Sorts the entries of ids (int64 [tokens, top_k], negative: of no expert) by expert, each
@@ -731,7 +736,7 @@ def route(ids: torch.Tensor, num_experts: int, rows: Optional[int] = None,
     n = tokens * top_k
     if rows is None:
         if n < 1 << 30:
-            rows = (n + 31 * min(n, num_experts)) // 32 * 32   # route_rows
+            rows = _plan_rows(n, num_experts)
         else:
             rows = route_rows(tokens, top_k, num_experts)
     elif rows < 0:
@@ -807,12 +812,16 @@ def dispatch(x: torch.Tensor, plan: RoutePlan, weights: Optional[torch.Tensor] =
     return out
 
 
+def _copy_scale_bytes(rows, cols, experts, axis):
+    """mxfp8_grouped_scale_bytes, without the call for the usual sizes."""
+    if experts > 0 and rows % 32 == 0 == cols % 32:
+        return (-(-rows // 128) + experts) * -(-cols // 128) * 512
+    return lib().mxfp8_grouped_scale_bytes(rows, cols, experts, axis)
+
+
 def _dispatch_copy(rows, cols, experts, axis, codes, scales, device, stream):
     """Codes and scales of one grouped copy: given ones checked, absent ones allocated."""
-    if experts > 0 and rows % 32 == 0 == cols % 32:   # grouped_scale_bytes
-        need = (-(-rows // 128) + experts) * -(-cols // 128) * 512
-    else:
-        need = lib().mxfp8_grouped_scale_bytes(rows, cols, experts, axis)
+    need = _copy_scale_bytes(rows, cols, experts, axis)
     if need == 0 and cols:   # cols not a multiple of 32, or sizes that do not fit: as the call says
         _check(ERR_ALIGNMENT if axis == ROW and cols % 32 else ERR_INVALID_ARG,
                "mxfp8_quantize_dispatch")

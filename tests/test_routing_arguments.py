@@ -1,4 +1,7 @@
-"""Arguments of the routing calls and of the activation that the C interface's types do not hold."""
+"""Arguments of the routing calls and of the activation that the C interface's types do not hold, and
+the sizes that the binding works out by itself."""
+import random
+
 import pytest
 import torch
 
@@ -43,3 +46,28 @@ def test_calls_refuse_what_does_not_fit():
         with pytest.raises(m.MXFP8Error):
             m.swiglu(x, rule=rule)
     assert m.device_status() == m.OK
+
+
+def sizes(n):
+    g = random.Random(0)
+    for _ in range(n):
+        yield int(2 ** g.uniform(0, 22)), g.randint(1, 64), g.randint(1, 1024)
+
+
+def test_rows_of_a_plan_are_the_librarys(lib):
+    for tokens, top_k, experts in sizes(3000):
+        want = lib.mxfp8_route_rows(tokens, top_k, experts)
+        assert want and m._plan_rows(tokens * top_k, experts) == want
+        assert m.route_rows(tokens, top_k, experts) == want
+    assert m._plan_rows(0, 7) == m.route_rows(0, 3, 7) == lib.mxfp8_route_rows(0, 3, 7) == 0
+
+
+def test_scales_of_a_copy_are_the_librarys(lib):
+    for rows, k, experts in sizes(3000):
+        for axis in (m.ROW, m.COL):
+            want = lib.mxfp8_grouped_scale_bytes(32 * rows, 32 * k, experts, axis)
+            assert want and m._copy_scale_bytes(32 * rows, 32 * k, experts, axis) == want
+    # widths that only the column copy takes
+    for rows, cols, experts in ((32, 8, 1), (96, 40, 3), (1024, 2056, 128)):
+        assert m._copy_scale_bytes(rows, cols, experts, m.COL) == \
+            lib.mxfp8_grouped_scale_bytes(rows, cols, experts, m.COL)
