@@ -37,9 +37,10 @@ def quantize_experts(gate_up, down):
                    m.quantize_batched(down, m.ROW), m.quantize_batched(down, m.COL))
 
 
-def forward(x, router, experts, top):
+def forward(x, router, experts, top, intermediates=True):
     """x: BF16 [tokens, hidden], router: float32 [experts, hidden]. Returns the result (BF16
-    [tokens, hidden]) and what the backward pass reads."""
+    [tokens, hidden]) and what the backward pass reads; with intermediates, for a look at each step,
+    also the activation's input and result in BF16, which it does not read."""
     logits = x.float() @ router.t()
     none = torch.full((x.shape[0],), -1, device=x.device)
     chosen = m.token_logprobs(logits, none, top=top)
@@ -51,8 +52,11 @@ def forward(x, router, experts, top):
     y = m.grouped_gemm(*m.quantize_grouped(act.h, plan.offsets, m.ROW), *experts.down,
                        plan.offsets, m.FPROP)
     out = m.combine(y, plan, weights)
-    return out, dict(logits=logits, chosen=chosen, weights=weights, plan=plan, x_col=(xc, xcs),
-                     codes=act.codes, scales=act.scales, y=y, gate_up=gate_up, h=act.h)
+    kept = dict(logits=logits, chosen=chosen, weights=weights, plan=plan, x_col=(xc, xcs),
+                codes=act.codes, scales=act.scales, y=y)
+    if intermediates:
+        kept.update(gate_up=gate_up, h=act.h)
+    return out, kept
 
 
 def backward(grad_out, x, router, experts, kept):
@@ -96,12 +100,12 @@ def main():
     router = rand(a.experts, a.hidden) * 0.02
     experts = quantize_experts((rand(a.experts, 2 * a.width, a.hidden) * 0.02).to(torch.bfloat16),
                                (rand(a.experts, a.hidden, a.width) * 0.02).to(torch.bfloat16))
-    out, kept = forward(x, router, experts, a.top)
+    out, kept = forward(x, router, experts, a.top, intermediates=False)
     grads = backward(rand(a.tokens, a.hidden).to(torch.bfloat16), x, router, experts, kept)
     status = m.device_status()
     if status != m.OK:
         raise m.MXFP8Error(status, "expert layer")
-    rows, width = kept["h"].shape
+    rows, width = kept["codes"].shape[0], kept["codes"].shape[1] // 2
     print(f"tokens {a.tokens}, hidden {a.hidden}, {a.top} of {a.experts} experts of {a.width}; "
           f"{rows} segment rows")
     print(f"kept for the activation's gradient: {(kept['codes'].numel() + kept['scales'].numel()) / 2**20:.1f} MiB "
