@@ -653,7 +653,8 @@ int mxfp8_combine(const void* y_dev, int dtype, int64_t total_rows, int64_t cols
  *   grad_y_dev        [total_rows][cols], of y's type, written in full, or NULL where only the
  *                     weights' gradient is wanted (entry_of_dev may then be NULL): the rows'
  *                     gradient also comes from mxfp8_quantize_dispatch(grad_out, weights), on the
- *                     MXFP8 grid. May be y itself, else the two may not overlap.
+ *                     MXFP8 grid. May be y itself, else the two may not overlap. It may not
+ *                     overlap grad_out.
  *   grad_weights_dev  float [tokens][top_k]
  */
 int mxfp8_combine_backward(const void* grad_out_dev, const void* y_dev, int dtype,

@@ -14,7 +14,8 @@
 // so, side by side or in turn. CTAs are persistent and derive the segments from the offsets once.
 //
 // 8192 tokens of 2048 columns, 8 of 128 experts each (69504 rows): row copy 32 us, column copy 45,
-// both 75 (with weights 56, 60 and 111). What bounds them: the row copy the rate at which an SM
+// both 75 (with weights 56, 60 and 111; that instance spills 80 bytes at its 64 registers, which
+// the row and the column copy share). What bounds them: the row copy the rate at which an SM
 // sends bulk copies away (22 bytes a clock) and the scattered scale words (6 us); the column copy
 // 268 MB read from L2 (27 us of it), the ALU pipe and the L1 path, each busy half of the time, and
 // two barriers a tile. What counted most: results leave by lines that L2 evicts first, so that the
@@ -132,7 +133,7 @@ __device__ __forceinline__ uint4 convert_piece(const uint32_t (&w)[8], uint32_t 
 // code other than 0 comes from leaves the normal numbers. Codes of 2^-10 and more of the scale are
 // normal BF16 products from scale byte 11 on, and the scaled weight is about 2^8 / amax, finite
 // where amax has an exponent field of 10 or more. Found anew for each weight, maximum and scale
-// included, 69504 x 2048 took 58 us in place of 54.
+// included, the row copy takes 7% longer.
 __device__ __forceinline__ uint4 weigh_piece(const uint32_t (&x)[8], uint32_t amax, float w,
                                              uint32_t& s) {
   const uint32_t top = cvt_bf16x2(0.f, __fmul_rn(__uint_as_float(amax << 16), fabsf(w)));
@@ -647,11 +648,15 @@ cudaError_t launch_quantize_dispatch(const QuantizeDispatchArgs& a, cudaStream_t
   // values, fitted to each alone (a token converts once, with weights once an expert, and goes out
   // once an expert; a segment's last tile costs as much as a full one). Shares go by eighths, so
   // that the SMs hold like mixtures: a share of 28% in place of 25 or 37 costs up to 7%. Where
-  // there is much, the copies go in turn, as the tokens' rows leave L2 sooner with both at work.
-  // Times, us, side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 12,
-  // 18; 4096 x 8 x 2048: 43, 48; 8192 x 8 x 2048: 75, 81; 16384 x 8 x 2048: 157, 156; 16384 x 8 x
-  // 7168: 702, 566; 16384 x 2 x 4096: 96, 102; 16384 x 1 x 2048: 40, 45; with weights 4096 x 8 x
-  // 2048: 64, 66; 8192 x 8 x 2048: 111, 115; 16384 x 4 x 4096: 217, 213.
+  // there is much to do, the copies go in turn: the second launch counts for little there, and each
+  // copy has L2 to itself. The rule goes by the values to be written; the size of the tokens' rows,
+  // which is what L2 holds, does not tell the better way either (1024 tokens of 64 experts). Times, us,
+  // side by side and in turn (tokens x experts of each x columns): 37 x 8 x 2048: 12, 18; 4096 x 8 x
+  // 2048: 44, 48; 8192 x 8 x 2048: 76, 82; 16384 x 2 x 7168: 197, 196; 16384 x 1 x 8192: 149, 155;
+  // 16384 x 8 x 2048: 157, 156; 16384 x 4 x 4096: 166, 171; 16384 x 1 x 16352: 326, 330; 1024 x 64 x
+  // 4096: 132, 144; 1024 x 64 x 8192: 303, 290; 32768 x 1 x 8192: 304, 294; 16384 x 8 x 7168: 740, 607.
+  // With weights 4096 x 8 x 2048: 64, 66; 8192 x 8 x 2048: 112, 116; 16384 x 1 x 8192: 205, 196; 16384
+  // x 4 x 4096: 233, 229. Over 48 such sizes the rule's way is the slower one by 9% at most.
   if (a.row_out && a.col_out) {
     if (p.entries * a.cols < int64_t{1} << 28) {
       const double x = static_cast<double>(a.tokens);

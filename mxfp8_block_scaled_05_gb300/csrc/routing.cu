@@ -445,8 +445,9 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowsParams p) 
 // ------------------------------------------------------------------------------- combine
 
 // A warp sums a piece (kC times 32 lanes x V columns) of a token's k rows, kU of them at a time:
-// enough of both that a lane has 128 bytes on their way. Bound by the reads: 8192 tokens of 2048
-// BF16 columns, 8 experts each, 46 us (6.5 TB/s); with 1999 columns, 2-byte accesses, 67 (4.4).
+// enough of both that a lane has 128 bytes on their way (64 in accesses of 2 bytes, 256 in those of 8).
+// Bound by the reads: 8192 tokens of 2048 BF16 columns, 8 experts each, 46 us (6.5 TB/s); with 1999
+// columns, 2-byte accesses, 67 (4.4).
 template <typename T, int V, bool kWeighted, int kU, int kC>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const RowsParams p) {
   using raw = typename Pack<T, V>::raw;
@@ -531,8 +532,9 @@ __device__ __forceinline__ float sums_of(float (&x)[N], int lane) {
 // rows of y, kU rows and kC times kGroup accesses of each at a time, writes w dout[t] to the rows'
 // gradients and sums the products for the weights'. The sums are joined over the lanes, then over
 // the warps in order. The rows' gradient may stand in y's place: a thread reads what it overwrites
-// first. Bound by memory: 8192 tokens of 2048 BF16 columns, 8 experts each, 91 us (6.5
-// TB/s); 509 tokens of 1033 FP32 columns, 2 each, 4.7 us (4.2 TB/s, of which 2 are the launch).
+// first. Bound by memory: 8192 tokens of 2048 BF16 columns, 8 experts each, 91 us (6.5 TB/s), in y's
+// place 92, without the rows' gradient 44 (6.8); 509 tokens of 1033 FP32 columns, 4 each, a tenth of them
+// dropped, 4.8 us (4.2 TB/s, of which 2 are the launch).
 template <typename T, int V, int kGroup, bool kRows, int kU, int kC>
 __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const RowsParams p) {
   using raw = typename Pack<T, V>::raw;

@@ -11,7 +11,7 @@
 //   dg = dh u' s' (1 + g' (1 - s')),   du = dh g' s',   h' = g' s' u'
 // in FP32, each rounded to BF16 once. e^-g is one ex2.approx (2^-22 relative) of g log2(e) in FP32,
 // whose own rounding adds up to |g| 2^-24: 2^-17 at the far end of the range, where BF16 keeps
-// 2^-9. Beyond it (g < -88) s is 0. A gate of -inf gives NaN (-inf * 0).
+// 2^-9. Beyond it (s below 2^-126, g below -87.33) s is 0. A gate of -inf gives NaN (-inf * 0).
 //
 // Bound by memory: forward 4 bytes read and 2 + 2.0625 written for each value of h, backward
 // 2 + 2.0625 read and 4 (with h' 6) written: 4096 x 12288 values of h take 59 us forward (6.9 TB/s),
@@ -207,6 +207,7 @@ __device__ __forceinline__ float at_most_largest(float v) {
 // values past FP32 (the round-up rule keeps BF16 values of 1.9375 x 2^127 and more as 2^128) count as
 // its largest number: as infinities they met factors of 0. Two values at a time: the registers are the
 // kernel's to have (care in its own loop took 80 us in place of 75, with 51 registers in place of 48).
+// Every thread comes here where every gradient is NaN: 296 us.
 template <bool kAgain>
 __device__ __forceinline__ void grads_again(const SwigluParams& p, const Place& q) {
   const int64_t at = q.row * 2 * p.width + q.c, h_at = q.row * p.width + q.c;
