@@ -84,6 +84,30 @@ def test_activation_in_place_of_its_rows_gradient(m, rows, width, start):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("start", [0, 8])
+def test_activation_in_place_of_rows_gradient_past_range(m, start):
+    """Threads that make their results again, beside those that do not: infinities, NaN and products
+    past FP32 among the values."""
+    rows, width = 257, 96
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(rows, 2 * width, generator=g)
+    x[::7, 3], x[::11, 40], x[::13, width + 70] = 3.39e38, -3.39e38, 3.39e38
+    x[5, 1], x[6, width + 1], x[8, 2] = float("nan"), float("inf"), -80
+    dh0 = torch.randn(rows, width, generator=g)
+    dh0[::5, ::9], dh0[9, 9], dh0[10, 10] = 2.0 ** 100, float("nan"), -float("inf")
+    dh0 = dh0.to(BF16).to(DEV)
+    kept = m.swiglu(x.to(BF16).to(DEV))[1:]
+    want, want_h = m.swiglu_backward(dh0, *kept, recompute=True)
+    assert not torch.isfinite(want).all() and not torch.isfinite(want_h).all()
+    dh = torch.empty(start + rows * width, dtype=BF16, device=DEV)[start:].view(rows, width)
+    dh.copy_(dh0)
+    got, h = m.swiglu_backward(dh, *kept, recompute=True, out_h=dh)
+    bits = lambda t: t.view(torch.int16)  # noqa: E731
+    assert h is dh and torch.equal(bits(got), bits(want)) and torch.equal(bits(h), bits(want_h))
+    alone, none = m.swiglu_backward(dh0, *kept)
+    assert none is None and torch.equal(bits(alone), bits(want))
+
+
 def test_without_programmatic_launches():
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", __file__, "-k", "rows_gradient"],
                        env=dict(os.environ, MXFP8_PDL="0"), capture_output=True, text=True,
